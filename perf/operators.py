@@ -1,0 +1,421 @@
+"""The cache operators' cases: what each one computes in plain torch, and the calls a user makes of the package.
+
+Four operators around the paged KV cache of single-token GQA decode (16-token pages, G = q_heads / kv_heads
+query heads per KV head):
+
+  scored      decode that also adds every cached token's attention weight (summed over the query heads that
+              share its KV head) to the fp32 scores an eviction goes by;
+  evict       in-place eviction: per (row, KV head) the `recent` newest tokens and the best-scored others stay,
+              `budget` in all;
+  mx4_write   new bf16 tokens quantised into a 4-bit microscaled cache (e2m1 values, one power-of-two scale per 32
+              dims), and the stored values read back, as a prompt's attention takes them;
+  mx4_decode  decode over that cache, with or without the scores.
+
+Rows' lengths run evenly from `shortest` to `longest`; every row's pages lie scattered over the pool.
+"""
+import math
+
+import torch
+
+own = False
+
+PAGE = 16
+
+
+# ---------------------------------------------------------------------------
+# cases
+
+def listed():
+    return [
+        # one short request, a small model: the call's latency
+        dict(name="scored_tiny", op="scored", batch=1, shortest=512, longest=512, q_heads=4, kv_heads=1, head_dim=64),
+        # an ordinary serving batch of ragged rows
+        dict(name="scored_mixed", op="scored", batch=8, shortest=533, longest=16381, q_heads=32, kv_heads=8,
+             head_dim=128),
+        # one long context
+        dict(name="scored_long", op="scored", batch=1, shortest=32768, longest=32768, q_heads=32, kv_heads=8,
+             head_dim=128),
+        # a decode loop's upkeep: every row one page over its budget
+        dict(name="evict_step", op="evict", batch=8, shortest=2064, longest=2064, kv_heads=8, head_dim=128,
+             budget=2048, recent=128, cache="bf16"),
+        # after long prompts: most of the cache goes
+        dict(name="evict_prompt", op="evict", batch=4, shortest=16384, longest=32768, kv_heads=8, head_dim=128,
+             budget=8192, recent=256, cache="bf16"),
+        # a ragged batch over the 4-bit cache, some rows within the budget
+        dict(name="evict_mx4", op="evict", batch=16, shortest=1001, longest=9001, kv_heads=8, head_dim=128,
+             budget=2048, recent=64, cache="mx4"),
+        # one new token for every row of a decode batch
+        dict(name="mx4_write_step", op="mx4_write", batch=64, shortest=1, longest=1, kv_heads=8, head_dim=128, start=777),
+        # the prompts of a prefill batch
+        dict(name="mx4_write_prompt", op="mx4_write", batch=5, shortest=1001, longest=8192, kv_heads=8, head_dim=128,
+             start=0),
+        # one short request over the 4-bit cache
+        dict(name="mx4_decode_tiny", op="mx4_decode", batch=1, shortest=501, longest=501, q_heads=4, kv_heads=1,
+             head_dim=64, scores=False),
+        # an ordinary serving batch of ragged rows, 4 bits
+        dict(name="mx4_decode_mixed", op="mx4_decode", batch=8, shortest=533, longest=16381, q_heads=32, kv_heads=8,
+             head_dim=128, scores=False),
+        # one long context, 4 bits
+        dict(name="mx4_decode_long", op="mx4_decode", batch=1, shortest=32768, longest=32768, q_heads=32, kv_heads=8,
+             head_dim=128, scores=False),
+        # a large batch of a model with eight query heads per KV head, keeping scores
+        dict(name="mx4_decode_scored", op="mx4_decode", batch=32, shortest=257, longest=8191, q_heads=64, kv_heads=8,
+             head_dim=128, scores=True),
+    ]
+
+
+def _spread(rng, lo, hi):
+    """A whole number from lo to hi, evenly over its logarithm."""
+    return min(hi, max(lo, int(math.exp(rng.uniform(math.log(lo), math.log(hi + 1))))))
+
+
+def draw(rng):
+    op = rng.choice(["scored", "evict", "mx4_write", "mx4_decode"])
+    kv_heads = rng.choice([1, 2, 4, 8])
+    head_dim = rng.choice([64, 128, 128])
+    batch = _spread(rng, 1, 64)
+    case = dict(op=op, batch=batch, kv_heads=kv_heads, head_dim=head_dim)
+    if op == "mx4_write":
+        longest = _spread(rng, 1, 22000 // batch)
+        case.update(shortest=rng.randint(0, longest), longest=longest, start=rng.randint(0, 2000))
+        return case
+    # no more cached tokens in all, and no more products, than the operator's largest listed case has
+    q_heads = kv_heads * rng.choice([1, 2, 4, 7, 8, 16])
+    most = 65536 * 4096 // max(4096, q_heads * head_dim) if op == "scored" else 40000 if op == "evict" else 65536
+    longest = _spread(rng, 1, min(32768, most // batch))
+    case.update(shortest=rng.randint(0, longest), longest=longest)
+    if op == "evict":
+        budget = rng.randint(1, longest)
+        case.update(budget=budget, recent=rng.randint(0, budget), cache=rng.choice(["bf16", "mx4"]))
+        return case
+    case.update(q_heads=q_heads)
+    if op == "mx4_decode":
+        case.update(scores=rng.random() < 0.5)
+    return case
+
+
+def _lens(case):
+    b, lo, hi = case["batch"], case["shortest"], case["longest"]
+    return [hi] if b == 1 else [lo + (hi - lo) * i // (b - 1) for i in range(b)]
+
+
+def work(case):
+    H, D = case["kv_heads"], case["head_dim"]
+    lens = _lens(case)
+    n = sum(lens)
+    row = 4 * D if case["op"] == "scored" or case.get("cache") == "bf16" else 17 * D // 16  # K and V of a token
+    if case["op"] == "evict":
+        total = 0.0
+        for x in lens:
+            if x > case["budget"]:
+                a, m = case["budget"] - case["recent"], x - case["recent"]
+                moved = case["recent"] + a * (m - a) / m  # holes among the kept slots, for scores in no order
+                total += 4 * x + moved * (2 * row + 16) + 4 * (x - case["budget"])
+        return {"bytes": H * total + 8 * len(lens), "flops": 0}
+    if case["op"] == "mx4_write":  # bf16 in, codes and scales out, and both ways once more for the reading
+        return {"bytes": n * H * 2 * (4 * D + 17 * D // 16), "flops": 0}
+    Hq = case["q_heads"]
+    scores = 8 * n * H if case["op"] == "scored" or case["scores"] else 0
+    return {"bytes": n * H * row + 4 * case["batch"] * Hq * D + scores, "flops": 4 * n * Hq * D}
+
+
+# ---------------------------------------------------------------------------
+# the 4-bit cache's layout: a page of one KV head is one record of 17 D bytes,
+#   K codes [16][D/2], V codes [16][D/2], K scales [16][D/32], V scales [16][D/32]
+# dim 32 b + 8 c + j of a K row lies in byte c D/8 + 4 b + j/2, dim 32 b + 4 r + j of a V row in byte
+# r D/16 + 2 b + j/2 (low four bits where j is even); a value is (-1)^s {0, .5, 1, 1.5, 2, 3, 4, 6}[low three bits]
+# times 2^(scale - 127), NaN where the scale is 255
+
+def _quantise(x):
+    """fp32 [..., D] -> codes (int32 0..15) [..., D], scales (int32 0..255) [..., D/32]."""
+    blocks = x.float().unflatten(-1, (-1, 32))
+    amax = blocks.abs().amax(-1)
+    bad = ~torch.isfinite(blocks).all(-1)
+    amax = torch.where(bad, 0.0, amax)
+    scale = ((amax.view(torch.int32) >> 23) - 2).clamp(1, 254)
+    scale = torch.where(amax == 0, 0, scale)
+    y = torch.ldexp(blocks, (127 - scale)[..., None])
+    a = y.abs()
+    mag = ((a > 0.25).int() + (a >= 0.75).int() + (a > 1.25).int() + (a >= 1.75).int() + (a > 2.5).int()
+           + (a >= 3.5).int() + (a > 5.0).int())
+    code = mag | (torch.signbit(y).int() << 3)
+    code = torch.where(bad[..., None], 0, code)
+    return code.flatten(-2), torch.where(bad, 255, scale)
+
+
+def _values(code, scale):
+    """fp32 values of codes [..., D] under scales [..., D/32]."""
+    grid = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6], device=code.device)
+    s = torch.ldexp(torch.ones((), device=code.device), (scale - 127).float())
+    s = torch.where(scale == 255, float("nan"), s)
+    return (grid[code.long()].unflatten(-1, (-1, 32)) * s[..., None]).flatten(-2)
+
+
+def _pack(code, value):
+    """Codes [..., D] as the bytes [..., D/2] of K rows, or (value) of V rows."""
+    d = code.shape[-1]
+    pair = code[..., 0::2] | (code[..., 1::2] << 4)  # [..., D/2]: byte b, c, j/2 of dims 32 b + ...
+    pair = pair.unflatten(-1, (d // 32, 8, 2) if value else (d // 32, 4, 4))
+    return pair.transpose(-3, -2).flatten(-3).to(torch.uint8)
+
+
+def _unpack(byte, value):
+    d = 2 * byte.shape[-1]
+    pair = byte.int().unflatten(-1, (8, d // 32, 2) if value else (4, d // 32, 4)).transpose(-3, -2).flatten(-3)
+    return torch.stack((pair & 15, pair >> 4), -1).flatten(-2)
+
+
+def _planes(pool, d):
+    """The record's four parts as views [pages][H][16][...] of the pool."""
+    at, parts = 0, []
+    for n in (d // 2, d // 2, d // 32, d // 32):
+        parts.append(pool[:, :, at:at + PAGE * n].unflatten(-1, (PAGE, n)))
+        at += PAGE * n
+    return parts
+
+
+def _make_mx4(k, v):
+    """The 4-bit pool [pages][H][17 D] of bf16 pages [pages][H][16][D]."""
+    (kc, ks), (vc, vs) = _quantise(k), _quantise(v)
+    parts = (_pack(kc, False), _pack(vc, True), ks.to(torch.uint8), vs.to(torch.uint8))
+    return torch.cat([p.flatten(2) for p in parts], 2)
+
+
+# ---------------------------------------------------------------------------
+# inputs
+
+def prepare(case, seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda", dtype=torch.float32).to(torch.bfloat16)
+
+    op, B, H, D = case["op"], case["batch"], case["kv_heads"], case["head_dim"]
+    lens = _lens(case)
+    start = case.get("start", 0)
+    held = [n + start for n in lens]
+    max_pages = max(1, -(-max(held) // PAGE))
+    pages = B * max_pages
+    s = dict(case)
+    s["table"] = torch.randperm(pages, generator=g, device="cuda").to(torch.int32).view(B, max_pages).contiguous()
+    s["lens_host"] = lens
+    s["lens"] = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    if op == "mx4_write":
+        s["pool"] = torch.zeros(pages, H, 17 * D, dtype=torch.uint8, device="cuda")
+        s["k"], s["v"] = normal(sum(lens), H, D), normal(sum(lens), H, D)
+        s["start"] = torch.full((B,), start, dtype=torch.int32, device="cuda")
+        s["indptr"] = torch.tensor([sum(lens[:i]) for i in range(B + 1)], dtype=torch.int32, device="cuda")
+    else:
+        k, v = normal(pages, H, PAGE, D), normal(pages, H, PAGE, D)
+        if op == "mx4_decode" or case.get("cache") == "mx4":
+            s["pool"] = torch.cat([_make_mx4(a, b) for a, b in zip(k.split(4096), v.split(4096))])
+        else:
+            s["k"], s["v"] = k, v
+    if op in ("scored", "mx4_decode"):
+        s["q"] = normal(B, case["q_heads"], D)
+        s["scale"] = D ** -0.5
+    if op == "evict" or op == "scored" or case.get("scores"):
+        # what earlier steps added up; slots past a row's end hold none yet
+        x = torch.empty(B, H, max_pages * PAGE, device="cuda").exponential_(1.0, generator=g)
+        s["scores"] = x * (torch.arange(max_pages * PAGE, device="cuda") < s["lens"][:, None, None])
+    if op == "evict":
+        s["positions"] = torch.arange(max_pages * PAGE, dtype=torch.int32, device="cuda").expand(B, H, -1).contiguous()
+    if own:
+        from paged_kv_gqa_17_b200 import binding as pkv
+
+        if op == "scored":
+            s["plan"] = pkv.plan_decode(lens, pkv.shape_of(s["q"], s["k"], s["table"]), "cuda", scores=True)
+        elif op == "evict":
+            s["plan"] = pkv.plan_evict(B, H, max_pages, "cuda")
+        elif op == "mx4_decode":
+            shape = pkv.mx4_shape(s["pool"], s["table"], q_heads=case["q_heads"])
+            s["plan"] = pkv.plan_mx4(shape, "cuda", scores=case["scores"])
+        else:
+            s["plan"] = pkv.plan_mx4(pkv.mx4_shape(s["pool"], s["table"]), "cuda")
+    return s
+
+
+# ---------------------------------------------------------------------------
+# one pass
+
+def run(s):
+    return {"scored": _run_scored, "evict": _run_evict, "mx4_write": _run_write, "mx4_decode": _run_mx4}[s["op"]](s)
+
+
+def _run_scored(s):
+    if own:
+        from paged_kv_gqa_17_b200 import binding as pkv
+
+        out = pkv.paged_decode_scored(s["q"], s["k"], s["v"], s["table"], s["lens"], PAGE, s["scale"], s["scores"],
+                                      plan=s["plan"])
+        return out, s["scores"]
+    return _attend(s, _rows(s["k"], s["table"]).float(), _rows(s["v"], s["table"]).float()), s["scores"]
+
+
+def _run_mx4(s):
+    if own:
+        from paged_kv_gqa_17_b200 import binding as pkv
+
+        out = pkv.mx4_decode(s["q"], s["pool"], s["table"], s["lens"], PAGE, s["scale"], plan=s["plan"],
+                             scores=s.get("scores"))
+        return (out, s["scores"]) if s["scores"] is not False else (out,)
+    kc, vc, ks, vs = (_rows(p, s["table"]) for p in _planes(s["pool"], s["head_dim"]))
+    out = _attend(s, _values(_unpack(kc, False), ks.int()), _values(_unpack(vc, True), vs.int()))
+    return (out, s["scores"]) if s["scores"] is not False else (out,)
+
+
+def _rows(pool, table):
+    """[pages][H][16][X] through the block table: [B][H][tokens][X]."""
+    return pool[table.long()].transpose(1, 2).flatten(2, 3)
+
+
+def _attend(s, k, v):
+    """softmax(scale q K^T) V of every row; adds the weights to s["scores"] where there are any."""
+    B, H, T, D = k.shape
+    q = s["q"].float().unflatten(1, (H, -1))  # [B][H][G][D]
+    live = torch.arange(T, device=k.device) < s["lens"][:, None, None, None]  # [B][1][1][T]
+    x = torch.matmul(q, k.transpose(2, 3)) * s["scale"]
+    x = torch.where(live, x, float("-inf"))
+    m = x.amax(-1, keepdim=True)
+    p = torch.where(live, torch.exp(x - torch.where(torch.isfinite(m), m, 0.0)), 0.0)
+    total = p.sum(-1, keepdim=True)
+    w = p / torch.where(total > 0, total, 1.0)
+    v = torch.where(live.transpose(2, 3), v, 0.0)
+    out = torch.matmul(w, v).flatten(1, 2).to(torch.bfloat16)
+    if torch.is_tensor(s.get("scores")):
+        s["scores"] += w.sum(2)
+    return out
+
+
+def _run_evict(s):
+    mx4 = s["cache"] == "mx4"
+    planes = _planes(s["pool"], s["head_dim"]) if mx4 else [s["k"], s["v"]]
+    if own:
+        from paged_kv_gqa_17_b200 import binding as pkv
+
+        if mx4:
+            planes = pkv.mx4_planes(s["pool"])
+        lens = pkv.evict_tokens(s["scores"], planes, s["table"], s["lens"], s["budget"], s["recent"],
+                                positions=s["positions"], plan=s["plan"])
+        return lens, s["scores"], s["positions"], (s["pool"] if mx4 else (s["k"], s["v"]))
+    source, lens = _evicted(s["scores"], s["lens"], s["budget"], s["recent"])
+    slot = torch.arange(source.shape[-1], device="cuda")
+    gone = (slot >= lens[:, None, None]) & (slot < s["lens"][:, None, None])
+    moved = torch.gather(s["scores"], 2, source)
+    s["scores"].copy_(torch.where(gone, 0.0, moved))
+    s["positions"].copy_(torch.gather(s["positions"], 2, source))
+    table = s["table"].long()
+    for plane in planes:
+        rows = _rows(plane, table)
+        rows = torch.gather(rows, 2, source[..., None].expand(-1, -1, -1, rows.shape[-1]))
+        plane[table] = rows.unflatten(2, (-1, PAGE)).transpose(1, 2)
+    return lens, s["scores"], s["positions"], (s["pool"] if mx4 else (s["k"], s["v"]))
+
+
+def _evicted(scores, lens, budget, recent):
+    """Where each slot's token comes from ([B][H][T], its own slot where it stays) and the new lengths."""
+    T = scores.shape[-1]
+    slot = torch.arange(T, device=scores.device)
+    n = lens[:, None, None].long()
+    over = n > budget
+    first = budget - recent           # slots of the kept older tokens
+    older = (slot < n - recent) & over
+    # the best-scored `first` of the older ones, the lowest slot first among equals
+    key = torch.where(older, torch.nan_to_num(scores, nan=float("-inf"), posinf=float("inf"), neginf=float("-inf")),
+                      float("-inf"))
+    order = torch.sort(key, dim=-1, descending=True, stable=True).indices
+    # older slots of the lowest score come before the slots that are none: both hold -inf
+    ranked = torch.gather(older.expand_as(key), 2, order)
+    order = torch.gather(order, 2, torch.sort(ranked.int(), dim=-1, descending=True, stable=True).indices)
+    keep = torch.zeros_like(key, dtype=torch.bool).scatter_(2, order[..., :max(first, 0)], True) & older
+    hole = older & ~keep & (slot < first)
+    mover = keep & (slot >= first)
+    # the j-th hole takes the j-th mover
+    lined = torch.sort(mover.int(), dim=-1, descending=True, stable=True).indices
+    nth = (hole.cumsum(-1) - 1).clamp(min=0)
+    source = torch.where(hole, torch.gather(lined, 2, nth), slot)
+    shifted = over & (slot >= first) & (slot < budget)
+    source = torch.where(shifted, slot + n - budget, source)
+    return source, torch.where(lens > budget, budget, lens).to(torch.int32)
+
+
+def _run_write(s):
+    if own:
+        from paged_kv_gqa_17_b200 import binding as pkv
+
+        pkv.mx4_append(s["k"], s["v"], s["pool"], s["table"], s["start"], plan=s["plan"], indptr=s["indptr"])
+        return pkv.mx4_read(s["pool"], s["table"], s["start"], s["k"].shape[0], plan=s["plan"], indptr=s["indptr"])
+    token = torch.arange(s["k"].shape[0], device="cuda", dtype=torch.int32)
+    row = torch.searchsorted(s["indptr"], token, right=True) - 1
+    at = (s["start"][row] + token - s["indptr"][row]).long()
+    page, slot = s["table"][row, at // PAGE].long(), at % PAGE
+    (kc, ks), (vc, vs) = _quantise(s["k"]), _quantise(s["v"])
+    parts = (_pack(kc, False), _pack(vc, True), ks.to(torch.uint8), vs.to(torch.uint8))
+    planes = _planes(s["pool"], s["head_dim"])
+    for plane, part in zip(planes, parts):
+        plane[page, :, slot] = part
+    kc, vc, ks, vs = (plane[page, :, slot] for plane in planes)
+    return (_values(_unpack(kc, False), ks.int()).to(torch.bfloat16),
+            _values(_unpack(vc, True), vs.int()).to(torch.bfloat16))
+
+
+# ---------------------------------------------------------------------------
+# the same from the definitions, in 64 bits and row by row
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op = case["op"]
+    if op == "mx4_write":
+        return _exact_stored(s["k"]), _exact_stored(s["v"])
+    if op == "evict":
+        return None  # nothing is computed: tokens move
+    H, D = case["kv_heads"], case["head_dim"]
+    out = torch.zeros(case["batch"], case["q_heads"], D, dtype=torch.float64, device="cuda")
+    scores = s["scores"].double() if torch.is_tensor(s.get("scores")) else None
+    for i, n in enumerate(s["lens_host"]):
+        if n == 0:
+            continue
+        pages = s["table"][i, :-(-n // PAGE)].long()
+        for h in range(H):
+            if "pool" in s:
+                k, v = _exact_records(s["pool"][pages, h], D)
+            else:
+                k, v = s["k"][pages, h].double().reshape(-1, D), s["v"][pages, h].double().reshape(-1, D)
+            group = slice(h * case["q_heads"] // H, (h + 1) * case["q_heads"] // H)
+            w = torch.softmax(s["q"][i, group].double() @ k[:n].T * s["scale"], -1)
+            out[i, group] = w @ v[:n]
+            if scores is not None:
+                scores[i, h, :n] += w.sum(0)
+    return (out,) if scores is None else (out, scores)
+
+
+def _exact_records(record, D):
+    """K and V [tokens][D] in 64 bits of one head's records [pages][17 D]."""
+    d = torch.arange(D, device=record.device)
+    b = d // 32
+    byte_k = d % 32 // 8 * (D // 8) + 4 * b + d % 8 // 2
+    byte_v = d % 32 // 4 * (D // 16) + 2 * b + d % 4 // 2
+    grid = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device=record.device)
+    slot = torch.arange(PAGE, device=record.device)[:, None]
+    got = []
+    for base, byte, scales in ((0, byte_k, 16 * D), (8 * D, byte_v, 16 * D + D // 2)):
+        x = record[:, base + slot * (D // 2) + byte].long() >> (4 * (d % 2))
+        e = record[:, scales + slot * (D // 32) + b].double() - 127
+        got.append((torch.where(x & 8 > 0, -1.0, 1.0) * grid[x & 7] * 2.0 ** e).reshape(-1, D))
+    return got
+
+
+def _exact_stored(x):
+    """The 4-bit values nearest to x (ties to the even code) under each 32 dims' scale."""
+    grid = torch.tensor([0, 1, 2, 3, 4, 6, 8, 12], dtype=torch.float64, device=x.device) / 2
+    y = x.double().reshape(-1, 32)
+    step = 2.0 ** (torch.floor(torch.log2(y.abs().amax(-1, keepdim=True))) - 2).clamp(min=-126)
+    step = torch.where(torch.isfinite(step), step, 1.0)
+    z = torch.empty_like(y)
+    for part, scaled, to in zip(y.split(1 << 18), (y / step).split(1 << 18), z.split(1 << 18)):
+        far = (scaled.abs()[..., None] - grid).abs()
+        best = far.amin(-1, keepdim=True)
+        even = torch.arange(8, device=x.device) % 2
+        # the nearest grid value; of two equally near ones the one whose number is even
+        to.copy_(torch.copysign(grid[(torch.where(far == best, even, 2)).argmin(-1)], part))
+    return (z * step).reshape(x.shape)
