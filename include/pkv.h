@@ -102,6 +102,12 @@ typedef enum {
                                      may be NULL; n_items (the grid) must be >= max(T, B * H_kv); B <=
                                      1024; not with PKV_FLAG_SEPARATE_MERGE (PKV_ERR_UNSUPPORTED) */
 
+#define PKV_FLAG_SCORES 128       /* the plan of a decode that adds the attention weights to scores
+                                     (pkv_paged_decode_scored, pkv_mx4_decode with scores): its workspace
+                                     also holds every token's logits.  Not with BALANCED (but for
+                                     pkv_mx4_decode), PKV_FLAG_CLUSTER_MERGE or PKV_FLAG_SHARED_PREFIX;
+                                     calls without scores refuse it (PKV_ERR_UNSUPPORTED) */
+
 /* Problem shape and pool layout.  Pool element (page, kv_head, slot, d) of
  * k_pool / v_pool lives at  page*kv_stride_page + kv_head*kv_stride_head +
  * slot*kv_stride_token + d  (elements).  The default "HND" pool
@@ -387,6 +393,134 @@ PKV_API int pkv_paged_decode(const void *q, const void *k_pool, const void *v_po
                              float scale, void *out, const pkv_shape *shape, const pkv_plan *plan,
                              const pkv_work_item *items, const int32_t *indptr, int32_t n_items,
                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* pkv_paged_decode that also accumulates attention weights, the input of an
+ * eviction (pkv_evict_tokens):
+ *     scores[i][h][t] += sum over the G query heads of KV head h of softmax(scale * q . K^T)[t]
+ * for every cached token t < N_i of row i.
+ *   scores  device float, element (i, h, t) at i * score_stride_row + h * score_stride_head + t
+ *           (strides in elements), with room for max_pages_per_seq * P tokens; elements at or
+ *           past N_i are neither read nor written
+ * `plan` carries PKV_FLAG_SCORES (NO_SPLIT, SPLIT_S or WORK_QUEUE, device-filled queues
+ * included); the workspace is sized by pkv_workspace_bytes for that plan and holds the logits
+ * between the decode kernel and the weights kernel that follows it on `stream`.  A token whose
+ * row attends to nothing (every logit -inf) gets no weight.  Deterministic.  Other arguments,
+ * layouts, errors and return codes as pkv_paged_decode. */
+PKV_API int pkv_paged_decode_scored(const void *q, const void *k_pool, const void *v_pool,
+                                    const int32_t *block_table, const int32_t *seq_lens,
+                                    int32_t page_size, float scale, void *out, float *scores,
+                                    int64_t score_stride_row, int64_t score_stride_head,
+                                    const pkv_shape *shape, const pkv_plan *plan,
+                                    const pkv_work_item *items, const int32_t *indptr, int32_t n_items,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+#define PKV_EVICT_MAX_PLANES 8
+#define PKV_EVICT_MAX_ROW_BYTES 4096
+
+/* One paged array that an eviction compacts: the row_bytes bytes of token
+ * slot s of (page, KV head h) lie at
+ *     base + page * stride_page + h * stride_head + s * stride_token   (bytes). */
+typedef struct {
+    void *base;
+    int64_t stride_page, stride_head, stride_token;
+    int32_t row_bytes; /* 1 .. PKV_EVICT_MAX_ROW_BYTES */
+    int32_t reserved;  /* 0 */
+} pkv_plane;
+
+/* Workspace of pkv_evict_tokens for this shape (B, H_kv, page_size and
+ * max_pages_per_seq): the error word and the lists of moves. */
+PKV_API int pkv_evict_workspace_bytes(const pkv_shape *shape, size_t *bytes);
+
+/* Evict cached tokens by accumulated attention weight, in place.  Every row
+ * with N_i > budget shrinks to `budget` tokens, per KV head: the `recent`
+ * newest tokens stay, and of the older ones, slots [0, N_i - recent), the
+ * budget - recent with the highest scores (the lowest slot first among equal
+ * scores; NaN counts as -inf).  With A = budget - recent:
+ *   - kept tokens in slots < A stay where they are;
+ *   - the vacated slots < A, in ascending order, receive the kept older
+ *     tokens of slots >= A, in ascending order;
+ *   - the recent tokens move down to slots [A, budget), in order.
+ * The order of the older tokens is not kept (attention does not depend on it).
+ * Scores, and positions where given, move with their tokens, and the scores
+ * of the vacated slots [budget, N_i) become 0.  Nothing else is written: not
+ * rows with N_i <= budget, not pool slots at or past `budget`.
+ *   scores     device float, as in pkv_paged_decode_scored
+ *   positions  NULL, or device int32 laid out alike under its own strides
+ *   planes     the pool's arrays (K and V of a bf16 pool; the four parts of a
+ *              4-bit pool); host array of n_planes <= PKV_EVICT_MAX_PLANES
+ *   seq_lens   device int32 [B], the lengths before the call
+ *   new_lens   device int32 [B], receives min(N_i, budget); not the same
+ *              array as seq_lens
+ *   shape      B, H_kv, page_size (16), max_pages_per_seq, num_pool_pages are used
+ *   workspace  >= pkv_evict_workspace_bytes(), zeroed once
+ * A page that two of the rows (or two places of one row) share is moved for
+ * each of them: give shared pages to one row, or copy them, before evicting.
+ * A page id out of range is reported (pkv_workspace_status) and its tokens
+ * are not moved; so is a length out of range, whose row is left alone
+ * (new_lens gets it clamped).  One kernel, asynchronous on `stream`,
+ * capturable, deterministic. */
+PKV_API int pkv_evict_tokens(float *scores, int64_t score_stride_row, int64_t score_stride_head,
+                             int32_t *positions, int64_t position_stride_row,
+                             int64_t position_stride_head, const pkv_plane *planes, int32_t n_planes,
+                             const int32_t *block_table, const int32_t *seq_lens, int32_t budget,
+                             int32_t recent, int32_t *new_lens, const pkv_shape *shape, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* The 4-bit paged cache.  A value is an e2m1 code, (-1)^s {0, .5, 1, 1.5, 2,
+ * 3, 4, 6}[low three bits], times 2^(scale - 127) with one scale byte per 32
+ * dims of a token (255: NaN; 0: all the block's values are taken as 0 by the
+ * decode).  A page (16 tokens) of one KV head is one record of 17 * D bytes:
+ *     K codes [16][D/2], V codes [16][D/2], K scales [16][D/32], V scales [16][D/32]
+ * with dim 32 b + 8 c + j (j < 8, c < 4) of a K row in byte c D/8 + 4 b + j/2 and dim
+ * 32 b + 4 r + j (j < 4, r < 8) of a V row in byte r D/16 + 2 b + j/2, in the low four bits
+ * for even j.  A record lies at pool + page * kv_stride_page + kv_head *
+ * kv_stride_head, both strides in BYTES and multiples of 16 (kv_stride_token
+ * is not used); packed pools have kv_stride_head = 17 D.  page_size 16,
+ * head_dim 64 or 128.
+ *
+ * pkv_mx4_append quantises n_tokens new tokens into their slots: token j
+ * belongs to the row i with indptr[i] <= j < indptr[i + 1] (device int32
+ * [B + 1], non-decreasing; NULL: one token per row, n_tokens = B) and goes to position
+ * seq_lens[i] + j - indptr[i], seq_lens being the lengths before the call.
+ * Tokens at or past indptr[B] are skipped.
+ *   k, v  device bf16, element (token, head, d) at token * stride_token +
+ *         head * stride_head + d (elements, multiples of 8, d contiguous)
+ * A block's scale is the exponent of its largest magnitude minus 2 (byte
+ * clamped to >= 1; 0 for a block of zeros; 255 where a value is infinite or
+ * NaN), codes are rounded to nearest even and saturate at 6.
+ * A position past the row's pages, or a page id out of range, is reported in
+ * the workspace's error word and its token skipped.  `workspace` is a decode
+ * plan's workspace, or any 256 zeroed bytes. */
+PKV_API int pkv_mx4_append(const void *k, const void *v, int64_t k_stride_token,
+                           int64_t k_stride_head, int64_t v_stride_token, int64_t v_stride_head,
+                           void *pool, const int32_t *block_table, const int32_t *seq_lens,
+                           const int32_t *indptr, int32_t n_tokens, const pkv_shape *shape,
+                           void *workspace, void *stream);
+
+/* The stored values of the tokens that pkv_mx4_append with the same seq_lens,
+ * indptr and n_tokens wrote: k, v device bf16 [n_tokens][H_kv][D], contiguous.
+ * Exact: every stored value is a bf16 number.  Fully overwritten: tokens that the append
+ * skips get zeros. */
+PKV_API int pkv_mx4_read(const void *pool, const int32_t *block_table, const int32_t *seq_lens,
+                         const int32_t *indptr, int32_t n_tokens, void *k, void *v,
+                         const pkv_shape *shape, void *workspace, void *stream);
+
+/* Workspace of pkv_mx4_decode for `plan` = {PKV_BALANCED, T, 0, flags}: T
+ * blocks (two per SM where G <= 8, else one, fill the GPU), flags 0,
+ * PKV_FLAG_SCORES and/or PKV_FLAG_NO_PDL. */
+PKV_API int pkv_mx4_workspace_bytes(const pkv_shape *shape, const pkv_plan *plan, size_t *bytes);
+
+/* pkv_paged_decode over the 4-bit cache, and with `scores` (and a plan with
+ * PKV_FLAG_SCORES) pkv_paged_decode_scored.  Every block derives its share of
+ * the pages from the device lengths, so one plan, or one captured graph,
+ * serves any lengths up to max_pages_per_seq * P.  q bf16 [B][H_q][D], out likewise; 1
+ * <= G <= 16, B <= 4096, B * H_kv * max_pages_per_seq < 2^31.  Zeros for rows without tokens;
+ * errors on device data as in pkv_paged_decode.  Deterministic. */
+PKV_API int pkv_mx4_decode(const void *q, const void *pool, const int32_t *block_table,
+                           const int32_t *seq_lens, int32_t page_size, float scale, void *out,
+                           float *scores, int64_t score_stride_row, int64_t score_stride_head,
+                           const pkv_shape *shape, const pkv_plan *plan, void *workspace,
+                           size_t workspace_bytes, void *stream);
 
 /* Scratch bytes held inside the library for pkv_paged_decode_noalloc. */
 #define PKV_NOALLOC_SCRATCH_BYTES ((size_t)16 << 20)

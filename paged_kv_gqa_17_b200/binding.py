@@ -23,6 +23,8 @@ NO_SPLIT, SPLIT_S, WORK_QUEUE, BALANCED = 0, 1, 2, 3
 FLAG_SEPARATE_MERGE, FLAG_NO_PDL, FLAG_DEEP_RING, FLAG_CLUSTER_MERGE, FLAG_PDL_EARLY = 1, 2, 4, 8, 16
 FLAG_DEVICE_FILL = 32
 FLAG_SHARED_PREFIX = 64
+FLAG_SCORES = 128
+EVICT_MAX_PLANES = 8
 FILL_MAX_ROWS = 1024  # rows a device-fill plan can plan for on the device
 INT32_MAX = 2**31 - 1
 _MODE_NAMES = {"NO_SPLIT": NO_SPLIT, "SPLIT_S": SPLIT_S, "WORK_QUEUE": WORK_QUEUE, "BALANCED": BALANCED}
@@ -74,6 +76,12 @@ class Counters(ctypes.Structure):
         return {f: int(getattr(self, f)) for f, _ in self._fields_}
 
 
+class Plane(ctypes.Structure):
+    """pkv_plane: one paged array that an eviction compacts (strides in bytes)."""
+    _fields_ = [("base", c_p), ("stride_page", c_i64), ("stride_head", c_i64), ("stride_token", c_i64),
+                ("row_bytes", c_i32), ("reserved", c_i32)]
+
+
 class HostTiming(ctypes.Structure):
     """Where one pkv_decode_host call's time went (pkv_host_timing), in microseconds."""
     _fields_ = [(n, ctypes.c_double) for n in ("host_plan_us", "host_enqueue_us", "host_wait_us", "host_unpack_us",
@@ -116,6 +124,18 @@ SIGNATURES = [
     ("pkv_selftest_wait_timeout", ctypes.c_int, [c_p, c_sz, ctypes.c_uint32, c_p]),
     ("pkv_paged_decode", ctypes.c_int,
      [c_p, c_p, c_p, c_p, c_p, c_i32, ctypes.c_float, c_p, c_p, c_p, c_p, c_p, c_i32, c_p, c_sz, c_p]),
+    ("pkv_paged_decode_scored", ctypes.c_int,
+     [c_p, c_p, c_p, c_p, c_p, c_i32, ctypes.c_float, c_p, c_p, c_i64, c_i64, c_p, c_p, c_p, c_p, c_i32, c_p, c_sz,
+      c_p]),
+    ("pkv_evict_workspace_bytes", ctypes.c_int, [c_p, c_p]),
+    ("pkv_evict_tokens", ctypes.c_int,
+     [c_p, c_i64, c_i64, c_p, c_i64, c_i64, c_p, c_i32, c_p, c_p, c_i32, c_i32, c_p, c_p, c_p, c_sz, c_p]),
+    ("pkv_mx4_append", ctypes.c_int,
+     [c_p, c_p, c_i64, c_i64, c_i64, c_i64, c_p, c_p, c_p, c_p, c_i32, c_p, c_p, c_p]),
+    ("pkv_mx4_read", ctypes.c_int, [c_p, c_p, c_p, c_p, c_i32, c_p, c_p, c_p, c_p, c_p]),
+    ("pkv_mx4_workspace_bytes", ctypes.c_int, [c_p, c_p, c_p]),
+    ("pkv_mx4_decode", ctypes.c_int,
+     [c_p, c_p, c_p, c_p, c_i32, ctypes.c_float, c_p, c_p, c_i64, c_i64, c_p, c_p, c_p, c_sz, c_p]),
     ("pkv_paged_decode_noalloc", ctypes.c_int,
      [c_p, c_p, c_p, c_p, c_p, c_i32, ctypes.c_float, c_p, c_p, c_p, c_p, c_p, c_i32, c_p]),
     ("pkv_noalloc_status", ctypes.c_int, [c_p, c_p]),
@@ -490,8 +510,14 @@ def prefix_counters(seq_lens_host, shape: Shape, items: torch.Tensor, indptr: to
 
 def plan_decode(seq_lens_host, shape: Shape, device, rules=None, plan: Optional[Plan] = None,
                 device_queue: bool = False, fill_blocks: int = 296,
-                device_fill: Optional[bool] = None, shared_prefix_table=None) -> DecodePlan:
+                device_fill: Optional[bool] = None, shared_prefix_table=None, scores: bool = False) -> DecodePlan:
     """Host planning for one batch: policy (unless `plan` is given), queue, workspace.
+
+    scores=True plans for paged_decode_scored (PKV_FLAG_SCORES: the workspace
+    also holds every token's logits).  The policy's pick keeps its mode, but
+    merges through the workspace rather than in a cluster, and a BALANCED
+    pick becomes the work queue that fills one wave of its blocks; a `plan`
+    or rule with PKV_FLAG_SCORES asks for the same.
 
     shared_prefix_table (the host block table) asks for the queue that stages
     the prefix pages rows share once for several rows (pkv_build_prefix_queue
@@ -507,8 +533,19 @@ def plan_decode(seq_lens_host, shape: Shape, device, rules=None, plan: Optional[
     asks for the builder kernel instead.  NO_SPLIT and SPLIT_S plans have no
     queue and read the lengths on the device anyway; they serve lengths up
     to those they were planned for (SPLIT_S: S' chunks of C pages)."""
+    given = plan
     if plan is None:
         plan = select_policy(seq_lens_host, shape, rules)
+    if scores or plan.flags & FLAG_SCORES:
+        if shared_prefix_table is not None or plan.flags & FLAG_SHARED_PREFIX:
+            raise ValueError("a scored plan has no prefix-sharing queue")
+        plan = Plan.from_buffer_copy(plan)
+        plan.flags = (plan.flags | FLAG_SCORES) & ~FLAG_CLUSTER_MERGE
+        if plan.mode == BALANCED:
+            if given is not None:
+                raise ValueError("a scored plan is NO_SPLIT, SPLIT_S or WORK_QUEUE")
+            fill = [Rule(0, INT32_MAX, 0, INT32_MAX, WORK_QUEUE, plan.num_splits, 0, plan.flags)]
+            plan = select_policy(seq_lens_host, shape, fill)
     if shared_prefix_table is not None and plan.mode != NO_SPLIT or (plan.flags & FLAG_SHARED_PREFIX):
         # the prefix-sharing queue at the plan's chunk (a queue-free plan's whole rows otherwise)
         if shared_prefix_table is None:
@@ -621,6 +658,359 @@ def paged_decode_noalloc(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Te
                                     plan.indptr.data_ptr() if plan.indptr is not None else None, plan.n_items,
                                     _stream_ptr(stream))
     _check(rc, "pkv_paged_decode_noalloc")
+    return out
+
+
+def _on(device, stream):
+    """Context in which a call's kernels and allocations belong to `stream` (default: the current stream of
+    `device`), whatever device is current."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+    return torch.cuda.stream(stream)
+
+
+def _cuda_device(name: str, t: torch.Tensor) -> torch.device:
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a CUDA device, not {t.device}")
+    return t.device
+
+
+def _check_tensor(name: str, t: torch.Tensor, dtype, device, contiguous: bool = True):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, not {t.device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _check_scores(name: str, t: torch.Tensor, dtype, B: int, H_kv: int, max_pages: int, device):
+    """[B][H_kv][>= max_pages * 16] with contiguous tokens, no two elements in one place."""
+    _check_tensor(name, t, dtype, device, contiguous=False)
+    if t.dim() != 3 or t.shape[0] != B or t.shape[1] != H_kv or t.shape[2] < max_pages * 16:
+        raise ValueError(f"{name} must be [{B}][{H_kv}][>= {max_pages * 16}], got {list(t.shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}'s tokens must be contiguous")
+    _check_no_overlap(name, t)
+
+
+def _check_no_overlap(name: str, t: torch.Tensor):
+    """Reject views (expanded, overlapping) in which two elements share memory: they would be written twice."""
+    reach = 1
+    for size, stride in sorted(((s, st) for s, st in zip(t.shape, t.stride()) if s > 1), key=lambda x: x[1]):
+        if stride < reach:
+            raise ValueError(f"{name} has elements that share memory")
+        reach = stride * (size - 1) + reach
+
+
+def paged_decode_scored(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, block_table: torch.Tensor,
+                        seq_lens: torch.Tensor, page_size: int, scale: float, scores: torch.Tensor, *,
+                        plan: Optional[DecodePlan] = None, seq_lens_host=None, layout: str = "HND", rules=None,
+                        out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """paged_decode that also adds every cached token's attention weight, summed over the query heads of its KV
+    head, to `scores` (fp32 [B][H_kv][>= max_pages * 16], contiguous tokens, in place):
+
+        scores[i, h, t] += sum over the G heads of KV head h of softmax(scale * q K^T)[t],  t < seq_lens[i]
+
+    the input of evict_tokens.  `plan` comes from plan_decode(..., scores=True); elements past a row's length
+    are left alone.  Everything else as paged_decode."""
+    L = lib()
+    device = _cuda_device("q", q)
+    with _on(device, stream):
+        if plan is None:
+            shape = shape_of(q, k_pool, block_table, layout, v_pool)
+            host = seq_lens_host if seq_lens_host is not None else seq_lens.detach().cpu()
+            plan = plan_decode(host, shape, device, rules, scores=True)
+        shape = plan.shape
+        if not plan.plan.flags & FLAG_SCORES:
+            raise ValueError("the plan was not made for scores: plan_decode(..., scores=True)")
+        if out is None:
+            out = torch.empty_like(q)
+        _check_decode_tensors(q, k_pool, v_pool, block_table, seq_lens, out, shape)
+        _check_scores("scores", scores, torch.float32, shape.B, shape.H_kv, shape.max_pages_per_seq, device)
+        if plan.device_queue and not plan.plan.flags & FLAG_DEVICE_FILL and plan.plan.mode == WORK_QUEUE:
+            build_fill_queue_device(seq_lens, shape, plan.fill_blocks, plan.items, plan.indptr, plan.workspace)
+        rc = L.pkv_paged_decode_scored(q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
+                                       seq_lens.data_ptr(), page_size, float(scale), out.data_ptr(),
+                                       scores.data_ptr(), scores.stride(0), scores.stride(1), ctypes.byref(shape),
+                                       ctypes.byref(plan.plan),
+                                       plan.items.data_ptr() if plan.items is not None else None,
+                                       plan.indptr.data_ptr() if plan.indptr is not None else None, plan.n_items,
+                                       plan.workspace.data_ptr(), plan.workspace.numel(), _stream_ptr())
+    _check(rc, "pkv_paged_decode_scored")
+    return out
+
+
+@dataclass
+class EvictPlan:
+    """What evict_tokens needs besides the tensors: the shape and a zeroed workspace, reusable for any lengths,
+    scores, budget and planes of that batch."""
+
+    shape: Shape
+    workspace: torch.Tensor
+
+
+def plan_evict(B: int, H_kv: int, max_pages: int, device) -> EvictPlan:
+    """Workspace for evict_tokens over B rows of H_kv KV heads and block tables of max_pages columns."""
+    L = lib()
+    shape = make_shape(B, H_kv, H_kv, 128, 16, max_pages, 1)
+    n = c_sz(0)
+    _check(L.pkv_evict_workspace_bytes(ctypes.byref(shape), ctypes.byref(n)), "pkv_evict_workspace_bytes")
+    return EvictPlan(shape, torch.zeros(n.value, dtype=torch.uint8, device=device))
+
+
+def evict_tokens(scores: torch.Tensor, planes: Sequence[torch.Tensor], block_table: torch.Tensor,
+                 seq_lens: torch.Tensor, budget: int, recent: int, *, positions: Optional[torch.Tensor] = None,
+                 layout: str = "HND", plan: Optional[EvictPlan] = None, out: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """Evict cached tokens by accumulated attention weight, in place; returns the new lengths (int32 [B]).
+
+    Every row longer than `budget` keeps, per KV head, its `recent` newest tokens and the budget - recent others
+    with the highest `scores` (the lowest slot first among equals; NaN counts as -inf).  Of the first
+    A = budget - recent slots, those whose tokens go receive, in ascending order, the kept older tokens of later slots;
+    the recent tokens move down to [A, budget) in order.  Scores and `positions` (int32, shaped like scores) move
+    with their tokens; vacated slots' scores become 0.  Rows within the budget stay as they are.
+
+    planes: the paged arrays to compact, [pages][H_kv][16][X] (layout "HND") or [pages][16][H_kv][X] ("NHD"), any
+    dtype, any strides with a contiguous last axis: (k_pool, v_pool), or mx4_planes(pool).  Pages that rows share
+    must be copied first: the call moves tokens within every row's pages.  `seq_lens` is not changed."""
+    L = lib()
+    device = _cuda_device("scores", scores)
+    B, max_pages = (int(x) for x in block_table.shape)
+    H_kv = int(scores.shape[1])
+    planes = list(planes)
+    if layout not in ("HND", "NHD"):
+        raise ValueError(layout)
+    if not planes or len(planes) > EVICT_MAX_PLANES:
+        raise ValueError(f"between 1 and {EVICT_MAX_PLANES} planes, got {len(planes)}")
+    if not 0 <= recent <= budget or budget > INT32_MAX:
+        raise ValueError(f"0 <= recent <= budget, got recent {recent}, budget {budget}")
+    with _on(device, stream):
+        if plan is None:
+            plan = plan_evict(B, H_kv, max_pages, device)
+        if (plan.shape.B, plan.shape.H_kv, plan.shape.max_pages_per_seq) != (B, H_kv, max_pages):
+            raise ValueError("the plan was made for another batch (B, H_kv or max_pages)")
+        if out is None:
+            out = torch.empty(B, dtype=torch.int32, device=device)
+        _check_scores("scores", scores, torch.float32, B, H_kv, max_pages, device)
+        if positions is not None:
+            _check_scores("positions", positions, torch.int32, B, H_kv, max_pages, device)
+        for name, t in (("block_table", block_table), ("seq_lens", seq_lens), ("out", out)):
+            _check_tensor(name, t, torch.int32, device)
+        if seq_lens.numel() < B or out.numel() < B:
+            raise ValueError(f"seq_lens and out must hold {B} lengths")
+        if out.data_ptr() < seq_lens.data_ptr() + 4 * B and seq_lens.data_ptr() < out.data_ptr() + 4 * B:
+            raise ValueError("out must not share memory with seq_lens")
+        pages = int(planes[0].shape[0])
+        head_axis, token_axis = (1, 2) if layout == "HND" else (2, 1)
+        arr = (Plane * len(planes))()
+        for i, t in enumerate(planes):
+            if t.device != device:
+                raise ValueError(f"plane {i} must be on {device}, not {t.device}")
+            if t.dim() != 4 or t.shape[0] != pages or t.shape[head_axis] != H_kv or t.shape[token_axis] != 16:
+                raise ValueError(f"plane {i}'s shape {list(t.shape)} is not {pages} {layout} pages of {H_kv} heads "
+                                 "and 16 tokens")
+            if t.shape[3] < 1 or (t.shape[3] > 1 and t.stride(3) != 1):
+                raise ValueError(f"plane {i}'s last axis must be contiguous")
+            _check_no_overlap(f"plane {i}", t)
+            size = t.element_size()
+            arr[i] = Plane(t.data_ptr(), t.stride(0) * size, t.stride(head_axis) * size, t.stride(token_axis) * size,
+                           int(t.shape[3]) * size, 0)
+        shape = make_shape(B, H_kv, H_kv, 128, 16, max_pages, pages)
+        rc = L.pkv_evict_tokens(scores.data_ptr(), scores.stride(0), scores.stride(1),
+                                positions.data_ptr() if positions is not None else None,
+                                positions.stride(0) if positions is not None else 0,
+                                positions.stride(1) if positions is not None else 0, arr, len(planes),
+                                block_table.data_ptr(), seq_lens.data_ptr(), int(budget), int(recent), out.data_ptr(),
+                                ctypes.byref(shape), plan.workspace.data_ptr(), plan.workspace.numel(), _stream_ptr())
+    _check(rc, "pkv_evict_tokens")
+    return out
+
+
+def mx4_pool(pages: int, H_kv: int, head_dim: int, device) -> torch.Tensor:
+    """An empty 4-bit pool: uint8 [pages][H_kv][17 * head_dim], one record per page and KV head (include/pkv.h
+    describes it).  Zero bytes are tokens of zeros."""
+    if head_dim not in (64, 128):
+        raise ValueError(f"head_dim must be 64 or 128, got {head_dim}")
+    return torch.zeros(pages, H_kv, 17 * head_dim, dtype=torch.uint8, device=device)
+
+
+def _mx4_head_dim(pool: torch.Tensor) -> int:
+    if pool.dim() != 3 or pool.shape[2] not in (17 * 64, 17 * 128):
+        raise ValueError(f"a 4-bit pool is [pages][H_kv][17 * head_dim], head_dim 64 or 128, got {list(pool.shape)}")
+    return int(pool.shape[2]) // 17
+
+
+def mx4_planes(pool: torch.Tensor) -> tuple:
+    """The four arrays of a 4-bit pool as views [pages][H_kv][16][...]: K codes, V codes, K scales, V scales (the
+    planes of evict_tokens)."""
+    D = _mx4_head_dim(pool)
+    parts, at = [], 0
+    for n in (D // 2, D // 2, D // 32, D // 32):
+        parts.append(pool[:, :, at:at + 16 * n].unflatten(2, (16, n)))
+        at += 16 * n
+    return tuple(parts)
+
+
+def mx4_shape(pool: torch.Tensor, block_table: torch.Tensor, q_heads: Optional[int] = None) -> Shape:
+    """Shape of the calls over a 4-bit pool (strides in bytes); q_heads is needed for mx4_decode."""
+    D = _mx4_head_dim(pool)
+    pages, H_kv = int(pool.shape[0]), int(pool.shape[1])
+    B, max_pages = (int(x) for x in block_table.shape)
+    if pool.stride(2) != 1:
+        raise ValueError("the pool's records must be contiguous")
+    _check_no_overlap("pool", pool)
+    head = pool.stride(1) if H_kv > 1 else 17 * D
+    page = pool.stride(0) if pages > 1 else H_kv * head
+    return Shape(B, H_kv if q_heads is None else q_heads, H_kv, D, 16, max_pages, pages, 0, page, head, D // 2)
+
+
+@dataclass
+class Mx4Plan:
+    """What the calls over a 4-bit pool need besides the tensors: the shape, the grid and a zeroed workspace.
+    Every call derives its work from the device lengths, so one plan serves any of them."""
+
+    shape: Shape
+    plan: Plan
+    workspace: torch.Tensor
+
+
+def plan_mx4(shape: Shape, device, scores: bool = False, blocks: Optional[int] = None) -> Mx4Plan:
+    """Plan for mx4_append, mx4_read and mx4_decode over mx4_shape(...); scores=True for mx4_decode with scores.
+    `blocks` (default: what fills the GPU, two per SM up to G = 8, else one) is the decode's grid."""
+    L = lib()
+    if blocks is None:
+        blocks = torch.cuda.get_device_properties(device).multi_processor_count
+        blocks *= 2 if shape.H_q <= 8 * shape.H_kv else 1
+    plan = Plan(BALANCED, blocks, 0, FLAG_SCORES if scores else 0)
+    n = c_sz(0)
+    _check(L.pkv_mx4_workspace_bytes(ctypes.byref(shape), ctypes.byref(plan), ctypes.byref(n)),
+           "pkv_mx4_workspace_bytes")
+    return Mx4Plan(shape, plan, torch.zeros(n.value, dtype=torch.uint8, device=device))
+
+
+def _check_mx4(pool, block_table, seq_lens, shape: Shape) -> torch.device:
+    device = _cuda_device("pool", pool)
+    _check_tensor("pool", pool, torch.uint8, device, contiguous=False)
+    if _mx4_head_dim(pool) != shape.head_dim or pool.shape[1] != shape.H_kv or pool.shape[0] < shape.num_pool_pages:
+        raise ValueError(f"pool {list(pool.shape)} differs from the plan's shape")
+    if (pool.stride(2) != 1 or (pool.shape[1] > 1 and pool.stride(1) != shape.kv_stride_head)
+            or (pool.shape[0] > 1 and pool.stride(0) != shape.kv_stride_page)):
+        raise ValueError("the pool's strides differ from the plan's shape")
+    _check_tensor("block_table", block_table, torch.int32, device)
+    _check_tensor("seq_lens", seq_lens, torch.int32, device)
+    if tuple(block_table.shape) != (shape.B, shape.max_pages_per_seq):
+        raise ValueError(f"block_table must be [{shape.B}][{shape.max_pages_per_seq}], got {list(block_table.shape)}")
+    if seq_lens.numel() < shape.B:
+        raise ValueError(f"seq_lens holds {seq_lens.numel()} lengths for {shape.B} rows")
+    return device
+
+
+def _check_indptr(indptr, n_tokens: int, shape: Shape, device):
+    if indptr is None:
+        if n_tokens != shape.B:
+            raise ValueError(f"without indptr there is one token per row: {n_tokens} tokens for {shape.B} rows")
+        return None
+    _check_tensor("indptr", indptr, torch.int32, device)
+    if indptr.numel() != shape.B + 1:
+        raise ValueError(f"indptr must hold {shape.B + 1} offsets, got {indptr.numel()}")
+    return indptr.data_ptr()
+
+
+def mx4_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor,
+               seq_lens: torch.Tensor, *, plan: Optional[Mx4Plan] = None, indptr: Optional[torch.Tensor] = None,
+               stream=None) -> None:
+    """Quantise new tokens into a 4-bit pool: k, v bf16 [n][H_kv][D] (contiguous D, other strides multiples of 8).
+
+    Token j belongs to the row i with indptr[i] <= j < indptr[i + 1] (int32 [B + 1] on the device; without it there
+    is one token per row) and goes to position seq_lens[i] + j - indptr[i]; seq_lens are the lengths before the call
+    and stay unchanged.  Positions past a row's pages and bad page ids are skipped and reported
+    (workspace_status(plan))."""
+    L = lib()
+    if plan is None:
+        plan = plan_mx4(mx4_shape(pool, block_table), _cuda_device("pool", pool))
+    shape = plan.shape
+    device = _check_mx4(pool, block_table, seq_lens, shape)
+    for name, t in (("k", k), ("v", v)):
+        _check_tensor(name, t, torch.bfloat16, device, contiguous=False)
+        if t.dim() != 3 or tuple(t.shape[1:]) != (shape.H_kv, shape.head_dim):
+            raise ValueError(f"{name} must be [n][{shape.H_kv}][{shape.head_dim}], got {list(t.shape)}")
+        if t.stride(2) != 1:
+            raise ValueError(f"{name}'s head_dim axis must be contiguous")
+    n = int(k.shape[0])
+    if v.shape[0] != n:
+        raise ValueError(f"k has {n} tokens, v {v.shape[0]}")
+    ptr = _check_indptr(indptr, n, shape, device)
+    ks, vs = ([t.stride(0) if n > 1 else 0, t.stride(1) if shape.H_kv > 1 else 0] for t in (k, v))
+    with _on(device, stream):
+        rc = L.pkv_mx4_append(k.data_ptr(), v.data_ptr(), *ks, *vs, pool.data_ptr(), block_table.data_ptr(),
+                              seq_lens.data_ptr(), ptr, n, ctypes.byref(shape), plan.workspace.data_ptr(),
+                              _stream_ptr())
+    _check(rc, "pkv_mx4_append")
+
+
+def mx4_read(pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, n_tokens: int, *,
+             plan: Optional[Mx4Plan] = None, indptr: Optional[torch.Tensor] = None,
+             out: Optional[tuple] = None, stream=None) -> tuple:
+    """The stored values, bf16 (k, v) [n_tokens][H_kv][D], of the tokens that mx4_append with the same seq_lens and
+    indptr wrote.  Exact.  `out` = (k, v) is written in place; tokens that the append skips get zeros."""
+    L = lib()
+    if plan is None:
+        plan = plan_mx4(mx4_shape(pool, block_table), _cuda_device("pool", pool))
+    shape = plan.shape
+    device = _check_mx4(pool, block_table, seq_lens, shape)
+    n = int(n_tokens)
+    if n < 0:
+        raise ValueError(f"n_tokens must be >= 0, got {n}")
+    ptr = _check_indptr(indptr, n, shape, device)
+    with _on(device, stream):
+        if out is None:
+            out = tuple(torch.empty(n, shape.H_kv, shape.head_dim, dtype=torch.bfloat16, device=device)
+                        for _ in range(2))
+        for name, t in zip(("k", "v"), out):
+            _check_tensor(f"out's {name}", t, torch.bfloat16, device)
+            if tuple(t.shape) != (n, shape.H_kv, shape.head_dim):
+                raise ValueError(f"out's {name} must be [{n}][{shape.H_kv}][{shape.head_dim}], got {list(t.shape)}")
+        rc = L.pkv_mx4_read(pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), ptr, n, out[0].data_ptr(),
+                            out[1].data_ptr(), ctypes.byref(shape), plan.workspace.data_ptr(), _stream_ptr())
+    _check(rc, "pkv_mx4_read")
+    return tuple(out)
+
+
+def mx4_decode(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+               page_size: int, scale: float, *, plan: Optional[Mx4Plan] = None,
+               scores: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """paged_decode over a 4-bit pool; with `scores` (as in paged_decode_scored, and a plan with scores=True) the
+    attention weights are added to them.  q bf16 [B][H_q][D], 1 <= H_q / H_kv <= 16.  The plan serves any lengths, so
+    a captured call can be replayed after seq_lens changed on the device."""
+    L = lib()
+    if plan is None:
+        plan = plan_mx4(mx4_shape(pool, block_table, int(q.shape[1])), _cuda_device("pool", pool), scores is not None)
+    shape = plan.shape
+    device = _check_mx4(pool, block_table, seq_lens, shape)
+    _check_tensor("q", q, torch.bfloat16, device)
+    if tuple(q.shape) != (shape.B, shape.H_q, shape.head_dim):
+        raise ValueError(f"q must be [{shape.B}][{shape.H_q}][{shape.head_dim}], got {list(q.shape)}")
+    if (scores is not None) != bool(plan.plan.flags & FLAG_SCORES):
+        raise ValueError("scores go with a plan made for them, plan_mx4(..., scores=True), and only with it")
+    if scores is not None:
+        _check_scores("scores", scores, torch.float32, shape.B, shape.H_kv, shape.max_pages_per_seq, device)
+    with _on(device, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        _check_tensor("out", out, torch.bfloat16, device)
+        if out.shape != q.shape:
+            raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
+        rc = L.pkv_mx4_decode(q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), page_size,
+                              float(scale), out.data_ptr(), scores.data_ptr() if scores is not None else None,
+                              scores.stride(0) if scores is not None else 0,
+                              scores.stride(1) if scores is not None else 0, ctypes.byref(shape),
+                              ctypes.byref(plan.plan), plan.workspace.data_ptr(), plan.workspace.numel(),
+                              _stream_ptr())
+    _check(rc, "pkv_mx4_decode")
     return out
 
 

@@ -13,6 +13,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -77,12 +79,19 @@ def build(force: bool = False, verbose: bool = False, out: str = LIB, extra=()) 
     if not force and not _stale(out):
         return out
     tmp = out + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-shared", "-o", tmp, *sources(),
-           "-cudart", "static"]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    with tempfile.TemporaryDirectory(prefix="pkv_build_") as objs:
+        # one nvcc per source, side by side, then one link
+        cmds = []
+        for src in sources():
+            obj = os.path.join(objs, os.path.basename(src) + ".o")
+            cmds.append([nvcc(), *(["-Xptxas=-v"] if verbose else []), *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC,
+                         "-c", src, "-o", obj])
+        link = [nvcc(), *NVCC_FLAGS, "-shared", "-o", tmp, *(c[-1] for c in cmds), "-cudart", "static"]
+        if verbose:
+            print("\n".join(" ".join(c) for c in (*cmds, link)), flush=True)
+        with ThreadPoolExecutor(max_workers=max(1, min(len(cmds), os.cpu_count() or 1))) as pool:
+            list(pool.map(lambda c: subprocess.run(c, check=True), cmds))
+        subprocess.run(link, check=True)
     os.replace(tmp, out)
     return out
 

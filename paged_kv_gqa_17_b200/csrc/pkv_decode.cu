@@ -51,6 +51,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "pkv_device.h"
 #include "pkv_internal.h"
 
 // One rank-5 TMA copy per K (or V) page; 0 selects one rank-4 copy per
@@ -69,8 +70,6 @@ namespace pkv {
 
 constexpr int kBoxD = 64;                   // head-dim elements per TMA box row (128 bytes)
 constexpr int kBoxBytes = kBoxD * kPage * 2; // one [16 tokens][64 d] bf16 box = 2 KiB
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr uint32_t kWaitLimitIters = 1u << 30;
 
 struct __align__(64) Params {
     CUtensorMap tm_k;  // pool views [pages][H_kv][P][D] -> boxes of [1][1][16][64]
@@ -96,6 +95,11 @@ struct __align__(64) Params {
     int32_t n_units;          // prefix-sharing queue: units (the grid); their offsets follow the pair offsets
     int32_t device_fill;      // WORK_QUEUE: every block derives its own item from the device lengths
     int32_t fill_blocks;      // ... of the queue whose chunk fills one wave of this many blocks
+    // scored decode (PKV_FLAG_SCORES): the logits in the log2 domain, [pair][max_pages * P][logit_heads], and each
+    // pair's first state slot and slot count, both for the weights kernel that follows
+    float *logits;
+    int2 *slot_range;
+    int32_t logit_heads;      // G rounded up to even, so that a lane's two heads are one 8-byte store
 #ifdef PKV_TRACE
     int32_t trace_epoch;
 #endif
@@ -110,51 +114,6 @@ __device__ __forceinline__ void raise_error(const Params &p, uint32_t bit)
     atomicOr(p.ws_error, bit);
     if (p.host_err)
         *reinterpret_cast<volatile uint32_t *>(p.host_err + (__ffs(bit) - 1)) = 1u;
-}
-
-// ---------------------------------------------------------------------------
-// PTX wrappers
-
-__device__ __forceinline__ uint32_t smem_addr(const void *p)
-{
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n"
-        " .reg .pred p;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n"
-        "}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-__device__ __forceinline__ uint64_t global_timer_ns()
-{
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
 }
 
 // Optional timeline tracing (build with -DPKV_TRACE): thread 0 of each block
@@ -175,163 +134,6 @@ __device__ unsigned long long g_pkv_trace_buf[2][kTraceBlocks][16];
     } while (0)
 #endif
 
-// Wait for phase `parity` of an mbarrier, giving up after kWaitLimitNs (or
-// kWaitLimitIters polls) with the timeout bit set in the error word (and,
-// when host_flags is not NULL, the timeout's flag word set in host memory).
-__device__ __noinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t *err, uint64_t limit_ns = kWaitLimitNs,
-                                       uint32_t *host_flags = nullptr)
-{
-    if (mbar_try_wait(bar, parity))
-        return true;
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t i = 1; i < kWaitLimitIters; ++i) {
-        if (mbar_try_wait(bar, parity))
-            return true;
-        if ((i & 255u) == 0 && global_timer_ns() - t0 > limit_ns)
-            break;
-    }
-    atomicOr(err, kErrTimeout);
-    if (host_flags)
-        *reinterpret_cast<volatile uint32_t *>(host_flags) = 1u;  // bit 0: timeout
-    return false;
-}
-
-__device__ __forceinline__ uint64_t evict_first_policy()
-{
-    uint64_t pol;
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
-    return pol;
-}
-
-// TMA tiled copy of one [1][1][16][64] box of a pool view into shared memory.
-__device__ __forceinline__ void tma_load_box(uint32_t dst, const CUtensorMap *tm, uint32_t bar, int d0, int head,
-                                             int page, uint64_t policy)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(d0), "r"(0), "r"(head), "r"(page), "r"(bar), "l"(policy)
-        : "memory");
-}
-
-// Bulk (non-tensor) async copy global -> shared, completion on an mbarrier.
-// Both addresses 16-byte aligned, size a multiple of 16.
-__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-
-// Per-thread asynchronous copies global -> shared that bypass L1 (16 or 4
-// bytes), and the wait for all of this thread's copies.
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src))
-                 : "memory");
-}
-
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src))
-                 : "memory");
-}
-
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-// Wait until at most the most recently committed group of this thread's
-// async copies is still in flight.
-__device__ __forceinline__ void cp_async_wait_but_last() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
-
-__device__ __forceinline__ void cp_async_wait_all()
-{
-    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-}
-
-// Ticket: atomic add with release (orders this block's earlier writes, made
-// visible to thread 0 by the preceding __syncthreads) and acquire (the last
-// arriver sees every other block's released writes).
-__device__ __forceinline__ uint32_t ticket_acq_rel(uint32_t *ctr)
-{
-    uint32_t prev;
-    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(prev) : "l"(ctr) : "memory");
-    return prev;
-}
-
-__device__ __forceinline__ void fence_proxy_async_global()
-{
-    asm volatile("fence.proxy.async.global;" ::: "memory");
-}
-
-// Programmatic dependent launch: wait for the grids this one depends on
-// (complete, memory visible); allow dependents to be scheduled.  Both are
-// no-ops when the kernel was launched without the PDL attribute.
-__device__ __forceinline__ void grid_dependency_wait()
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-__device__ __forceinline__ void grid_launch_dependents()
-{
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-// Thread-block clusters: rank in the cluster, a full cluster barrier
-// (release / acquire), and loads from a peer block's shared memory.
-__device__ __forceinline__ uint32_t cluster_ctarank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_sync_all()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ uint32_t map_shared_rank(uint32_t addr, uint32_t rank)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
-{
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
-{
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
-// Barrier among the first `threads` threads of the block (named barrier `id`).
-__device__ __forceinline__ void named_barrier(int id, int threads)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// TMA tiled copy of a whole (page, head) block [d_hi][16 tokens][64 d] of a
-// rank-5 pool view (head_dim split as 64 x d_hi) in one instruction.
-__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap *tm, uint32_t bar, int head, int page,
-                                              uint64_t policy)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(0), "r"(0), "r"(0), "r"(head), "r"(page), "r"(bar), "l"(policy)
-        : "memory");
-}
-
 // L2 prefetch of one (page, head) block through the same tensor map: no
 // shared memory, no barrier; coordinates outside the tensor fetch nothing.
 template <int D>
@@ -349,101 +151,6 @@ __device__ __forceinline__ void tma_prefetch_page_l2(const CUtensorMap *tm, int 
                      "r"(d0), "r"(0), "r"(head), "r"(page)
                      : "memory");
 #endif
-}
-
-// Loads that are cached in L2 only (never in L1), for reads of data that a
-// kernel still running may be writing: a later load of the same address
-// after the dependency wait cannot hit a stale L1 line.
-__device__ __forceinline__ int ld_l2_only(const int32_t *ptr)
-{
-    int v;
-    asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(ptr));
-    return v;
-}
-
-__device__ __forceinline__ int4 ld_l2_only(const int4 *ptr)
-{
-    int4 v;
-    asm volatile("ld.global.cg.v4.s32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(ptr));
-    return v;
-}
-
-__device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *tm)
-{
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
-}
-
-__device__ __forceinline__ void fence_proxy_async_smem()
-{
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-                 : "r"(addr));
-}
-
-__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2,
-                                              uint32_t &r3)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-                 : "r"(addr));
-}
-
-// D = A * B + D, m16n8k16, bf16 operands, fp32 accumulators.
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1)
-{
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Transpose an 8x8 b16 matrix held one row pair per lane.
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x)
-{
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-
-// 2^x on the SFU (ex2.approx: relative error ~2^-22); 2^-inf = +0.
-__device__ __forceinline__ float exp2_approx(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t *>(&v);
-}
-
-__device__ __forceinline__ void store_bf16x4(__nv_bfloat16 *dst, float4 v)
-{
-    uint2 u;
-    u.x = pack_bf16(v.x, v.y);
-    u.y = pack_bf16(v.z, v.w);
-    *reinterpret_cast<uint2 *>(dst) = u;
-}
-
-__device__ __forceinline__ float4 fma4(float4 a, float s, float4 b)  // a * s + b
-{
-    return make_float4(fmaf(a.x, s, b.x), fmaf(a.y, s, b.y), fmaf(a.z, s, b.z), fmaf(a.w, s, b.w));
-}
-
-__device__ __forceinline__ float4 scale4(float4 a, float s)
-{
-    return make_float4(a.x * s, a.y * s, a.z * s, a.w * s);
 }
 
 // ---------------------------------------------------------------------------
@@ -538,12 +245,15 @@ __device__ __forceinline__ bool issue_pages(const Params &p, int lane, int e, in
 // back to the producer as soon as the K/V fragments are in registers, the
 // online-softmax update of (m, l, o) in the log2 domain with tokens >= nvalid
 // masked, and O^T += V^T P^T.
-template <int D, int NT>
+// SCORED also stores the logits of the valid tokens to `logits` (this page's first token, `logit_heads`
+// floats per token; see Params).
+template <int D, int NT, bool SCORED = false>
 __device__ __forceinline__ void attend_page(uint8_t *smem, uint32_t sbase, uint32_t ks_base, uint32_t vs_base,
                                             uint32_t bar_empty_s, int nvalid, int lane, int r, int ri,
                                             uint32_t k_off, int k_hi, uint32_t v_off, int v_hi, float sl2,
                                             const uint32_t (&qf)[D / 16][NT][2], float (&m_run)[NT][2],
-                                            float (&l_run)[NT][2], float (&o)[D / 16][NT][4])
+                                            float (&l_run)[NT][2], float (&o)[D / 16][NT][4], float *logits = nullptr,
+                                            int logit_heads = 0)
 {
     constexpr int kHalves = D / kBoxD;
     if (nvalid < kPage) {
@@ -597,6 +307,15 @@ __device__ __forceinline__ void attend_page(uint8_t *smem, uint32_t sbase, uint3
         const float x1 = lo_ok ? sacc[nt][1] * sl2 : -INFINITY;
         const float x2 = hi_ok ? sacc[nt][2] * sl2 : -INFINITY;
         const float x3 = hi_ok ? sacc[nt][3] * sl2 : -INFINITY;
+        if constexpr (SCORED) {
+            const int g = 8 * nt + 2 * (lane & 3);
+            if (g < logit_heads) {
+                if (lo_ok)
+                    *reinterpret_cast<float2 *>(logits + r * logit_heads + g) = make_float2(x0, x1);
+                if (hi_ok)
+                    *reinterpret_cast<float2 *>(logits + (r + 8) * logit_heads + g) = make_float2(x2, x3);
+            }
+        }
         float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) {
@@ -1357,7 +1076,7 @@ __device__ __forceinline__ FillItem fill_queue_item(const Params &p, int32_t *sm
 // FILL: the self-planned queue (PKV_FLAG_DEVICE_FILL) and its speculative
 // start are compiled into a variant of their own: in the other variants
 // their code cost the main loop 6 registers and 0.1-0.3 us per step.
-template <int D, int NT, int NW, int NST, bool CL, bool FILL>
+template <int D, int NT, int NW, int NST, bool CL, bool FILL, bool SCORED>
 __global__ void __launch_bounds__((NW + 1) * 32, (NST >= 12 ? 2 : 3)) split_kernel(const __grid_constant__ Params p)
 {
     using C = Cfg<D, NT, NW, NST>;
@@ -1581,6 +1300,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, (NST >= 12 ? 2 : 3)) split_kern
         } else {
             tb = 0;
             te = N;
+            if constexpr (SCORED)
+                slot0 = my_slot = pair;  // its state goes to the weights kernel
         }
     }
     const int pair = row * p.H_kv + h;
@@ -1736,8 +1457,11 @@ __global__ void __launch_bounds__((NW + 1) * 32, (NST >= 12 ? 2 : 3)) split_kern
             const uint32_t vs_base = v_ring + s * C::kStageBytes;
             const int tok0 = (pg0 + pidx) * kPage;
             const int nvalid = te - tok0 < kPage ? te - tok0 : kPage;
-            attend_page<D, NT>(smem, sbase, ks_base, vs_base, bar_empty + 8 * s, nvalid, lane, r, ri, k_off, k_hi,
-                               v_off, v_hi, sl2, qf, m_run, l_run, o);
+            float *logits = nullptr;
+            if constexpr (SCORED)
+                logits = p.logits + ((int64_t)pair * row_cap + tok0) * p.logit_heads;
+            attend_page<D, NT, SCORED>(smem, sbase, ks_base, vs_base, bar_empty + 8 * s, nvalid, lane, r, ri, k_off,
+                                       k_hi, v_off, v_hi, sl2, qf, m_run, l_run, o, logits, p.logit_heads);
             if (pidx == 0)
                 PKV_TRACE_POINT(2);
         }
@@ -1813,6 +1537,12 @@ __global__ void __launch_bounds__((NW + 1) * 32, (NST >= 12 ? 2 : 3)) split_kern
         } else if (nslots == 1) {
             const float inv = L > 0.f ? 1.f / L : 0.f;
             store_bf16x4(p.out + ((int64_t)row * p.H_q + (int64_t)h * G + g) * D + d4, scale4(O, inv));
+            if constexpr (SCORED) {
+                if (d4 == 0) {
+                    p.ws_m[(int64_t)my_slot * G + g] = M;
+                    p.ws_l[(int64_t)my_slot * G + g] = L;
+                }
+            }
         } else {
             const int64_t idx = (int64_t)my_slot * G + g;
             *reinterpret_cast<float4 *>(p.ws_acc + idx * D + d4) = O;
@@ -1823,6 +1553,10 @@ __global__ void __launch_bounds__((NW + 1) * 32, (NST >= 12 ? 2 : 3)) split_kern
         }
     }
 
+    if constexpr (SCORED) {
+        if (tid == 0 && my_slot == slot0)
+            p.slot_range[pair] = make_int2(slot0, nslots);
+    }
     PKV_TRACE_POINT(4);
     if (CL) {
         // ---- cluster merge: the S blocks of this (row, KV head) form one
@@ -3099,12 +2833,12 @@ cudaError_t launch_ex(void (*kernel)(Args...), unsigned grid, unsigned block, si
     return cudaLaunchKernelEx(&cfg, kernel, prm);
 }
 
-template <int D, int NT, int NST, bool CL, bool FILL>
+template <int D, int NT, int NST, bool CL, bool FILL, bool SCORED>
 cudaError_t launch_split(const Params &prm, int64_t grid, cudaStream_t st, bool pdl, unsigned cluster)
 {
     using C = Cfg<D, NT, kNW, NST>;
     static std::atomic<uint64_t> configured{0};
-    auto kernel = split_kernel<D, NT, kNW, NST, CL, FILL>;
+    auto kernel = split_kernel<D, NT, kNW, NST, CL, FILL, SCORED>;
     cudaError_t e = set_smem(kernel, kMaxDynSmem, configured);
     if (e != cudaSuccess)
         return e;
@@ -3130,20 +2864,20 @@ cudaError_t launch_split(const Params &prm, int64_t grid, cudaStream_t st, bool 
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int NST, bool CL, bool FILL>
+template <int NST, bool CL, bool FILL, bool SCORED = false>
 cudaError_t launch_split_nst(int D, int NT, const Params &prm, int64_t grid, cudaStream_t st, bool pdl,
                              unsigned cluster)
 {
     if (D == 128) {
         if (NT == 1)
-            return launch_split<128, 1, NST, CL, FILL>(prm, grid, st, pdl, cluster);
+            return launch_split<128, 1, NST, CL, FILL, SCORED>(prm, grid, st, pdl, cluster);
         if constexpr (NST >= 12)
-            return launch_split<128, 2, NST, CL, FILL>(prm, grid, st, pdl, cluster);
+            return launch_split<128, 2, NST, CL, FILL, SCORED>(prm, grid, st, pdl, cluster);
         else
             return cudaErrorInvalidConfiguration;  // launch_split_any gives this tile the deep ring
     }
-    return NT == 1 ? launch_split<64, 1, NST, CL, FILL>(prm, grid, st, pdl, cluster)
-                   : launch_split<64, 2, NST, CL, FILL>(prm, grid, st, pdl, cluster);
+    return NT == 1 ? launch_split<64, 1, NST, CL, FILL, SCORED>(prm, grid, st, pdl, cluster)
+                   : launch_split<64, 2, NST, CL, FILL, SCORED>(prm, grid, st, pdl, cluster);
 }
 
 #ifndef PKV_NST_BAL
@@ -3213,6 +2947,12 @@ cudaError_t launch_split_any(int D, int NT, bool deep, const Params &prm, int64_
                              unsigned cluster)
 {
     deep = deep || (D == 128 && NT == 2);
+    if (prm.logits && prm.device_fill)
+        return deep ? launch_split_nst<kNSTDeep, false, true, true>(D, NT, prm, grid, st, pdl, 0)
+                    : launch_split_nst<kNST, false, true, true>(D, NT, prm, grid, st, pdl, 0);
+    if (prm.logits)
+        return deep ? launch_split_nst<kNSTDeep, false, false, true>(D, NT, prm, grid, st, pdl, 0)
+                    : launch_split_nst<kNST, false, false, true>(D, NT, prm, grid, st, pdl, 0);
     if (cluster > 0)
         return deep ? launch_split_nst<kNSTDeep, true, false>(D, NT, prm, grid, st, pdl, cluster)
                     : launch_split_nst<kNST, true, false>(D, NT, prm, grid, st, pdl, cluster);
@@ -3222,8 +2962,6 @@ cudaError_t launch_split_any(int D, int NT, bool deep, const Params &prm, int64_
     return deep ? launch_split_nst<kNSTDeep, false, false>(D, NT, prm, grid, st, pdl, 0)
                 : launch_split_nst<kNST, false, false>(D, NT, prm, grid, st, pdl, 0);
 }
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int check_fast_path(const pkv_shape &s)
 {
@@ -3259,7 +2997,7 @@ int paged_decode_impl(const void *q, const void *k_pool, const void *v_pool, con
                       const int32_t *seq_lens, int32_t page_size, float scale, void *out, const pkv_shape *shape,
                       const pkv_plan *plan, const pkv_work_item *items, const int32_t *indptr, int32_t n_items,
                       void *workspace, size_t workspace_bytes, cudaStream_t st, const WsPtrs *sections = nullptr,
-                      size_t zero_bytes = 0)
+                      size_t zero_bytes = 0, const ScoreArgs *scores = nullptr)
 {
     if (check_shape(shape) != PKV_OK || !plan || page_size != shape->page_size)
         return PKV_ERR_INVALID;
@@ -3271,6 +3009,11 @@ int paged_decode_impl(const void *q, const void *k_pool, const void *v_pool, con
         return PKV_ERR_INVALID;
     const bool device_fill = (pl.flags & PKV_FLAG_DEVICE_FILL) != 0;
     const bool shared_prefix = (pl.flags & PKV_FLAG_SHARED_PREFIX) != 0;
+    // a plan's scores flag sizes its workspace: it goes with the scored entry point, and only there
+    if (((pl.flags & PKV_FLAG_SCORES) != 0) != (scores != nullptr))
+        return PKV_ERR_UNSUPPORTED;
+    if (scores && (shared_prefix || pl.mode == PKV_BALANCED || (pl.flags & PKV_FLAG_CLUSTER_MERGE)))
+        return PKV_ERR_UNSUPPORTED;
     if (shared_prefix) {
         // the prefix-sharing queue: num_splits carries the unit count (the grid)
         if (pl.mode != PKV_WORK_QUEUE || device_fill || (pl.flags & PKV_FLAG_PDL_EARLY))
@@ -3309,11 +3052,14 @@ int paged_decode_impl(const void *q, const void *k_pool, const void *v_pool, con
         (!sections && !aligned(workspace, 256)) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
         (items && !aligned(items, 16)) || (indptr && !aligned(indptr, 4)))
         return PKV_ERR_UNSUPPORTED;
+    if (scores && (!scores->scores || !aligned(scores->scores, 4)))
+        return scores->scores ? PKV_ERR_UNSUPPORTED : PKV_ERR_INVALID;
     WsPtrs wp;
+    WsLayout ws;
     if (sections) {
         wp = *sections;
     } else {
-        const WsLayout ws = ws_layout(s, pl, n_items);
+        ws = ws_layout(s, pl, n_items);
         if (workspace_bytes < ws.total)
             return PKV_ERR_CAPACITY;
         uint8_t *wsb = static_cast<uint8_t *>(workspace);
@@ -3358,6 +3104,11 @@ int paged_decode_impl(const void *q, const void *k_pool, const void *v_pool, con
     prm.device_fill = device_fill ? 1 : 0;
     prm.n_units = shared_prefix ? pl.num_splits : 0;
     prm.fill_blocks = device_fill ? pl.num_splits : 0;
+    if (scores) {
+        prm.logits = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + ws.logits_off);
+        prm.slot_range = reinterpret_cast<int2 *>(static_cast<uint8_t *>(workspace) + ws.range_off);
+        prm.logit_heads = logit_heads(prm.G);
+    }
 #ifdef PKV_TRACE
     static std::atomic<int32_t> trace_launches{0};
     prm.trace_epoch = trace_launches.fetch_add(1);
@@ -3369,6 +3120,8 @@ int paged_decode_impl(const void *q, const void *k_pool, const void *v_pool, con
                          : pl.mode == PKV_BALANCED || shared_prefix ? (int64_t)pl.num_splits
                                                                      : n_items;
     if (grid > INT32_MAX || pairs > INT32_MAX)
+        return PKV_ERR_UNSUPPORTED;
+    if (scores && weight_blocks(pairs, (int64_t)s.max_pages_per_seq * kPage) > INT32_MAX)
         return PKV_ERR_UNSUPPORTED;
     const int NT = prm.G <= 8 ? 1 : 2;
     const bool pdl = (pl.flags & PKV_FLAG_NO_PDL) == 0;
@@ -3393,6 +3146,23 @@ int paged_decode_impl(const void *q, const void *k_pool, const void *v_pool, con
                             ? launch_ex(merge_kernel<128>, (unsigned)pairs, kMergeThreads, 0, st, pdl, prm)
                             : launch_ex(merge_kernel<64>, (unsigned)pairs, kMergeThreads, 0, st, pdl, prm);
         if (e != cudaSuccess || cudaGetLastError() != cudaSuccess)
+            return PKV_ERR_CUDA;
+    }
+    if (scores) {
+        WeightParams w{};
+        w.logits = prm.logits;
+        w.m = prm.ws_m;
+        w.l = prm.ws_l;
+        w.slot_range = prm.slot_range;
+        w.seq_lens = seq_lens;
+        w.scores = scores->scores;
+        w.stride_row = scores->stride_row;
+        w.stride_head = scores->stride_head;
+        w.H_kv = s.H_kv;
+        w.G = prm.G;
+        w.capacity = (int64_t)s.max_pages_per_seq * kPage;
+        w.n_slots = ws.n_slots;
+        if (launch_add_weights(w, pairs, st, pdl) != cudaSuccess)
             return PKV_ERR_CUDA;
     }
     return PKV_OK;
@@ -3429,6 +3199,17 @@ __attribute__((visibility("default"))) int pkv_trace_read(void *host, size_t byt
     return cudaMemcpyFromSymbol(host, g_pkv_trace_buf, bytes) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 #endif
+
+int pkv_paged_decode_scored(const void *q, const void *k_pool, const void *v_pool, const int32_t *block_table,
+                            const int32_t *seq_lens, int32_t page_size, float scale, void *out, float *scores,
+                            int64_t score_stride_row, int64_t score_stride_head, const pkv_shape *shape,
+                            const pkv_plan *plan, const pkv_work_item *items, const int32_t *indptr, int32_t n_items,
+                            void *workspace, size_t workspace_bytes, void *stream)
+{
+    const ScoreArgs sc{scores, score_stride_row, score_stride_head};
+    return paged_decode_impl(q, k_pool, v_pool, block_table, seq_lens, page_size, scale, out, shape, plan, items,
+                             indptr, n_items, workspace, workspace_bytes, (cudaStream_t)stream, nullptr, 0, &sc);
+}
 
 int pkv_build_balanced_queue_device(const int32_t *seq_lens, const pkv_shape *shape, int32_t n_blocks,
                                     pkv_work_item *items, int32_t capacity, int32_t *indptr, void *workspace,

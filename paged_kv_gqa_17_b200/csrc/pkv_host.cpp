@@ -439,6 +439,8 @@ int pkv_plan_counters(const int32_t *seq_lens_host, const pkv_shape *shape, cons
     default:
         return PKV_ERR_INVALID;
     }
+    if (plan->flags & PKV_FLAG_SCORES)
+        ++out.launches;  // the weights kernel
     out.kv_bytes = tokens * H_kv * 2 * D * 2;
     out.kv_bytes_streamed = pages * P * H_kv * 2 * D * 2;
     out.q_bytes = B * shape->H_q * D * 2;

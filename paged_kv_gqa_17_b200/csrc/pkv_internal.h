@@ -30,9 +30,15 @@ struct WsLayout {
     size_t m_off = 0;        // float m[slot][G]  (running max, log2 domain)
     size_t l_off = 0;        // float l[slot][G]
     size_t acc_off = 0;      // float acc[slot][G][D]
+    size_t range_off = 0;    // PKV_FLAG_SCORES: {first slot, slots} per pair
+    size_t logits_off = 0;   // PKV_FLAG_SCORES: float logits[pair][max_pages * P][logit_heads(G)]
     size_t total = 0;
     int64_t n_slots = 0;
 };
+
+// Heads a token's stored logits are laid out for: G rounded up to even, so
+// that two heads' logits are one aligned 8-byte store.
+inline int32_t logit_heads(int64_t G) { return (int32_t)((G + 1) & ~int64_t(1)); }
 
 inline WsLayout ws_layout(const pkv_shape &s, const pkv_plan &p, int32_t n_items)
 {
@@ -43,6 +49,9 @@ inline WsLayout ws_layout(const pkv_shape &s, const pkv_plan &p, int32_t n_items
         w.n_slots = pairs * p.num_splits;
     else if (p.mode == PKV_WORK_QUEUE || p.mode == PKV_BALANCED)
         w.n_slots = n_items;
+    const bool scores = (p.flags & PKV_FLAG_SCORES) != 0;
+    if (scores && p.mode == PKV_NO_SPLIT)
+        w.n_slots = pairs;  // every pair's final state is read back for its weights
     size_t off = kWsAlign;  // error word section
     w.counters_off = off;
     off += round_up((size_t)pairs * 4, kWsAlign);
@@ -52,6 +61,12 @@ inline WsLayout ws_layout(const pkv_shape &s, const pkv_plan &p, int32_t n_items
     off += round_up((size_t)(w.n_slots * G) * 4, kWsAlign);
     w.acc_off = off;
     off += round_up((size_t)(w.n_slots * G * s.head_dim) * 4, kWsAlign);
+    if (scores) {
+        w.range_off = off;
+        off += round_up((size_t)pairs * 8, kWsAlign);
+        w.logits_off = off;
+        off += round_up((size_t)pairs * s.max_pages_per_seq * s.page_size * logit_heads(G) * 4, kWsAlign);
+    }
     w.total = off;
     return w;
 }

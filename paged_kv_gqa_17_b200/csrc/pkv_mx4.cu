@@ -1,0 +1,1363 @@
+// The 4-bit paged cache: tokens quantised into it, read back, and attended.
+//
+// Format.  A value is (-1)^s {0, .5, 1, 1.5, 2, 3, 4, 6}[low three bits]
+// 2^(scale - 127): e2m1 codes under one power-of-two scale (an exponent byte)
+// per 32 dims of a token, 17/64 of bf16's bytes.  A page (16 tokens) of one KV head
+// is one record of 17 D bytes, so that one bulk copy stages it:
+//     K codes [16][D/2], V codes [16][D/2], K scales [16][D/32], V scales [16][D/32].
+// Codes lie in the order in which the tensor-core fragments take them:
+//   - K: dim 32 b + 8 c + j in byte c D/8 + 4 b + j/2 of its row.  Lane (r, c) of
+//     a warp holds row r of K as the MMA's A operand; its D/8 bytes at c D/8 are
+//     eight dims of every scale block, one 16-byte (D = 128) shared load, and a
+//     k-step of 16 dims never mixes two scale blocks;
+//   - V: dim 32 b + 4 r + j in byte r D/16 + 2 b + j/2.  Lane (r, c) holds dims of
+//     row r of V^T for four tokens; the four dims it owns in every block are two
+//     bytes, all blocks together one 8-byte load per token.
+// (j/2 names the byte, its low four bits the even j.)
+#include "pkv_device.h"
+
+#include <algorithm>
+#include <atomic>
+#include <climits>
+#include <cstring>
+
+#include <cuda_fp16.h>
+
+namespace pkv {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Record layout
+
+template <int D>
+struct Rec {
+    static constexpr int kRow = D / 2;        // bytes of a token's codes
+    static constexpr int kScaleRow = D / 32;  // bytes of a token's scales
+    static constexpr int kV = kPage * kRow;
+    static constexpr int kKs = 2 * kPage * kRow;
+    static constexpr int kVs = kKs + kPage * kScaleRow;
+    static constexpr int kBytes = kVs + kPage * kScaleRow;
+    static_assert(kBytes == 17 * D, "record size");
+};
+
+// Two e2m1 codes (a byte) to two halves, exactly; the low four bits to the low half.
+__device__ __forceinline__ void codes_to_half2(uint32_t w, uint32_t (&out)[4])
+{
+    asm("{\n"
+        " .reg .b8 b0, b1, b2, b3;\n"
+        " mov.b32 {b0, b1, b2, b3}, %4;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, b0;\n"
+        " cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, b2;\n"
+        " cvt.rn.f16x2.e2m1x2 %3, b3;\n"
+        "}\n"
+        : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3])
+        : "r"(w));
+}
+
+// Eight floats to eight e2m1 codes, round to nearest even, saturating at 6;
+// x[0] in the lowest four bits.
+__device__ __forceinline__ uint32_t floats_to_codes(const float (&x)[8])
+{
+    uint32_t w;
+    asm("{\n"
+        " .reg .b8 b0, b1, b2, b3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+        " mov.b32 %0, {b0, b1, b2, b3};\n"
+        "}\n"
+        : "=r"(w)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    return w;
+}
+
+// ---------------------------------------------------------------------------
+// Tokens in and out
+
+// Token j of the call belongs to row i with indptr[i] <= j < indptr[i + 1] (to
+// row j without an indptr) and lies at seq_lens[i] + j - indptr[i] there.
+struct TokenMap {
+    const int32_t *block_table;
+    const int32_t *seq_lens;
+    const int32_t *indptr;
+    uint32_t *ws_error;
+    int32_t B, max_pages, num_pool_pages;
+};
+
+// The record of token j (of head 0) and its slot, or NULL: no row's token, or
+// out of its row's pages or the pool (reported).
+__device__ __forceinline__ uint8_t *token_record(const TokenMap &m, uint8_t *pool, int64_t stride_page, int j,
+                                                 bool report, int &slot)
+{
+    int row = j;
+    int64_t at;
+    if (m.indptr) {
+        int lo = 0, hi = m.B;  // the last row with indptr <= j
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (__ldg(m.indptr + mid) <= j)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        row = lo;
+        const int begin = __ldg(m.indptr + row);
+        if (j < begin || j >= __ldg(m.indptr + row + 1))
+            return nullptr;  // behind the last row's tokens
+        at = (int64_t)__ldg(m.seq_lens + row) + j - begin;
+    } else {
+        at = __ldg(m.seq_lens + row);
+    }
+    if (at < 0 || at >= (int64_t)m.max_pages * kPage) {
+        if (report)
+            atomicOr(m.ws_error, kErrSeqLen);
+        return nullptr;
+    }
+    const int page = __ldg(m.block_table + (int64_t)row * m.max_pages + at / kPage);
+    if (page < 0 || page >= m.num_pool_pages) {
+        if (report)
+            atomicOr(m.ws_error, kErrPageId);
+        return nullptr;
+    }
+    slot = (int)(at % kPage);
+    return pool + (int64_t)page * stride_page;
+}
+
+struct WriteParams {
+    TokenMap map;
+    const __nv_bfloat16 *k, *v;
+    int64_t k_token, k_head, v_token, v_head;  // strides in elements
+    uint8_t *pool;
+    int64_t stride_page, stride_head;
+    int32_t n_tokens, H_kv;
+};
+
+struct ReadParams {
+    TokenMap map;
+    __nv_bfloat16 *k, *v;  // [token][head][D]
+    const uint8_t *pool;
+    int64_t stride_page, stride_head;
+    int32_t n_tokens, H_kv;
+};
+
+constexpr int kTokenThreads = 256;
+
+// Quantises K and V of the new tokens into their slots.  D/8 lanes work on one
+// row (K or V of a token's head), eight dims each: a 16-byte load, the block's
+// largest magnitude by two shuffles among its four lanes, the scale from that
+// magnitude's exponent field (its largest value lands in [4, 8) and saturates
+// at 6), and the products by a power of two, which are exact.  Memory-bound:
+// 4 D bytes in, 17 D / 16 out per token and head.
+template <int D>
+__global__ void __launch_bounds__(kTokenThreads) mx4_write_kernel(const __grid_constant__ WriteParams p)
+{
+    using R = Rec<D>;
+    constexpr int kLanes = D / 8;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t rows = (int64_t)p.n_tokens * p.H_kv * 2;
+    const int sub = threadIdx.x % kLanes;  // b = sub / 4, c = sub % 4
+    const int b = sub >> 2, c = sub & 3;
+    for (int64_t base = (int64_t)blockIdx.x * (kTokenThreads / kLanes); base < rows;
+         base += (int64_t)gridDim.x * (kTokenThreads / kLanes)) {
+        const int64_t at = base + threadIdx.x / kLanes;
+        if (at >= rows)
+            continue;
+        const int is_v = (int)(at & 1);
+        const int head = (int)((at >> 1) % p.H_kv);
+        const int j = (int)((at >> 1) / p.H_kv);
+        const uint32_t lanes = 0xfu << (threadIdx.x & 28);  // the four lanes of this scale block
+        int slot = 0;
+        uint8_t *rec = token_record(p.map, p.pool, p.stride_page, j, sub == 0 && head == 0 && !is_v, slot);
+        const __nv_bfloat16 *src = is_v ? p.v + j * p.v_token + head * p.v_head : p.k + j * p.k_token + head * p.k_head;
+        const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(src) + sub);
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        float x[8];
+        uint32_t amax = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            // magnitudes order like their bits, infinities and NaN above every number
+            amax = max(amax, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+        }
+        amax = max(amax, __shfl_xor_sync(lanes, amax, 1));
+        amax = max(amax, __shfl_xor_sync(lanes, amax, 2));
+        int scale = max((int)(amax >> 23) - 2, 1);
+        float mul = __uint_as_float((uint32_t)(254 - scale) << 23);  // 2^(127 - scale)
+        if (amax == 0)
+            scale = 0;
+        const bool bad = amax >= 0x7f800000u;  // the block reads back as NaN
+        if (bad) {
+            scale = 255;
+            mul = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = bad ? 0.f : x[i] * mul;
+        const uint32_t codes = floats_to_codes(x);
+        if (!rec)
+            continue;
+        rec += (int64_t)head * p.stride_head;
+        if (is_v) {
+            uint8_t *row = rec + R::kV + slot * R::kRow + 2 * b;
+            *reinterpret_cast<uint16_t *>(row + (2 * c) * (D / 16)) = (uint16_t)codes;
+            *reinterpret_cast<uint16_t *>(row + (2 * c + 1) * (D / 16)) = (uint16_t)(codes >> 16);
+        } else {
+            *reinterpret_cast<uint32_t *>(rec + slot * R::kRow + c * (D / 8) + 4 * b) = codes;
+        }
+        if (c == 0)
+            rec[(is_v ? R::kVs : R::kKs) + slot * R::kScaleRow + b] = (uint8_t)scale;
+    }
+}
+
+// A scale byte's value: 2^(s - 127), NaN for 255.
+__device__ __forceinline__ float scale_value(uint32_t s)
+{
+    return __uint_as_float(s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23);
+}
+
+// The stored values as bf16, exactly (e2m1 has two significant bits).  Lanes
+// as in mx4_write_kernel.
+template <int D>
+__global__ void __launch_bounds__(kTokenThreads) mx4_read_kernel(const __grid_constant__ ReadParams p)
+{
+    using R = Rec<D>;
+    constexpr int kLanes = D / 8;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t rows = (int64_t)p.n_tokens * p.H_kv * 2;
+    const int sub = threadIdx.x % kLanes;
+    const int b = sub >> 2, c = sub & 3;
+    for (int64_t base = (int64_t)blockIdx.x * (kTokenThreads / kLanes); base < rows;
+         base += (int64_t)gridDim.x * (kTokenThreads / kLanes)) {
+        const int64_t at = base + threadIdx.x / kLanes;
+        if (at >= rows)
+            continue;
+        const int is_v = (int)(at & 1);
+        const int head = (int)((at >> 1) % p.H_kv);
+        const int j = (int)((at >> 1) / p.H_kv);
+        int slot = 0;
+        const uint8_t *rec = token_record(p.map, const_cast<uint8_t *>(p.pool), p.stride_page, j,
+                                          sub == 0 && head == 0 && !is_v, slot);
+        __nv_bfloat16 *dst = (is_v ? p.v : p.k) + ((int64_t)j * p.H_kv + head) * D;
+        if (!rec) {
+            reinterpret_cast<uint4 *>(dst)[sub] = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        rec += (int64_t)head * p.stride_head;
+        uint32_t codes;
+        if (is_v) {
+            const uint8_t *row = rec + R::kV + slot * R::kRow + 2 * b;
+            codes = *reinterpret_cast<const uint16_t *>(row + (2 * c) * (D / 16)) |
+                    (uint32_t) * reinterpret_cast<const uint16_t *>(row + (2 * c + 1) * (D / 16)) << 16;
+        } else {
+            codes = *reinterpret_cast<const uint32_t *>(rec + slot * R::kRow + c * (D / 8) + 4 * b);
+        }
+        const float s = scale_value(rec[(is_v ? R::kVs : R::kKs) + slot * R::kScaleRow + b]);
+        uint32_t h[4], o[4];
+        codes_to_half2(codes, h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+            o[i] = pack_bf16(f.x * s, f.y * s);
+        }
+        reinterpret_cast<uint4 *>(dst)[sub] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Decode
+//
+// The (row, KV head) pairs' pages lie end to end, ceil(N_i / 16) per pair; of
+// the U pages in all, block b of T owns [floor(b U / T), floor((b + 1) U / T)) and
+// its eight warps split that share the same way, so every warp streams a
+// contiguous run of pages, through as many pairs as it takes, and derives it
+// from the device lengths alone: one plan, or one captured graph, serves any
+// lengths.
+//
+// A warp stages its pages itself: each page is one bulk copy (17 D bytes) into
+// the warp's own ring, completion on an mbarrier, so warps never wait for one
+// another while they stream.  Per page:
+//   - S^T = K q^T by mma.sync m16n8k16 on f16 (tokens x heads): e2m1 is exact in f16,
+//     q is scaled to f16 by a power of two per head (bf16's eight bits fit).
+//     Each scale block's partial products, two k-steps, are multiplied by their
+//     tokens' scales in fp32;
+//   - the softmax runs in the log2 domain against a reference max that moves
+//     only when a logit exceeds it (a warp vote), which after the first pages
+//     is rare, so most pages need no shuffles and no rescaling;
+//   - O^T += V^T P^T: V's scale multiplies P per block of 32 dims, as an exact power of
+//     two on packed halves.  Halves cover 2^-24 .. 2^15, so a block's scales are
+//     taken relative to a reference exponent; pages whose scales leave the
+//     eight steps below it take the same product in bf16, whose exponents
+//     reach everywhere.
+// A pair within one warp's run is finished by the warp; a pair that spans warps
+// is merged in shared memory, one that spans blocks by the last block to
+// finish it (an atomic ticket), in ascending order: results are deterministic.
+
+constexpr int kWarps = 8;
+constexpr int kDecodeThreads = kWarps * 32;
+constexpr int kMaxRows = 4096;       // rows whose page offsets a block keeps in shared memory
+constexpr int kMinBlockPages = 8;    // a share below a page per warp only adds states to merge
+constexpr int kMaxBlocks = 1024;     // a merge keeps a weight per block and head in shared memory
+constexpr float kPShift = 15.f;      // P is held times 2^15: the top of f16's range
+
+struct DecodeParams {
+    const __nv_bfloat16 *q;
+    __nv_bfloat16 *out;
+    const uint8_t *pool;
+    int64_t stride_page, stride_head;
+    const int32_t *block_table;
+    const int32_t *seq_lens;
+    float *ws_m, *ws_l, *ws_acc;  // [2 T][G], [2 T][G], [2 T][G][D]: a block's first and last unfinished pair
+    uint32_t *ws_counters;        // tickets per pair
+    uint32_t *ws_error;
+    float *logits, *fin_m, *fin_l;  // scored decode: logits, and every pair's final state
+    float scale_log2;
+    int32_t B, H_q, H_kv, G, max_pages, num_pool_pages, blocks;
+};
+
+template <int D, int NT>
+struct DCfg {
+    static constexpr int kHeads = 8 * NT;
+    static constexpr int kState = kHeads * (D + 4) + 2 * kHeads;  // floats: o (rows padded), m, l
+    static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kWarpRing = kStages * Rec<D>::kBytes;
+    static_assert(kState * 4 <= kWarpRing, "a warp's last state takes the place of its ring");
+    static constexpr int kFirstOff = kWarps * kWarpRing;  // the states of the warps' first runs
+    static constexpr int kBarOff = kFirstOff + kWarps * kState * 4;
+    static constexpr int kPairOff = kBarOff + kWarps * kStages * 8;  // pair of each of the 2 kWarps states
+    static constexpr int kMiscOff = kPairOff + 2 * kWarps * 4;
+    static constexpr int kScanOff = kMiscOff + 32;
+    static constexpr int kPrefixOff = kScanOff + 64;  // int32 [B + 1]
+    static constexpr int kPerSM = NT == 1 ? 2 : 1;
+    static_assert((kMaxBlocks * kHeads + 4 + 16 + 4 * kDecodeThreads) * 4 <= kBarOff, "a merge's weights and partial sums");
+    static_assert(kWarpRing % 16 == 0 && kBarOff % 8 == 0, "alignment of the copies and their barriers");
+};
+
+__device__ __forceinline__ int64_t share_begin(int64_t U, int64_t T, int64_t b) { return b * U / T; }
+
+// The block whose share holds page u.
+__device__ __forceinline__ int64_t share_of(int64_t U, int64_t T, int64_t u)
+{
+    int64_t b = u * T / U;
+    while (share_begin(U, T, b + 1) <= u)
+        ++b;
+    while (share_begin(U, T, b) > u)
+        --b;
+    return b;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
+{
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// A warp's running state for one pair: heads 8 nt + 2 c + {0, 1}.  o is in units of
+// 2^(vref[b] - 142) for its block b of 32 dims, l in units of 2^-15.
+template <int D, int NT>
+struct State {
+    uint32_t qf[D / 16][NT][2];  // q as the MMA's B operand
+    float sl[NT][2];             // logit = product * sl (log2 domain)
+    float m[NT][2], l[NT][2];
+    float o[D / 16][NT][4];
+    int vref[D / 32];            // top of the window of V's scales, -1: none yet
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void load_q(const DecodeParams &p, int pair, int lane, State<D, NT> &st)
+{
+    const int r = lane >> 2, c = lane & 3;
+    const int row = pair / p.H_kv, h = pair % p.H_kv;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int g = nt * 8 + r;
+        uint4 raw[D / 32];
+        uint32_t amax = 0;
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b) {
+            raw[b] = make_uint4(0, 0, 0, 0);
+            if (g < p.G)
+                raw[b] = __ldg(reinterpret_cast<const uint4 *>(
+                                   p.q + ((int64_t)row * p.H_q + (int64_t)h * p.G + g) * D + 32 * b) + c);
+            const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                amax = max(amax, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+        }
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // the largest element to [2^13, 2^14): 2^up and its inverse stay normal floats for |up| <= 126
+        const int e = (int)(amax >> 23);
+        const int up = e == 0 || e == 255 ? 0 : min(126, 13 + 127 - e);
+        const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b) {
+            const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+            uint32_t f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                f[i] = pack_f16(__uint_as_float(w[i] << 16) * mul, __uint_as_float(w[i] & 0xffff0000u) * mul);
+            st.qf[2 * b][nt][0] = f[0];
+            st.qf[2 * b][nt][1] = f[1];
+            st.qf[2 * b + 1][nt][0] = f[2];
+            st.qf[2 * b + 1][nt][1] = f[3];
+        }
+        const float inv = p.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
+        st.sl[nt][0] = __shfl_sync(0xffffffffu, inv, 8 * c);
+        st.sl[nt][1] = __shfl_sync(0xffffffffu, inv, 8 * c + 4);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        st.m[nt][0] = st.m[nt][1] = -INFINITY;
+        st.l[nt][0] = st.l[nt][1] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt)
+            st.o[mt][nt][0] = st.o[mt][nt][1] = st.o[mt][nt][2] = st.o[mt][nt][3] = 0.f;
+    }
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+        st.vref[b] = -1;
+}
+
+// Byte b of w as a float's exponent field: 2^(byte - 127), 0 for 0, infinity for 255.
+__device__ __forceinline__ float exponent_float(uint32_t w, int b)
+{
+    const uint32_t at = b == 0 ? w << 23 : b == 1 ? w << 15 : b == 2 ? w << 7 : w >> 1;
+    return __uint_as_float(at & 0x7f800000u);
+}
+
+// Codes of two tokens, interleaved for the tensor cores: nibble pairs (token
+// a's, token b's) of the even dims and of the odd dims.
+__device__ __forceinline__ void interleave(uint32_t a, uint32_t b, uint32_t &even, uint32_t &odd)
+{
+    even = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
+    odd = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+}
+
+// One page in shared memory (rec) into the state.  `release` runs once the
+// record has been read.
+template <int D, int NT, bool SCORED, typename F>
+__device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, int lane, State<D, NT> &st,
+                                              float *logits, int logit_heads, F release)
+{
+    using R = Rec<D>;
+    constexpr int kBlocks = D / 32;
+    const int r = lane >> 2, c = lane & 3;
+    // K codes of tokens r and r + 8, V codes of tokens 2c, 2c + 1, 2c + 8, 2c + 9, their scales
+    uint32_t ka[kBlocks], kb[kBlocks], vw[4][kBlocks / 2], ksa, ksb, vs[4];
+    const int vt[4] = {2 * c, 2 * c + 1, 2 * c + 8, 2 * c + 9};
+    if constexpr (D == 128) {
+        const uint4 a4 = *reinterpret_cast<const uint4 *>(rec + r * R::kRow + c * 16);
+        const uint4 b4 = *reinterpret_cast<const uint4 *>(rec + (r + 8) * R::kRow + c * 16);
+        ka[0] = a4.x, ka[1] = a4.y, ka[2] = a4.z, ka[3] = a4.w;
+        kb[0] = b4.x, kb[1] = b4.y, kb[2] = b4.z, kb[3] = b4.w;
+        ksa = *reinterpret_cast<const uint32_t *>(rec + R::kKs + r * 4);
+        ksb = *reinterpret_cast<const uint32_t *>(rec + R::kKs + (r + 8) * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint2 v2 = *reinterpret_cast<const uint2 *>(rec + R::kV + vt[i] * R::kRow + r * 8);
+            vw[i][0] = v2.x, vw[i][1] = v2.y;
+            vs[i] = *reinterpret_cast<const uint32_t *>(rec + R::kVs + vt[i] * 4);
+        }
+    } else {
+        const uint2 a2 = *reinterpret_cast<const uint2 *>(rec + r * R::kRow + c * 8);
+        const uint2 b2 = *reinterpret_cast<const uint2 *>(rec + (r + 8) * R::kRow + c * 8);
+        ka[0] = a2.x, ka[1] = a2.y;
+        kb[0] = b2.x, kb[1] = b2.y;
+        ksa = *reinterpret_cast<const uint16_t *>(rec + R::kKs + r * 2);
+        ksb = *reinterpret_cast<const uint16_t *>(rec + R::kKs + (r + 8) * 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            vw[i][0] = *reinterpret_cast<const uint32_t *>(rec + R::kV + vt[i] * R::kRow + r * 4);
+            vs[i] = *reinterpret_cast<const uint16_t *>(rec + R::kVs + vt[i] * 2);
+        }
+    }
+    release();
+
+    // ---- S^T = K q^T, each block of 32 dims under its tokens' scales ----
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+        uint32_t fa[4], fb[4];
+        codes_to_half2(ka[b], fa);
+        codes_to_half2(kb[b], fb);
+        const float sa = exponent_float(ksa, b), sb = exponent_float(ksb, b);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_f16(part, fa[0], fb[0], fa[1], fb[1], st.qf[2 * b][nt][0], st.qf[2 * b][nt][1]);
+            mma_f16(part, fa[2], fb[2], fa[3], fb[3], st.qf[2 * b + 1][nt][0], st.qf[2 * b + 1][nt][1]);
+            s[nt][0] = fmaf(part[0], sa, s[nt][0]);
+            s[nt][1] = fmaf(part[1], sa, s[nt][1]);
+            s[nt][2] = fmaf(part[2], sb, s[nt][2]);
+            s[nt][3] = fmaf(part[3], sb, s[nt][3]);
+        }
+    }
+
+    // ---- softmax against the reference max ----
+    const bool lo_ok = r < nvalid, hi_ok = r + 8 < nvalid;
+    bool above = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // an infinite product comes of a NaN scale (255): + 0 * s makes it NaN
+            const float x = fmaf(s[nt][i], 0.f, s[nt][i] * st.sl[nt][i & 1]);
+            s[nt][i] = (i < 2 ? lo_ok : hi_ok) ? x : -INFINITY;
+            above |= s[nt][i] > st.m[nt][i & 1];
+        }
+        if constexpr (SCORED) {
+            const int g = 8 * nt + 2 * c;
+            if (g < logit_heads) {
+                if (lo_ok)
+                    *reinterpret_cast<float2 *>(logits + r * logit_heads + g) = make_float2(s[nt][0], s[nt][1]);
+                if (hi_ok)
+                    *reinterpret_cast<float2 *>(logits + (r + 8) * logit_heads + g) = make_float2(s[nt][2], s[nt][3]);
+            }
+        }
+    }
+    if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float mx = fmaxf(s[nt][j], s[nt][2 + j]);
+#pragma unroll
+                for (int sh = 4; sh < 32; sh <<= 1)
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+                const float mn = fmaxf(st.m[nt][j], mx);
+                const float al = mn == -INFINITY ? 1.f : exp2_approx(st.m[nt][j] - mn);
+                st.m[nt][j] = mn;
+                st.l[nt][j] *= al;
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt) {
+                    st.o[mt][nt][j] *= al;
+                    st.o[mt][nt][2 + j] *= al;
+                }
+            }
+    }
+    float pr[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float base = (st.m[nt][j] == -INFINITY ? 0.f : st.m[nt][j]) - kPShift;
+            pr[nt][j] = exp2_approx(s[nt][j] - base);
+            pr[nt][2 + j] = exp2_approx(s[nt][2 + j] - base);
+            st.l[nt][j] += pr[nt][j] + pr[nt][2 + j];
+        }
+
+    // ---- O^T += V^T (P V-scale)^T ----
+    if (st.vref[0] < 0) {
+        // the pair's first page sets each block's window: two steps above its largest scale
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            int top = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = (vs[i] >> (8 * b)) & 255;
+                if (vt[i] < nvalid && e < 255)
+                    top = max(top, e);
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            st.vref[b] = min(top + 2, 254);
+        }
+    }
+    // every valid token's scales within [vref - 7, vref]?
+    uint32_t out_of = 0;
+    uint32_t d[4][kBlocks / 2];  // scale - (vref - 7), blocks b and b + kBlocks / 2... in 16-bit halves
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int b = 0; b < kBlocks / 2; ++b) {
+            // halves: D = 128: blocks b and b + 2; D = 64: blocks 0 and 1
+            const uint32_t pairw = D == 128 ? (vs[i] >> (8 * b)) & 0x00ff00ffu
+                                            : (vs[i] & 255u) | (vs[i] & 0xff00u) << 8;
+            const int second = D == 128 ? b + 2 : 1;
+            const uint32_t low = (uint32_t)(st.vref[b] - 7) + ((uint32_t)(st.vref[second] - 7) << 16);
+            d[i][b] = pairw - low;
+            if (vt[i] >= nvalid)
+                d[i][b] = 0;
+            out_of |= d[i][b];
+        }
+    uint32_t ve[2][kBlocks / 2], vo[2][kBlocks / 2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int w = 0; w < kBlocks / 2; ++w)
+            interleave(vw[2 * t][w], vw[2 * t + 1][w], ve[t][w], vo[t][w]);
+    if (!__any_sync(0xffffffffu, (out_of & 0xfff8fff8u) != 0)) {
+        uint32_t pt[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            pt[nt][0] = movmatrix_trans(pack_f16(pr[nt][0], pr[nt][1]));
+            pt[nt][1] = movmatrix_trans(pack_f16(pr[nt][2], pr[nt][3]));
+        }
+#pragma unroll
+        for (int w = 0; w < kBlocks / 2; ++w) {
+            uint32_t e0[4], o0[4], e1[4], o1[4];
+            codes_to_half2(ve[0][w], e0);
+            codes_to_half2(vo[0][w], o0);
+            codes_to_half2(ve[1][w], e1);
+            codes_to_half2(vo[1][w], o1);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {  // blocks 2 w and 2 w + 1
+                const int b = 2 * w + k;
+                // tokens' steps of block b side by side, then 2^(step - 7) as two halves
+                const int dw = D == 128 ? b & 1 : 0, hi = D == 128 ? b >> 1 : b;
+                const uint32_t sel = hi ? 0x7632 : 0x5410;
+                const uint32_t f0 = __byte_perm(d[0][dw], d[1][dw], sel) * 0x400u + 0x20002000u;
+                const uint32_t f1 = __byte_perm(d[2][dw], d[3][dw], sel) * 0x400u + 0x20002000u;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint32_t p0 = mul_f16x2(pt[nt][0], f0), p1 = mul_f16x2(pt[nt][1], f1);
+                    mma_f16(st.o[2 * b][nt], e0[2 * k], o0[2 * k], e1[2 * k], o1[2 * k], p0, p1);
+                    mma_f16(st.o[2 * b + 1][nt], e0[2 * k + 1], o0[2 * k + 1], e1[2 * k + 1], o1[2 * k + 1], p0, p1);
+                }
+            }
+        }
+        return;
+    }
+    // Some scale lies outside its window.  A larger one moves the window up;
+    // then bf16 takes the product: e2m1 as f16 bits shifted down by three is
+    // the same value times 2^-112 in bf16, and P 2^(scale - vref + 127) undoes that.
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+        int top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = (vs[i] >> (8 * b)) & 255;
+            if (vt[i] < nvalid && e < 255)
+                top = max(top, e);
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        if (top > st.vref[b]) {
+            const int up = top - st.vref[b];  // 1 .. 254
+            const float f = up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    st.o[2 * b][nt][i] *= f;
+                    st.o[2 * b + 1][nt][i] *= f;
+                }
+            st.vref[b] = top;
+        }
+    }
+    // this lane's rows of P are tokens r and r + 8: their scales, from a lane that holds them
+    const uint32_t even_lo = __shfl_sync(0xffffffffu, vs[0], r >> 1), odd_lo = __shfl_sync(0xffffffffu, vs[1], r >> 1);
+    const uint32_t even_hi = __shfl_sync(0xffffffffu, vs[2], r >> 1), odd_hi = __shfl_sync(0xffffffffu, vs[3], r >> 1);
+    const uint32_t vs_lo = r & 1 ? odd_lo : even_lo, vs_hi = r & 1 ? odd_hi : even_hi;
+#pragma unroll
+    for (int w = 0; w < kBlocks / 2; ++w) {
+        uint32_t a[4][4];
+        codes_to_half2(ve[0][w], a[0]);
+        codes_to_half2(vo[0][w], a[1]);
+        codes_to_half2(ve[1][w], a[2]);
+        codes_to_half2(vo[1][w], a[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                a[i][k] = (a[i][k] & 0x80008000u) | ((a[i][k] >> 3) & 0x0fff0fffu);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int b = 2 * w + k;
+            auto factor = [&](uint32_t e, bool ok) {
+                const int x = (int)e - st.vref[b] + 254;
+                return !ok || x <= 0 || e == 0u ? 0.f
+                       : e == 255u              ? __uint_as_float(0x7fc00000u)
+                                                : __uint_as_float((uint32_t)x << 23);
+            };
+            const float f0 = factor((vs_lo >> (8 * b)) & 255u, lo_ok), f1 = factor((vs_hi >> (8 * b)) & 255u, hi_ok);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                // P holds 2^15 too much for bf16's top: 2^-15 first, then the factor
+                const float q0 = pr[nt][0] * 0x1p-15f * f0, q1 = pr[nt][1] * 0x1p-15f * f0;
+                const float q2 = pr[nt][2] * 0x1p-15f * f1, q3 = pr[nt][3] * 0x1p-15f * f1;
+                const uint32_t p0 = movmatrix_trans(pack_bf16(q0, q1)), p1 = movmatrix_trans(pack_bf16(q2, q3));
+                mma_bf16(st.o[2 * b][nt], a[0][2 * k], a[1][2 * k], a[2][2 * k], a[3][2 * k], p0, p1);
+                mma_bf16(st.o[2 * b + 1][nt], a[0][2 * k + 1], a[1][2 * k + 1], a[2][2 * k + 1], a[3][2 * k + 1], p0,
+                         p1);
+            }
+        }
+    }
+}
+
+// A warp's finished state to shared memory, in true units: o [head][D + 4], m, l per head.
+template <int D, int NT>
+__device__ __forceinline__ void put_state(float *dst, int lane, const State<D, NT> &st)
+{
+    using C = DCfg<D, NT>;
+    const int r = lane >> 2, c = lane & 3;
+    float *dm = dst + C::kHeads * (D + 4), *dl = dm + C::kHeads;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int g = nt * 8 + 2 * c + j;
+            float l = st.l[nt][j];
+#pragma unroll
+            for (int sh = 4; sh < 32; sh <<= 1)
+                l += __shfl_xor_sync(0xffffffffu, l, sh);
+            if (r == 0) {
+                dm[g] = st.m[nt][j];
+                dl[g] = l * 0x1p-15f;
+            }
+#pragma unroll
+            for (int b = 0; b < D / 32; ++b) {
+                // 2^(vref - 142) in two steps: 2^-15, then the exponent byte itself
+                const float f = __uint_as_float((uint32_t)max(st.vref[b], 1) << 23);
+                *reinterpret_cast<float4 *>(dst + g * (D + 4) + 32 * b + 4 * r) =
+                    make_float4(st.o[2 * b][nt][j] * 0x1p-15f * f, st.o[2 * b][nt][2 + j] * 0x1p-15f * f,
+                                st.o[2 * b + 1][nt][j] * 0x1p-15f * f, st.o[2 * b + 1][nt][2 + j] * 0x1p-15f * f);
+            }
+        }
+}
+
+// The same state of a pair that this warp alone has seen, normalised and written out.
+template <int D, int NT, bool SCORED>
+__device__ __forceinline__ void write_pair(const DecodeParams &p, int pair, int lane, const State<D, NT> &st)
+{
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int g = nt * 8 + 2 * c + j;
+            float l = st.l[nt][j];
+#pragma unroll
+            for (int sh = 4; sh < 32; sh <<= 1)
+                l += __shfl_xor_sync(0xffffffffu, l, sh);
+            if (g >= p.G)
+                continue;
+            l *= 0x1p-15f;
+            const float inv = (l == 0.f ? 0.f : 1.f / l) * 0x1p-15f;
+            __nv_bfloat16 *dst = p.out + ((int64_t)pair * p.G + g) * D;
+#pragma unroll
+            for (int b = 0; b < D / 32; ++b) {
+                const float f = __uint_as_float((uint32_t)max(st.vref[b], 1) << 23);
+                store_bf16x4(dst + 32 * b + 4 * r,
+                             make_float4(st.o[2 * b][nt][j] * inv * f, st.o[2 * b][nt][2 + j] * inv * f,
+                                         st.o[2 * b + 1][nt][j] * inv * f, st.o[2 * b + 1][nt][2 + j] * inv * f));
+            }
+            if (SCORED && r == 0) {
+                p.fin_m[(int64_t)pair * p.G + g] = st.m[nt][j];
+                p.fin_l[(int64_t)pair * p.G + g] = l;
+            }
+        }
+}
+
+// Where a page of the grid's page line lies.
+struct Page {
+    int pair;   // row * H_kv + head
+    int index;  // page of its row
+    int pages;  // pages its row has
+    int phys;   // pool page
+    int len;    // its row's tokens
+};
+
+template <int D, int NT, bool SCORED>
+__global__ void __launch_bounds__(kDecodeThreads, (DCfg<D, NT>::kPerSM)) mx4_decode_kernel(const __grid_constant__ DecodeParams p)
+{
+    using C = DCfg<D, NT>;
+    using R = Rec<D>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    int32_t *state_pair = reinterpret_cast<int32_t *>(smem + C::kPairOff);
+    volatile int32_t *misc = reinterpret_cast<volatile int32_t *>(smem + C::kMiscOff);
+    int32_t *scan = reinterpret_cast<int32_t *>(smem + C::kScanOff);
+    int32_t *prefix = reinterpret_cast<int32_t *>(smem + C::kPrefixOff);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t capacity = (int64_t)p.max_pages * kPage;
+    uint8_t *ring = smem + warp * C::kStages * R::kBytes;
+    const uint32_t ring_addr = smem_addr(ring);
+    const uint32_t bars = smem_addr(smem + C::kBarOff) + warp * C::kStages * 8;
+    if (lane == 0) {
+        for (int s = 0; s < C::kStages; ++s)
+            mbar_init(bars + 8 * s, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async_smem();
+    }
+    if (tid < 2 * kWarps)
+        state_pair[tid] = -1;
+    grid_dependency_wait();
+
+    // ---- page offsets of the rows ----
+    auto row_len = [&](int row, bool report) {
+        const int n = __ldg(p.seq_lens + row);
+        if (n >= 0 && n <= capacity)
+            return n;
+        if (report)
+            atomicOr(p.ws_error, kErrSeqLen);
+        return n < 0 ? 0 : (int)capacity;
+    };
+    if (tid == 0)
+        prefix[0] = 0;
+    int carry = 0;
+    for (int base = 0; base < p.B; base += kDecodeThreads) {
+        const int row = base + tid;
+        int v = row < p.B ? (row_len(row, blockIdx.x == 0) + kPage - 1) / kPage : 0;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o)
+                v += up;
+        }
+        if (lane == 31)
+            scan[warp] = v;
+        __syncthreads();
+        int add = carry;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp)
+                add += scan[w];
+            carry += scan[w];
+        }
+        if (row < p.B)
+            prefix[row + 1] = v + add;
+        __syncthreads();
+    }
+    const int64_t U = (int64_t)prefix[p.B] * p.H_kv;
+    // rows without tokens have no pages: their zeros are dealt out by row
+    for (int row = blockIdx.x; row < p.B; row += p.blocks) {
+        if (prefix[row + 1] != prefix[row])
+            continue;
+        uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)row * p.H_q * D);
+        for (int i = tid; i < p.H_q * D / 8; i += kDecodeThreads)
+            dst[i] = make_uint4(0, 0, 0, 0);
+    }
+    const int64_t want = (U + kMinBlockPages - 1) / kMinBlockPages;
+    const int64_t T = want < p.blocks ? (want < 1 ? 1 : want) : p.blocks;
+    if ((int64_t)blockIdx.x >= T || U == 0)
+        return;
+    const int64_t u0 = share_begin(U, T, blockIdx.x), u1 = share_begin(U, T, blockIdx.x + 1);
+    const int64_t w0 = u0 + share_begin(u1 - u0, kWarps, warp), w1 = u0 + share_begin(u1 - u0, kWarps, warp + 1);
+    const int n = (int)(w1 - w0);
+
+    // ---- stream this warp's pages ----
+    auto locate = [&](int64_t u) {
+        Page g{-1, 0, 0, 0, 0};
+        if (u >= w1)
+            return g;
+        int lo = 0, hi = p.B;  // the last row that begins at or before u
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if ((int64_t)prefix[mid] * p.H_kv <= u)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        g.pages = prefix[lo + 1] - prefix[lo];
+        const int in = (int)(u - (int64_t)prefix[lo] * p.H_kv);
+        const int head = in / g.pages;
+        g.index = in - head * g.pages;
+        g.pair = lo * p.H_kv + head;
+        g.len = row_len(lo, false);
+        g.phys = __ldg(p.block_table + (int64_t)lo * p.max_pages + g.index);
+        if (g.phys < 0 || g.phys >= p.num_pool_pages) {
+            atomicOr(p.ws_error, kErrPageId);
+            g.phys = 0;  // read a real page instead; the error bit reports the bad entry
+        }
+        return g;
+    };
+    auto issue = [&](const Page &g, int j) {  // by the lane that holds page j
+        const int s = j % C::kStages;
+        mbar_expect_tx(bars + 8 * s, R::kBytes);
+        bulk_g2s(ring_addr + s * R::kBytes, p.pool + (int64_t)g.phys * p.stride_page + (int64_t)(g.pair % p.H_kv) * p.stride_head,
+                 R::kBytes, bars + 8 * s);
+    };
+    // lane l holds page 32 k + l of batch k: the current batch and the next
+    Page cur = locate(w0 + lane), next = locate(w0 + 32 + lane);
+    __syncwarp();  // the barriers' initialisation
+    if (lane < C::kStages && lane < n)
+        issue(cur, lane);
+
+    // A run that is its whole pair is written out at once; one that the warp's
+    // share cuts becomes a state: the warp's first run beside the rings (in use
+    // until the warp is done), its last one in the warp's own ring.
+    auto state_at = [&](int i) {  // state i = 2 * warp + (0 first, 1 last)
+        return reinterpret_cast<float *>(i & 1 ? smem + (i >> 1) * C::kWarpRing
+                                               : smem + C::kFirstOff + (i >> 1) * C::kState * 4);
+    };
+    State<D, NT> st;
+    int pair = -1, begin = 0, run = 0;  // current pair, its run's first page, the warp's runs so far
+    bool ok = true;
+    auto finish = [&](int end, int pages, bool last) {
+        if (begin == 0 && end == pages) {
+            write_pair<D, NT, SCORED>(p, pair, lane, st);
+        } else {
+            const int i = 2 * warp + (last && run > 1 ? 1 : 0);
+            put_state<D, NT>(state_at(i), lane, st);
+            if (lane == 0)
+                state_pair[i] = pair;
+        }
+    };
+    int end = 0, pages = 0;  // the current run's end (page of its row) and its row's pages
+    for (int j = 0; j < n; ++j) {
+        const int src = j & 31;
+        if (src == 0 && j > 0) {
+            cur = next;
+            next = locate(w0 + j + 32 + lane);
+        }
+        const int g_pair = __shfl_sync(0xffffffffu, cur.pair, src);
+        const int g_index = __shfl_sync(0xffffffffu, cur.index, src);
+        const int g_len = __shfl_sync(0xffffffffu, cur.len, src);
+        if (g_pair != pair) {
+            if (pair >= 0)
+                finish(end, pages, false);
+            pair = g_pair;
+            begin = g_index;
+            ++run;
+            load_q<D, NT>(p, pair, lane, st);
+        }
+        end = g_index + 1;
+        pages = (g_len + kPage - 1) / kPage;
+        const int s = j % C::kStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * s, (j / C::kStages) & 1, p.ws_error));
+        if (!ok) {
+            // give up on the pair, but not before the copies in flight had their time to land
+            for (int k = j + 1; k < min(n, j + C::kStages); ++k)
+                mbar_wait(bars + 8 * (k % C::kStages), (k / C::kStages) & 1, p.ws_error);
+            break;
+        }
+        const int nvalid = min(kPage, g_len - g_index * kPage);
+        float *logits = nullptr;
+        int heads = 0;
+        if constexpr (SCORED) {
+            heads = (p.G + 1) & ~1;
+            logits = p.logits + ((int64_t)pair * capacity + (int64_t)g_index * kPage) * heads;
+        }
+        attend_record<D, NT, SCORED>(ring + s * R::kBytes, nvalid, lane, st, logits, heads, [&]() {
+            __syncwarp();
+            const int k = j + C::kStages;  // the page that takes this one's place
+            if (k < n && lane == (k & 31))
+                issue((k >> 5) == (j >> 5) ? cur : next, k);
+        });
+    }
+    grid_launch_dependents();
+    if (n > 0 && ok)
+        finish(end, pages, true);
+    __syncthreads();
+
+    // ---- merge the states of pairs that the warps share ----
+    constexpr int D4 = D / 4;
+    const int G = p.G;
+    int open[2] = {-1, -1};  // pairs that reach into other blocks
+    for (int i = 0; i < 2 * kWarps;) {
+        const int which = state_pair[i];
+        int next_i = i + 1;
+        if (which < 0) {
+            i = next_i;
+            continue;
+        }
+        while (next_i < 2 * kWarps && (state_pair[next_i] == which || state_pair[next_i] < 0))
+            ++next_i;
+        const int row = which / p.H_kv;
+        const int row_pages = prefix[row + 1] - prefix[row];
+        const int64_t P0 = (int64_t)prefix[row] * p.H_kv + (int64_t)(which % p.H_kv) * row_pages;
+        const bool whole = P0 >= u0 && P0 + row_pages <= u1;
+        const int slot = 2 * blockIdx.x + (P0 > u0 ? 1 : 0);
+        if (!whole)
+            open[P0 > u0 ? 1 : 0] = which;
+        for (int e = tid; e < G * D4; e += kDecodeThreads) {
+            const int g = e / D4, d4 = (e % D4) * 4;
+            float M = -INFINITY, L = 0.f;
+            for (int k = i; k < next_i; ++k)
+                if (state_pair[k] == which)
+                    M = fmaxf(M, state_at(k)[C::kHeads * (D + 4) + g]);
+            const float base = M == -INFINITY ? 0.f : M;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = i; k < next_i; ++k) {
+                if (state_pair[k] != which)
+                    continue;
+                const float *sk = state_at(k);
+                const float w = exp2_approx(sk[C::kHeads * (D + 4) + g] - base);
+                L = fmaf(sk[C::kHeads * (D + 4) + C::kHeads + g], w, L);
+                O = fma4(*reinterpret_cast<const float4 *>(sk + g * (D + 4) + d4), w, O);
+            }
+            if (whole) {
+                store_bf16x4(p.out + ((int64_t)which * G + g) * D + d4, scale4(O, L == 0.f ? 0.f : 1.f / L));
+                if (SCORED && d4 == 0) {
+                    p.fin_m[(int64_t)which * G + g] = M;
+                    p.fin_l[(int64_t)which * G + g] = L;
+                }
+            } else {
+                const int64_t at = (int64_t)slot * G + g;
+                *reinterpret_cast<float4 *>(p.ws_acc + at * D + d4) = O;
+                if (d4 == 0) {
+                    p.ws_m[at] = M;
+                    p.ws_l[at] = L;
+                }
+            }
+        }
+        i = next_i;
+    }
+    if (open[0] < 0 && open[1] < 0)
+        return;
+
+    // ---- pairs that span blocks: the last block to finish one merges its states ----
+    __syncthreads();
+    int64_t first_block[2] = {0, 0};
+    int slots[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (open[k] < 0)
+            continue;
+        const int row = open[k] / p.H_kv;
+        const int row_pages = prefix[row + 1] - prefix[row];
+        const int64_t P0 = (int64_t)prefix[row] * p.H_kv + (int64_t)(open[k] % p.H_kv) * row_pages;
+        first_block[k] = share_of(U, T, P0);
+        slots[k] = (int)(share_of(U, T, P0 + row_pages - 1) - first_block[k]) + 1;
+        first_block[k] = 2 * first_block[k] + (share_begin(U, T, first_block[k]) == P0 ? 0 : 1);  // its slot
+        if (tid == 0)
+            misc[k] = ticket_acq_rel(p.ws_counters + open[k]) == (uint32_t)(slots[k] - 1);
+    }
+    __syncthreads();
+    for (int k = 0; k < 2; ++k) {
+        if (open[k] < 0 || !misc[k])
+            continue;
+        const int which = open[k], count = slots[k];
+        // slot of the i-th state: the pair's first block holds it as its first or last unfinished pair, the
+        // others as their first
+        const int64_t first = first_block[k];
+        auto slot_of = [&](int i) { return i == 0 ? first : 2 * (first / 2 + i); };
+        float *weight = reinterpret_cast<float *>(smem);        // [count][G]
+        float *norm = weight + (count * G + 3) / 4 * 4;         // [16]
+        float *parts = norm + 16;                               // [kDecodeThreads][4], 16-byte aligned
+        for (int g = warp; g < G; g += kWarps) {
+            float M = -INFINITY;
+            for (int i = lane; i < count; i += 32)
+                M = fmaxf(M, p.ws_m[slot_of(i) * G + g]);
+            for (int sh = 16; sh > 0; sh >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
+            const float base = M == -INFINITY ? 0.f : M;
+            float L = 0.f;
+            for (int i = lane; i < count; i += 32) {
+                const int64_t at = slot_of(i) * G + g;
+                const float w = exp2_approx(p.ws_m[at] - base);
+                weight[i * G + g] = w;
+                L = fmaf(p.ws_l[at], w, L);
+            }
+            for (int sh = 16; sh > 0; sh >>= 1)
+                L += __shfl_xor_sync(0xffffffffu, L, sh);
+            if (lane == 0) {
+                norm[g] = L == 0.f ? 0.f : 1.f / L;
+                if (SCORED) {
+                    p.fin_m[(int64_t)which * G + g] = M;
+                    p.fin_l[(int64_t)which * G + g] = L;
+                }
+            }
+        }
+        __syncthreads();
+        // few columns: several threads share one, each over a run of the states
+        const int tasks = G * D4;
+        const int split = tasks < kDecodeThreads ? kDecodeThreads / tasks : 1;
+        for (int e0 = 0; e0 < tasks; e0 += kDecodeThreads) {
+            const int e = split > 1 ? tid % tasks : e0 + tid, part = split > 1 ? tid / tasks : 0;
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (e < tasks && part < split) {
+                const int g = e / D4, d4 = (e % D4) * 4;
+                const int i1 = count * (part + 1) / split;
+#pragma unroll 4
+                for (int i = count * part / split; i < i1; ++i)
+                    O = fma4(__ldcg(reinterpret_cast<const float4 *>(p.ws_acc + (slot_of(i) * G + g) * D + d4)),
+                             weight[i * G + g], O);
+            }
+            if (split > 1) {
+                reinterpret_cast<float4 *>(parts)[tid] = O;
+                __syncthreads();
+                if (part == 0)
+                    for (int k2 = 1; k2 < split; ++k2)
+                        O = fma4(reinterpret_cast<const float4 *>(parts)[k2 * tasks + e], 1.f, O);
+            }
+            if (e < tasks && part == 0)
+                store_bf16x4(p.out + ((int64_t)which * G + e / D4) * D + (e % D4) * 4, scale4(O, norm[e / D4]));
+        }
+        if (tid == 0)
+            p.ws_counters[which] = 0u;  // ready for the next call
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+
+// Workspace of a 4-bit decode plan: the error word, tickets, two states per
+// block and, with PKV_FLAG_SCORES, the pairs' final states and the logits.
+struct Mx4Layout {
+    size_t counters_off, m_off, l_off, acc_off, fin_m_off, fin_l_off, logits_off, total;
+};
+
+Mx4Layout mx4_layout(const pkv_shape &s, const pkv_plan &p)
+{
+    Mx4Layout w{};
+    const size_t pairs = (size_t)s.B * s.H_kv, G = (size_t)(s.H_q / s.H_kv), slots = 2 * (size_t)p.num_splits;
+    size_t off = kWsAlign;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += round_up(bytes, kWsAlign);
+        return at;
+    };
+    w.counters_off = take(pairs * 4);
+    w.m_off = take(slots * G * 4);
+    w.l_off = take(slots * G * 4);
+    w.acc_off = take(slots * G * s.head_dim * 4);
+    if (p.flags & PKV_FLAG_SCORES) {
+        w.fin_m_off = take(pairs * G * 4);
+        w.fin_l_off = take(pairs * G * 4);
+        w.logits_off = take(pairs * s.max_pages_per_seq * s.page_size * logit_heads((int64_t)G) * 4);
+    }
+    w.total = off;
+    return w;
+}
+
+int check_mx4(const pkv_shape &s)
+{
+    if (s.page_size != kPage || (s.head_dim != 64 && s.head_dim != 128))
+        return PKV_ERR_UNSUPPORTED;
+    if (s.kv_stride_page <= 0 || s.kv_stride_head <= 0 || s.kv_stride_page % 16 || s.kv_stride_head % 16)
+        return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+int check_mx4_plan(const pkv_plan *p)
+{
+    if (!p || p->mode != PKV_BALANCED || p->num_splits < 1 || p->chunk_pages != 0)
+        return PKV_ERR_INVALID;
+    if (p->num_splits > kMaxBlocks || (p->flags & ~(PKV_FLAG_SCORES | PKV_FLAG_NO_PDL)))
+        return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+template <int D, int NT, bool SCORED>
+cudaError_t launch_mx4(const DecodeParams &p, cudaStream_t st, bool pdl)
+{
+    using C = DCfg<D, NT>;
+    auto kernel = mx4_decode_kernel<D, NT, SCORED>;
+    const size_t smem = (size_t)C::kPrefixOff + (size_t)(p.B + 1) * 4;
+    static_assert(C::kPrefixOff + (kMaxRows + 1) * 4 <= 227 * 1024, "shared memory of a block");
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess)
+        return e;
+    return launch_kernel(kernel, (unsigned)p.blocks, kDecodeThreads, smem, st, pdl, p);
+}
+
+unsigned token_grid(int64_t rows, int lanes)
+{
+    const int64_t blocks = ceil_div(rows * lanes, kTokenThreads);
+    return (unsigned)std::min<int64_t>(blocks, 148 * 8);
+}
+
+int check_tokens(const pkv_shape *shape, const void *pool, const int32_t *block_table, const int32_t *seq_lens,
+                 const int32_t *indptr, int32_t n_tokens, const void *workspace)
+{
+    if (check_shape(shape) != PKV_OK || n_tokens < 0)
+        return PKV_ERR_INVALID;
+    const int rc = check_mx4(*shape);
+    if (rc != PKV_OK)
+        return rc;
+    if (n_tokens == 0 || shape->B == 0)
+        return n_tokens == 0 ? PKV_OK : PKV_ERR_INVALID;
+    if (!pool || !block_table || !seq_lens || !workspace || shape->max_pages_per_seq < 1 || shape->num_pool_pages < 1 ||
+        (!indptr && n_tokens != shape->B))
+        return PKV_ERR_INVALID;
+    if (!aligned(pool, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(indptr, 4) ||
+        !aligned(workspace, 4))
+        return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+}  // namespace
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+int pkv_mx4_append(const void *k, const void *v, int64_t k_stride_token, int64_t k_stride_head, int64_t v_stride_token,
+                   int64_t v_stride_head, void *pool, const int32_t *block_table, const int32_t *seq_lens,
+                   const int32_t *indptr, int32_t n_tokens, const pkv_shape *shape, void *workspace, void *stream)
+{
+    const int rc = check_tokens(shape, pool, block_table, seq_lens, indptr, n_tokens, workspace);
+    if (rc != PKV_OK || n_tokens == 0)
+        return rc;
+    if (!k || !v)
+        return PKV_ERR_INVALID;
+    if (!aligned(k, 16) || !aligned(v, 16) || (k_stride_token | k_stride_head | v_stride_token | v_stride_head) % 8 ||
+        k_stride_token < 0 || k_stride_head < 0 || v_stride_token < 0 || v_stride_head < 0)
+        return PKV_ERR_UNSUPPORTED;
+    const pkv_shape &s = *shape;
+    WriteParams p{};
+    p.map = {block_table, seq_lens, indptr, static_cast<uint32_t *>(workspace), s.B, s.max_pages_per_seq, s.num_pool_pages};
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    p.k_token = k_stride_token;
+    p.k_head = k_stride_head;
+    p.v_token = v_stride_token;
+    p.v_head = v_stride_head;
+    p.pool = static_cast<uint8_t *>(pool);
+    p.stride_page = s.kv_stride_page;
+    p.stride_head = s.kv_stride_head;
+    p.n_tokens = n_tokens;
+    p.H_kv = s.H_kv;
+    const unsigned grid = token_grid((int64_t)n_tokens * s.H_kv * 2, s.head_dim / 8);
+    const cudaError_t e =
+        s.head_dim == 128 ? launch_kernel(mx4_write_kernel<128>, grid, kTokenThreads, 0, (cudaStream_t)stream, true, p)
+                          : launch_kernel(mx4_write_kernel<64>, grid, kTokenThreads, 0, (cudaStream_t)stream, true, p);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int pkv_mx4_read(const void *pool, const int32_t *block_table, const int32_t *seq_lens, const int32_t *indptr,
+                 int32_t n_tokens, void *k, void *v, const pkv_shape *shape, void *workspace, void *stream)
+{
+    const int rc = check_tokens(shape, pool, block_table, seq_lens, indptr, n_tokens, workspace);
+    if (rc != PKV_OK || n_tokens == 0)
+        return rc;
+    if (!k || !v)
+        return PKV_ERR_INVALID;
+    if (!aligned(k, 16) || !aligned(v, 16))
+        return PKV_ERR_UNSUPPORTED;
+    const pkv_shape &s = *shape;
+    ReadParams p{};
+    p.map = {block_table, seq_lens, indptr, static_cast<uint32_t *>(workspace), s.B, s.max_pages_per_seq, s.num_pool_pages};
+    p.k = static_cast<__nv_bfloat16 *>(k);
+    p.v = static_cast<__nv_bfloat16 *>(v);
+    p.pool = static_cast<const uint8_t *>(pool);
+    p.stride_page = s.kv_stride_page;
+    p.stride_head = s.kv_stride_head;
+    p.n_tokens = n_tokens;
+    p.H_kv = s.H_kv;
+    const unsigned grid = token_grid((int64_t)n_tokens * s.H_kv * 2, s.head_dim / 8);
+    const cudaError_t e =
+        s.head_dim == 128 ? launch_kernel(mx4_read_kernel<128>, grid, kTokenThreads, 0, (cudaStream_t)stream, true, p)
+                          : launch_kernel(mx4_read_kernel<64>, grid, kTokenThreads, 0, (cudaStream_t)stream, true, p);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int pkv_mx4_workspace_bytes(const pkv_shape *shape, const pkv_plan *plan, size_t *bytes)
+{
+    if (!bytes || check_shape(shape) != PKV_OK)
+        return PKV_ERR_INVALID;
+    const int rc = check_mx4_plan(plan);
+    if (rc != PKV_OK)
+        return rc;
+    *bytes = mx4_layout(*shape, *plan).total;
+    return PKV_OK;
+}
+
+int pkv_mx4_decode(const void *q, const void *pool, const int32_t *block_table, const int32_t *seq_lens,
+                   int32_t page_size, float scale, void *out, float *scores, int64_t score_stride_row,
+                   int64_t score_stride_head, const pkv_shape *shape, const pkv_plan *plan, void *workspace,
+                   size_t workspace_bytes, void *stream)
+{
+    if (check_shape(shape) != PKV_OK || page_size != shape->page_size)
+        return PKV_ERR_INVALID;
+    int rc = check_mx4_plan(plan);
+    if (rc != PKV_OK)
+        return rc;
+    const pkv_shape &s = *shape;
+    if ((rc = check_mx4(s)) != PKV_OK)
+        return rc;
+    const int G = s.H_q / s.H_kv;
+    const int64_t pairs = (int64_t)s.B * s.H_kv, capacity = (int64_t)s.max_pages_per_seq * kPage;
+    if (G < 1 || G > 16 || s.B > kMaxRows || pairs * s.max_pages_per_seq > INT32_MAX || capacity > INT32_MAX)
+        return PKV_ERR_UNSUPPORTED;
+    // a plan's scores flag sizes its workspace: it goes with scores, and only with them
+    if (((plan->flags & PKV_FLAG_SCORES) != 0) != (scores != nullptr))
+        return PKV_ERR_UNSUPPORTED;
+    if (s.B == 0)
+        return PKV_OK;
+    if (!q || !pool || !block_table || !seq_lens || !out || !workspace || s.max_pages_per_seq < 1 ||
+        s.num_pool_pages < 1)
+        return PKV_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(pool, 16) || !aligned(block_table, 4) ||
+        !aligned(seq_lens, 4) || !aligned(scores, 4) || !aligned(workspace, 256))
+        return PKV_ERR_UNSUPPORTED;
+    if (scores && weight_blocks(pairs, capacity) > INT32_MAX)
+        return PKV_ERR_UNSUPPORTED;
+    const Mx4Layout w = mx4_layout(s, *plan);
+    if (workspace_bytes < w.total)
+        return PKV_ERR_CAPACITY;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    DecodeParams p{};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.pool = static_cast<const uint8_t *>(pool);
+    p.stride_page = s.kv_stride_page;
+    p.stride_head = s.kv_stride_head;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.ws_error = reinterpret_cast<uint32_t *>(ws);
+    p.ws_counters = reinterpret_cast<uint32_t *>(ws + w.counters_off);
+    p.ws_m = reinterpret_cast<float *>(ws + w.m_off);
+    p.ws_l = reinterpret_cast<float *>(ws + w.l_off);
+    p.ws_acc = reinterpret_cast<float *>(ws + w.acc_off);
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.B = s.B;
+    p.H_q = s.H_q;
+    p.H_kv = s.H_kv;
+    p.G = G;
+    p.max_pages = s.max_pages_per_seq;
+    p.num_pool_pages = s.num_pool_pages;
+    p.blocks = plan->num_splits;
+    if (scores) {
+        p.fin_m = reinterpret_cast<float *>(ws + w.fin_m_off);
+        p.fin_l = reinterpret_cast<float *>(ws + w.fin_l_off);
+        p.logits = reinterpret_cast<float *>(ws + w.logits_off);
+    }
+    const cudaStream_t st = (cudaStream_t)stream;
+    const bool pdl = (plan->flags & PKV_FLAG_NO_PDL) == 0;
+    cudaError_t e;
+    if (s.head_dim == 128)
+        e = G <= 8 ? (scores ? launch_mx4<128, 1, true>(p, st, pdl) : launch_mx4<128, 1, false>(p, st, pdl))
+                   : (scores ? launch_mx4<128, 2, true>(p, st, pdl) : launch_mx4<128, 2, false>(p, st, pdl));
+    else
+        e = G <= 8 ? (scores ? launch_mx4<64, 1, true>(p, st, pdl) : launch_mx4<64, 1, false>(p, st, pdl))
+                   : (scores ? launch_mx4<64, 2, true>(p, st, pdl) : launch_mx4<64, 2, false>(p, st, pdl));
+    if (e != cudaSuccess)
+        return PKV_ERR_CUDA;
+    if (scores) {
+        WeightParams x{};
+        x.logits = p.logits;
+        x.m = p.fin_m;
+        x.l = p.fin_l;
+        x.seq_lens = seq_lens;
+        x.scores = scores;
+        x.stride_row = score_stride_row;
+        x.stride_head = score_stride_head;
+        x.H_kv = s.H_kv;
+        x.G = G;
+        x.capacity = capacity;
+        x.n_slots = pairs;
+        if (launch_add_weights(x, pairs, st, pdl) != cudaSuccess)
+            return PKV_ERR_CUDA;
+    }
+    return PKV_OK;
+}
+
+}  // extern "C"
