@@ -506,7 +506,7 @@ PKV_API int pkv_mx4_read(const void *pool, const int32_t *block_table, const int
                          const pkv_shape *shape, void *workspace, void *stream);
 
 /* Workspace of pkv_mx4_decode for `plan` = {PKV_BALANCED, T, 0, flags}: T
- * blocks (two per SM where G <= 8, else one, fill the GPU), flags 0,
+ * blocks (one per SM fills the GPU; at most 1024), flags 0,
  * PKV_FLAG_SCORES and/or PKV_FLAG_NO_PDL. */
 PKV_API int pkv_mx4_workspace_bytes(const pkv_shape *shape, const pkv_plan *plan, size_t *bytes);
 

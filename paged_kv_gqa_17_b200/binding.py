@@ -879,11 +879,10 @@ class Mx4Plan:
 
 def plan_mx4(shape: Shape, device, scores: bool = False, blocks: Optional[int] = None) -> Mx4Plan:
     """Plan for mx4_append, mx4_read and mx4_decode over mx4_shape(...); scores=True for mx4_decode with scores.
-    `blocks` (default: what fills the GPU, two per SM up to G = 8, else one) is the decode's grid."""
+    `blocks` (default: one per SM, which fills the GPU) is the decode's grid."""
     L = lib()
     if blocks is None:
         blocks = torch.cuda.get_device_properties(device).multi_processor_count
-        blocks *= 2 if shape.H_q <= 8 * shape.H_kv else 1
     plan = Plan(BALANCED, blocks, 0, FLAG_SCORES if scores else 0)
     n = c_sz(0)
     _check(L.pkv_mx4_workspace_bytes(ctypes.byref(shape), ctypes.byref(plan), ctypes.byref(n)),

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kTokenThreads) mx4_read_kernel(const __grid_co
 //
 // The (row, KV head) pairs' pages lie end to end, ceil(N_i / 16) per pair; of
 // the U pages in all, block b of T owns [floor(b U / T), floor((b + 1) U / T)) and
-// its eight warps split that share the same way, so every warp streams a
+// its warps split that share the same way, so every warp streams a
 // contiguous run of pages, through as many pairs as it takes, and derives it
 // from the device lengths alone: one plan, or one captured graph, serves any
 // lengths.
@@ -298,10 +298,7 @@ __global__ void __launch_bounds__(kTokenThreads) mx4_read_kernel(const __grid_co
 // is merged in shared memory, one that spans blocks by the last block to
 // finish it (an atomic ticket), in ascending order: results are deterministic.
 
-constexpr int kWarps = 8;
-constexpr int kDecodeThreads = kWarps * 32;
 constexpr int kMaxRows = 4096;       // rows whose page offsets a block keeps in shared memory
-constexpr int kMinBlockPages = 8;    // a share below a page per warp only adds states to merge
 constexpr int kMaxBlocks = 1024;     // a merge keeps a weight per block and head in shared memory
 constexpr float kPShift = 15.f;      // P is held times 2^15: the top of f16's range
 
@@ -320,11 +317,16 @@ struct DecodeParams {
     int32_t B, H_q, H_kv, G, max_pages, num_pool_pages, blocks;
 };
 
+// One block per SM: 16 warps of at most 128 registers, or 8 where the 16-head
+// tile needs more.
 template <int D, int NT>
 struct DCfg {
+    static constexpr int kWarps = NT == 1 ? 16 : 8;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kMinPages = 2 * kWarps;  // a smaller share costs more in merging than it saves
     static constexpr int kHeads = 8 * NT;
     static constexpr int kState = kHeads * (D + 4) + 2 * kHeads;  // floats: o (rows padded), m, l
-    static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kStages = D == 128 && NT == 1 ? 4 : 6;
     static constexpr int kWarpRing = kStages * Rec<D>::kBytes;
     static_assert(kState * 4 <= kWarpRing, "a warp's last state takes the place of its ring");
     static constexpr int kFirstOff = kWarps * kWarpRing;  // the states of the warps' first runs
@@ -332,24 +334,24 @@ struct DCfg {
     static constexpr int kPairOff = kBarOff + kWarps * kStages * 8;  // pair of each of the 2 kWarps states
     static constexpr int kMiscOff = kPairOff + 2 * kWarps * 4;
     static constexpr int kScanOff = kMiscOff + 32;
-    static constexpr int kPrefixOff = kScanOff + 64;  // int32 [B + 1]
-    static constexpr int kPerSM = NT == 1 ? 2 : 1;
-    static_assert((kMaxBlocks * kHeads + 4 + 16 + 4 * kDecodeThreads) * 4 <= kBarOff, "a merge's weights and partial sums");
+    static constexpr int kWeightOff = kScanOff + 64;                // the block's merge: weights, maxima and sums
+    static constexpr int kPrefixOff = kWeightOff + 3 * 16 * 32 * 4;  // int32 [B + 1]
+    static_assert((kMaxBlocks * kHeads + 4 + 16 + 4 * kThreads) * 4 <= kBarOff, "a merge's weights and partial sums");
     static_assert(kWarpRing % 16 == 0 && kBarOff % 8 == 0, "alignment of the copies and their barriers");
+    static_assert(kPrefixOff + (kMaxRows + 1) * 4 <= 227 * 1024, "shared memory of a block");
 };
 
-__device__ __forceinline__ int64_t share_begin(int64_t U, int64_t T, int64_t b) { return b * U / T; }
-
-// The block whose share holds page u.
-__device__ __forceinline__ int64_t share_of(int64_t U, int64_t T, int64_t u)
-{
-    int64_t b = u * T / U;
-    while (share_begin(U, T, b + 1) <= u)
-        ++b;
-    while (share_begin(U, T, b) > u)
-        --b;
-    return b;
-}
+// [0, U) in T shares of U / T or one more: share b begins at b (U / T) + min(b, U mod T).
+struct Shares {
+    uint32_t size, more;
+    __device__ Shares(uint32_t U, uint32_t T) : size(U / T), more(U - size * T) {}
+    __device__ uint32_t begin(uint32_t b) const { return b * size + min(b, more); }
+    __device__ uint32_t owner(uint32_t u) const
+    {
+        const uint32_t split = more * (size + 1);
+        return u < split ? u / (size + 1) : more + (u - split) / size;  // size > 0 wherever u >= split
+    }
+};
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1)
@@ -374,14 +376,17 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
 }
 
 // A warp's running state for one pair: heads 8 nt + 2 c + {0, 1}.  o is in units of
-// 2^(vref[b] - 142) for its block b of 32 dims, l in units of 2^-15.
+// 2^(vref(b) - 142) for its block b of 32 dims, l in units of 2^-15.
 template <int D, int NT>
 struct State {
     uint32_t qf[D / 16][NT][2];  // q as the MMA's B operand
     float sl[NT][2];             // logit = product * sl (log2 domain)
-    float m[NT][2], l[NT][2];
+    float nb[NT][2];             // 15 - m, with m the reference max (log2 domain): P is 2^(logit + nb)
+    float l[NT][2];
     float o[D / 16][NT][4];
-    int vref[D / 32];            // top of the window of V's scales, -1: none yet
+    uint32_t vlow;               // per block the lower end of its window of V's scales, 0 .. 247; ~0: none yet
+    // the window's top: the scale in whose units o is
+    __device__ int vref(int b) const { return (int)((vlow >> (8 * b)) & 255u) + 7; }
 };
 
 template <int D, int NT>
@@ -429,30 +434,55 @@ __device__ __forceinline__ void load_q(const DecodeParams &p, int pair, int lane
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        st.m[nt][0] = st.m[nt][1] = -INFINITY;
+        st.nb[nt][0] = st.nb[nt][1] = INFINITY;
         st.l[nt][0] = st.l[nt][1] = 0.f;
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt)
             st.o[mt][nt][0] = st.o[mt][nt][1] = st.o[mt][nt][2] = st.o[mt][nt][3] = 0.f;
     }
-#pragma unroll
-    for (int b = 0; b < D / 32; ++b)
-        st.vref[b] = -1;
+    st.vlow = ~0u;
 }
 
-// Byte b of w as a float's exponent field: 2^(byte - 127), 0 for 0, infinity for 255.
+// Byte b of w as a float's exponent field: 2^(byte - 127), 0 for 0, infinity
+// for 255.  Left shifts as products: the integer multiplier is idle here, the
+// logic unit is what bounds the kernel.
 __device__ __forceinline__ float exponent_float(uint32_t w, int b)
 {
-    const uint32_t at = b == 0 ? w << 23 : b == 1 ? w << 15 : b == 2 ? w << 7 : w >> 1;
-    return __uint_as_float(at & 0x7f800000u);
+    const uint32_t at = w & (0xffu << (8 * b));
+    return __uint_as_float(b == 3 ? at >> 1 : at * (1u << (23 - 8 * b)));
 }
 
 // Codes of two tokens, interleaved for the tensor cores: nibble pairs (token
 // a's, token b's) of the even dims and of the odd dims.
 __device__ __forceinline__ void interleave(uint32_t a, uint32_t b, uint32_t &even, uint32_t &odd)
 {
-    even = (a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u);
+    even = (a & 0x0f0f0f0fu) | ((b * 16u) & 0xf0f0f0f0u);
     odd = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+}
+
+// D = A * B, m16n8k16, f16 operands, fp32 accumulators.
+__device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// The largest scale byte (255 aside) of block b over the valid tokens, for the whole warp.
+__device__ __forceinline__ int top_scale(const uint32_t (&vs)[4], const int (&vt)[4], int nvalid, int b)
+{
+    int top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = (vs[i] >> (8 * b)) & 255;
+        if (vt[i] < nvalid && e < 255)
+            top = max(top, e);
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    return max(top, __shfl_xor_sync(0xffffffffu, top, 2));
 }
 
 // One page in shared memory (rec) into the state.  `release` runs once the
@@ -478,7 +508,11 @@ __device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, in
         for (int i = 0; i < 4; ++i) {
             const uint2 v2 = *reinterpret_cast<const uint2 *>(rec + R::kV + vt[i] * R::kRow + r * 8);
             vw[i][0] = v2.x, vw[i][1] = v2.y;
-            vs[i] = *reinterpret_cast<const uint32_t *>(rec + R::kVs + vt[i] * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const uint2 s2 = *reinterpret_cast<const uint2 *>(rec + R::kVs + vt[i] * 4);
+            vs[i] = s2.x, vs[i + 1] = s2.y;
         }
     } else {
         const uint2 a2 = *reinterpret_cast<const uint2 *>(rec + r * R::kRow + c * 8);
@@ -488,18 +522,18 @@ __device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, in
         ksa = *reinterpret_cast<const uint16_t *>(rec + R::kKs + r * 2);
         ksb = *reinterpret_cast<const uint16_t *>(rec + R::kKs + (r + 8) * 2);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i)
             vw[i][0] = *reinterpret_cast<const uint32_t *>(rec + R::kV + vt[i] * R::kRow + r * 4);
-            vs[i] = *reinterpret_cast<const uint16_t *>(rec + R::kVs + vt[i] * 2);
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const uint32_t s2 = *reinterpret_cast<const uint32_t *>(rec + R::kVs + vt[i] * 2);
+            vs[i] = s2 & 0xffffu, vs[i + 1] = s2 >> 16;
         }
     }
     release();
 
     // ---- S^T = K q^T, each block of 32 dims under its tokens' scales ----
     float s[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
         uint32_t fa[4], fb[4];
@@ -508,50 +542,69 @@ __device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, in
         const float sa = exponent_float(ksa, b), sb = exponent_float(ksb, b);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float part[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(part, fa[0], fb[0], fa[1], fb[1], st.qf[2 * b][nt][0], st.qf[2 * b][nt][1]);
+            float part[4];
+            mma_f16_new(part, fa[0], fb[0], fa[1], fb[1], st.qf[2 * b][nt][0], st.qf[2 * b][nt][1]);
             mma_f16(part, fa[2], fb[2], fa[3], fb[3], st.qf[2 * b + 1][nt][0], st.qf[2 * b + 1][nt][1]);
-            s[nt][0] = fmaf(part[0], sa, s[nt][0]);
-            s[nt][1] = fmaf(part[1], sa, s[nt][1]);
-            s[nt][2] = fmaf(part[2], sb, s[nt][2]);
-            s[nt][3] = fmaf(part[3], sb, s[nt][3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s[nt][i] = b == 0 ? part[i] * (i < 2 ? sa : sb) : fmaf(part[i], i < 2 ? sa : sb, s[nt][i]);
         }
     }
 
     // ---- softmax against the reference max ----
     const bool lo_ok = r < nvalid, hi_ok = r + 8 < nvalid;
-    bool above = false;
+    float t[NT][4], top = -INFINITY;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             // an infinite product comes of a NaN scale (255): + 0 * s makes it NaN
-            const float x = fmaf(s[nt][i], 0.f, s[nt][i] * st.sl[nt][i & 1]);
-            s[nt][i] = (i < 2 ? lo_ok : hi_ok) ? x : -INFINITY;
-            above |= s[nt][i] > st.m[nt][i & 1];
+            t[nt][i] = fmaf(s[nt][i], 0.f, fmaf(s[nt][i], st.sl[nt][i & 1], st.nb[nt][i & 1]));
         }
         if constexpr (SCORED) {
             const int g = 8 * nt + 2 * c;
             if (g < logit_heads) {
+                float x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[i] = fmaf(s[nt][i], 0.f, s[nt][i] * st.sl[nt][i & 1]);
                 if (lo_ok)
-                    *reinterpret_cast<float2 *>(logits + r * logit_heads + g) = make_float2(s[nt][0], s[nt][1]);
+                    *reinterpret_cast<float2 *>(logits + r * logit_heads + g) = make_float2(x[0], x[1]);
                 if (hi_ok)
-                    *reinterpret_cast<float2 *>(logits + (r + 8) * logit_heads + g) = make_float2(s[nt][2], s[nt][3]);
+                    *reinterpret_cast<float2 *>(logits + (r + 8) * logit_heads + g) = make_float2(x[2], x[3]);
             }
         }
     }
-    if (__any_sync(0xffffffffu, above)) {
+    if (nvalid < kPage) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (!(i < 2 ? lo_ok : hi_ok))
+                    t[nt][i] = -INFINITY;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        top = fmaxf(top, fmaxf(fmaxf(t[nt][0], t[nt][1]), fmaxf(t[nt][2], t[nt][3])));
+    if (__any_sync(0xffffffffu, top > kPShift)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float mx = fmaxf(s[nt][j], s[nt][2 + j]);
+                float x0 = fmaf(s[nt][j], 0.f, s[nt][j] * st.sl[nt][j]);
+                float x1 = fmaf(s[nt][2 + j], 0.f, s[nt][2 + j] * st.sl[nt][j]);
+                x0 = lo_ok ? x0 : -INFINITY;
+                x1 = hi_ok ? x1 : -INFINITY;
+                const float old = kPShift - st.nb[nt][j];
+                float mx = fmaxf(fmaxf(x0, x1), old);
 #pragma unroll
                 for (int sh = 4; sh < 32; sh <<= 1)
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-                const float mn = fmaxf(st.m[nt][j], mx);
-                const float al = mn == -INFINITY ? 1.f : exp2_approx(st.m[nt][j] - mn);
-                st.m[nt][j] = mn;
+                // a head with nothing but NaN so far: -inf - -inf, NaN as its sums are
+                const float al = exp2_approx(old - mx);
+                st.nb[nt][j] = kPShift - mx;
+                t[nt][j] = x0 + st.nb[nt][j];
+                t[nt][2 + j] = x1 + st.nb[nt][j];
                 st.l[nt][j] *= al;
 #pragma unroll
                 for (int mt = 0; mt < D / 16; ++mt) {
@@ -562,56 +615,42 @@ __device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, in
     }
     float pr[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float base = (st.m[nt][j] == -INFINITY ? 0.f : st.m[nt][j]) - kPShift;
-            pr[nt][j] = exp2_approx(s[nt][j] - base);
-            pr[nt][2 + j] = exp2_approx(s[nt][2 + j] - base);
-            st.l[nt][j] += pr[nt][j] + pr[nt][2 + j];
-        }
+        for (int i = 0; i < 4; ++i)
+            pr[nt][i] = exp2_approx(t[nt][i]);
+        st.l[nt][0] += pr[nt][0] + pr[nt][2];
+        st.l[nt][1] += pr[nt][1] + pr[nt][3];
+    }
 
     // ---- O^T += V^T (P V-scale)^T ----
-    if (st.vref[0] < 0) {
-        // the pair's first page sets each block's window: two steps above its largest scale
+    if (st.vlow == ~0u) {
+        // the pair's first page sets each block's window, up to two steps above its largest scale
+        st.vlow = 0;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            int top = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int e = (vs[i] >> (8 * b)) & 255;
-                if (vt[i] < nvalid && e < 255)
-                    top = max(top, e);
-            }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            st.vref[b] = min(top + 2, 254);
-        }
+        for (int b = 0; b < kBlocks; ++b)
+            st.vlow |= (uint32_t)min(max(top_scale(vs, vt, nvalid, b) - 5, 0), 247) << (8 * b);
     }
-    // every valid token's scales within [vref - 7, vref]?
-    uint32_t out_of = 0;
-    uint32_t d[4][kBlocks / 2];  // scale - (vref - 7), blocks b and b + kBlocks / 2... in 16-bit halves
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int b = 0; b < kBlocks / 2; ++b) {
-            // halves: D = 128: blocks b and b + 2; D = 64: blocks 0 and 1
-            const uint32_t pairw = D == 128 ? (vs[i] >> (8 * b)) & 0x00ff00ffu
-                                            : (vs[i] & 255u) | (vs[i] & 0xff00u) << 8;
-            const int second = D == 128 ? b + 2 : 1;
-            const uint32_t low = (uint32_t)(st.vref[b] - 7) + ((uint32_t)(st.vref[second] - 7) << 16);
-            d[i][b] = pairw - low;
-            if (vt[i] >= nvalid)
-                d[i][b] = 0;
-            out_of |= d[i][b];
-        }
     uint32_t ve[2][kBlocks / 2], vo[2][kBlocks / 2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int w = 0; w < kBlocks / 2; ++w)
-            interleave(vw[2 * t][w], vw[2 * t + 1][w], ve[t][w], vo[t][w]);
-    if (!__any_sync(0xffffffffu, (out_of & 0xfff8fff8u) != 0)) {
+            interleave(vw[2 * i][w], vw[2 * i + 1][w], ve[i][w], vo[i][w]);
+    // Steps of the tokens' scales above the windows' lower ends, a byte per
+    // block: in their windows iff every byte is 0 .. 7.  (A byte below its
+    // window borrows, but is itself at least 256 - 247 then.)
+    uint32_t d[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        d[i] = vs[i] - st.vlow;
+    if (nvalid < kPage) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (vt[i] >= nvalid)
+                d[i] = 0;
+    }
+    if (!__any_sync(0xffffffffu, ((d[0] | d[1] | d[2] | d[3]) & 0xf8f8f8f8u) != 0)) {
         uint32_t pt[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -626,13 +665,16 @@ __device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, in
             codes_to_half2(ve[1][w], e1);
             codes_to_half2(vo[1][w], o1);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {  // blocks 2 w and 2 w + 1
+            for (int k = 0; k < 2; ++k) {
                 const int b = 2 * w + k;
-                // tokens' steps of block b side by side, then 2^(step - 7) as two halves
-                const int dw = D == 128 ? b & 1 : 0, hi = D == 128 ? b >> 1 : b;
-                const uint32_t sel = hi ? 0x7632 : 0x5410;
-                const uint32_t f0 = __byte_perm(d[0][dw], d[1][dw], sel) * 0x400u + 0x20002000u;
-                const uint32_t f1 = __byte_perm(d[2][dw], d[3][dw], sel) * 0x400u + 0x20002000u;
+                // two tokens' steps of block b as the high bytes of two halves (a byte below 128
+                // replicates a zero sign into the low ones), then 2^(step - 7) by its exponent field
+                const uint32_t sel = (uint32_t)((8 | b) | b << 4 | (8 | 4 | b) << 8 | (4 | b) << 12);
+                uint32_t f0, f1;
+                asm("prmt.b32 %0, %1, %2, %3;" : "=r"(f0) : "r"(d[0]), "r"(d[1]), "r"(sel));
+                asm("prmt.b32 %0, %1, %2, %3;" : "=r"(f1) : "r"(d[2]), "r"(d[3]), "r"(sel));
+                f0 = f0 * 4u + 0x20002000u;
+                f1 = f1 * 4u + 0x20002000u;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const uint32_t p0 = mul_f16x2(pt[nt][0], f0), p1 = mul_f16x2(pt[nt][1], f1);
@@ -648,17 +690,9 @@ __device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, in
     // the same value times 2^-112 in bf16, and P 2^(scale - vref + 127) undoes that.
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
-        int top = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = (vs[i] >> (8 * b)) & 255;
-            if (vt[i] < nvalid && e < 255)
-                top = max(top, e);
-        }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        if (top > st.vref[b]) {
-            const int up = top - st.vref[b];  // 1 .. 254
+        const int top_b = top_scale(vs, vt, nvalid, b);
+        if (top_b > st.vref(b)) {
+            const int up = top_b - st.vref(b);  // 1 .. 247
             const float f = up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -667,7 +701,7 @@ __device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, in
                     st.o[2 * b][nt][i] *= f;
                     st.o[2 * b + 1][nt][i] *= f;
                 }
-            st.vref[b] = top;
+            st.vlow += (uint32_t)up << (8 * b);
         }
     }
     // this lane's rows of P are tokens r and r + 8: their scales, from a lane that holds them
@@ -690,7 +724,7 @@ __device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, in
         for (int k = 0; k < 2; ++k) {
             const int b = 2 * w + k;
             auto factor = [&](uint32_t e, bool ok) {
-                const int x = (int)e - st.vref[b] + 254;
+                const int x = (int)e - st.vref(b) + 254;
                 return !ok || x <= 0 || e == 0u ? 0.f
                        : e == 255u              ? __uint_as_float(0x7fc00000u)
                                                 : __uint_as_float((uint32_t)x << 23);
@@ -727,13 +761,13 @@ __device__ __forceinline__ void put_state(float *dst, int lane, const State<D, N
             for (int sh = 4; sh < 32; sh <<= 1)
                 l += __shfl_xor_sync(0xffffffffu, l, sh);
             if (r == 0) {
-                dm[g] = st.m[nt][j];
+                dm[g] = kPShift - st.nb[nt][j];
                 dl[g] = l * 0x1p-15f;
             }
 #pragma unroll
             for (int b = 0; b < D / 32; ++b) {
                 // 2^(vref - 142) in two steps: 2^-15, then the exponent byte itself
-                const float f = __uint_as_float((uint32_t)max(st.vref[b], 1) << 23);
+                const float f = __uint_as_float((uint32_t)st.vref(b) << 23);
                 *reinterpret_cast<float4 *>(dst + g * (D + 4) + 32 * b + 4 * r) =
                     make_float4(st.o[2 * b][nt][j] * 0x1p-15f * f, st.o[2 * b][nt][2 + j] * 0x1p-15f * f,
                                 st.o[2 * b + 1][nt][j] * 0x1p-15f * f, st.o[2 * b + 1][nt][2 + j] * 0x1p-15f * f);
@@ -762,32 +796,24 @@ __device__ __forceinline__ void write_pair(const DecodeParams &p, int pair, int 
             __nv_bfloat16 *dst = p.out + ((int64_t)pair * p.G + g) * D;
 #pragma unroll
             for (int b = 0; b < D / 32; ++b) {
-                const float f = __uint_as_float((uint32_t)max(st.vref[b], 1) << 23);
+                const float f = __uint_as_float((uint32_t)st.vref(b) << 23);
                 store_bf16x4(dst + 32 * b + 4 * r,
                              make_float4(st.o[2 * b][nt][j] * inv * f, st.o[2 * b][nt][2 + j] * inv * f,
                                          st.o[2 * b + 1][nt][j] * inv * f, st.o[2 * b + 1][nt][2 + j] * inv * f));
             }
             if (SCORED && r == 0) {
-                p.fin_m[(int64_t)pair * p.G + g] = st.m[nt][j];
+                p.fin_m[(int64_t)pair * p.G + g] = kPShift - st.nb[nt][j];
                 p.fin_l[(int64_t)pair * p.G + g] = l;
             }
         }
 }
 
-// Where a page of the grid's page line lies.
-struct Page {
-    int pair;   // row * H_kv + head
-    int index;  // page of its row
-    int pages;  // pages its row has
-    int phys;   // pool page
-    int len;    // its row's tokens
-};
-
 template <int D, int NT, bool SCORED>
-__global__ void __launch_bounds__(kDecodeThreads, (DCfg<D, NT>::kPerSM)) mx4_decode_kernel(const __grid_constant__ DecodeParams p)
+__global__ void __launch_bounds__(DCfg<D, NT>::kThreads, 1) mx4_decode_kernel(const __grid_constant__ DecodeParams p)
 {
     using C = DCfg<D, NT>;
     using R = Rec<D>;
+    constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
     extern __shared__ __align__(128) uint8_t smem[];
     int32_t *state_pair = reinterpret_cast<int32_t *>(smem + C::kPairOff);
     volatile int32_t *misc = reinterpret_cast<volatile int32_t *>(smem + C::kMiscOff);
@@ -795,7 +821,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (DCfg<D, NT>::kPerSM)) mx4_dec
     int32_t *prefix = reinterpret_cast<int32_t *>(smem + C::kPrefixOff);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t capacity = (int64_t)p.max_pages * kPage;
-    uint8_t *ring = smem + warp * C::kStages * R::kBytes;
+    uint8_t *ring = smem + warp * C::kWarpRing;
     const uint32_t ring_addr = smem_addr(ring);
     const uint32_t bars = smem_addr(smem + C::kBarOff) + warp * C::kStages * 8;
     if (lane == 0) {
@@ -820,7 +846,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (DCfg<D, NT>::kPerSM)) mx4_dec
     if (tid == 0)
         prefix[0] = 0;
     int carry = 0;
-    for (int base = 0; base < p.B; base += kDecodeThreads) {
+    for (int base = 0; base < p.B; base += kThreads) {
         const int row = base + tid;
         int v = row < p.B ? (row_len(row, blockIdx.x == 0) + kPage - 1) / kPage : 0;
         for (int o = 1; o < 32; o <<= 1) {
@@ -841,229 +867,261 @@ __global__ void __launch_bounds__(kDecodeThreads, (DCfg<D, NT>::kPerSM)) mx4_dec
             prefix[row + 1] = v + add;
         __syncthreads();
     }
-    const int64_t U = (int64_t)prefix[p.B] * p.H_kv;
+    const uint32_t U = (uint32_t)carry * p.H_kv;  // below 2^31 (checked on the host)
     // rows without tokens have no pages: their zeros are dealt out by row
     for (int row = blockIdx.x; row < p.B; row += p.blocks) {
         if (prefix[row + 1] != prefix[row])
             continue;
         uint4 *dst = reinterpret_cast<uint4 *>(p.out + (int64_t)row * p.H_q * D);
-        for (int i = tid; i < p.H_q * D / 8; i += kDecodeThreads)
+        for (int i = tid; i < p.H_q * D / 8; i += kThreads)
             dst[i] = make_uint4(0, 0, 0, 0);
     }
-    const int64_t want = (U + kMinBlockPages - 1) / kMinBlockPages;
-    const int64_t T = want < p.blocks ? (want < 1 ? 1 : want) : p.blocks;
-    if ((int64_t)blockIdx.x >= T || U == 0)
+    const uint32_t T = max(1u, min((uint32_t)p.blocks, (U + C::kMinPages - 1) / C::kMinPages));
+    if (blockIdx.x >= T || U == 0)
         return;
-    const int64_t u0 = share_begin(U, T, blockIdx.x), u1 = share_begin(U, T, blockIdx.x + 1);
-    const int64_t w0 = u0 + share_begin(u1 - u0, kWarps, warp), w1 = u0 + share_begin(u1 - u0, kWarps, warp + 1);
-    const int n = (int)(w1 - w0);
+    const Shares blocks(U, T);
+    const uint32_t u0 = blocks.begin(blockIdx.x), u1 = blocks.begin(blockIdx.x + 1);
+    const Shares warps(u1 - u0, kWarps);
+    const uint32_t w0 = u0 + warps.begin(warp);
+    const int n = (int)(warps.begin(warp + 1) - warps.begin(warp));
 
     // ---- stream this warp's pages ----
-    auto locate = [&](int64_t u) {
-        Page g{-1, 0, 0, 0, 0};
-        if (u >= w1)
-            return g;
+    // lane l holds page 32 k + l of batch k of them: where it lies, for this batch and the next
+    const uint8_t *cur_src = nullptr, *next_src = nullptr;
+    int cur_pair = -1, next_pair = -1, first_index = 0;
+    auto locate = [&](int j, const uint8_t *&src, int &pair) {
+        if (j >= n)
+            return;
+        const uint32_t u = w0 + j;
         int lo = 0, hi = p.B;  // the last row that begins at or before u
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if ((int64_t)prefix[mid] * p.H_kv <= u)
+            if ((uint32_t)prefix[mid] * p.H_kv <= u)
                 lo = mid;
             else
                 hi = mid;
         }
-        g.pages = prefix[lo + 1] - prefix[lo];
-        const int in = (int)(u - (int64_t)prefix[lo] * p.H_kv);
-        const int head = in / g.pages;
-        g.index = in - head * g.pages;
-        g.pair = lo * p.H_kv + head;
-        g.len = row_len(lo, false);
-        g.phys = __ldg(p.block_table + (int64_t)lo * p.max_pages + g.index);
-        if (g.phys < 0 || g.phys >= p.num_pool_pages) {
+        const uint32_t pages = prefix[lo + 1] - prefix[lo];
+        const uint32_t in = u - (uint32_t)prefix[lo] * p.H_kv;
+        const uint32_t head = in / pages, index = in - head * pages;
+        if (j == 0)
+            first_index = (int)index;
+        pair = lo * p.H_kv + (int)head;
+        int phys = __ldg(p.block_table + (int64_t)lo * p.max_pages + index);
+        if (phys < 0 || phys >= p.num_pool_pages) {
             atomicOr(p.ws_error, kErrPageId);
-            g.phys = 0;  // read a real page instead; the error bit reports the bad entry
+            phys = 0;  // read a real page instead; the error bit reports the bad entry
         }
-        return g;
+        src = p.pool + (int64_t)phys * p.stride_page + (int64_t)head * p.stride_head;
     };
-    auto issue = [&](const Page &g, int j) {  // by the lane that holds page j
-        const int s = j % C::kStages;
+    auto issue = [&](const uint8_t *src, int s) {
         mbar_expect_tx(bars + 8 * s, R::kBytes);
-        bulk_g2s(ring_addr + s * R::kBytes, p.pool + (int64_t)g.phys * p.stride_page + (int64_t)(g.pair % p.H_kv) * p.stride_head,
-                 R::kBytes, bars + 8 * s);
+        bulk_g2s(ring_addr + s * R::kBytes, src, R::kBytes, bars + 8 * s);
     };
-    // lane l holds page 32 k + l of batch k: the current batch and the next
-    Page cur = locate(w0 + lane), next = locate(w0 + 32 + lane);
+    locate(lane, cur_src, cur_pair);
     __syncwarp();  // the barriers' initialisation
     if (lane < C::kStages && lane < n)
-        issue(cur, lane);
+        issue(cur_src, lane);
+    if (n > 32)
+        locate(32 + lane, next_src, next_pair);
+    first_index = __shfl_sync(0xffffffffu, first_index, 0);
 
-    // A run that is its whole pair is written out at once; one that the warp's
-    // share cuts becomes a state: the warp's first run beside the rings (in use
-    // until the warp is done), its last one in the warp's own ring.
+    // A run of pages that is its whole pair is written out at once; one that the
+    // warp's share cuts becomes a state: the warp's first run beside the rings (in
+    // use until the warp is done), its last one in the warp's own ring.
     auto state_at = [&](int i) {  // state i = 2 * warp + (0 first, 1 last)
         return reinterpret_cast<float *>(i & 1 ? smem + (i >> 1) * C::kWarpRing
                                                : smem + C::kFirstOff + (i >> 1) * C::kState * 4);
     };
     State<D, NT> st;
-    int pair = -1, begin = 0, run = 0;  // current pair, its run's first page, the warp's runs so far
+    int stage = 0, phase = 0;
     bool ok = true;
-    auto finish = [&](int end, int pages, bool last) {
+    for (int j = 0; j < n && ok;) {
+        const int pair = __shfl_sync(0xffffffffu, cur_pair, j & 31);
+        const int row = pair / p.H_kv;
+        const int len = row_len(row, false);
+        const int pages = prefix[row + 1] - prefix[row];
+        const int begin = j == 0 ? first_index : 0;
+        const int end = min(pages, begin + n - j);
+        load_q<D, NT>(p, pair, lane, st);
+        for (int index = begin; index < end; ++index) {
+            const uint32_t bar = bars + 8 * stage;
+            if (!mbar_try_wait(bar, phase))
+                ok = mbar_wait(bar, phase, p.ws_error);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+                // give up on the pair, but not before the copies in flight had their time to land
+                for (int k = 1; k < C::kStages && j + k < n; ++k) {
+                    stage = stage + 1 == C::kStages ? 0 : stage + 1;
+                    phase ^= stage == 0;
+                    mbar_wait(bars + 8 * stage, phase, p.ws_error);
+                }
+                break;
+            }
+            float *logits = nullptr;
+            int heads = 0;
+            if constexpr (SCORED) {
+                heads = (p.G + 1) & ~1;
+                logits = p.logits + ((int64_t)pair * capacity + (int64_t)index * kPage) * heads;
+            }
+            attend_record<D, NT, SCORED>(ring + stage * R::kBytes, min(kPage, len - index * kPage), lane, st, logits,
+                                         heads, [&]() {
+                __syncwarp();
+                const int k = j + C::kStages;  // the page that takes this one's place
+                if (lane == (k & 31) && k < n)
+                    issue(((k ^ j) & ~31) == 0 ? cur_src : next_src, stage);
+            });
+            stage = stage + 1 == C::kStages ? 0 : stage + 1;
+            phase ^= stage == 0;
+            ++j;
+            if ((j & 31) == 0) {
+                cur_src = next_src;
+                cur_pair = next_pair;
+                locate(j + 32 + lane, next_src, next_pair);
+            }
+        }
+        if (!ok)
+            break;
         if (begin == 0 && end == pages) {
             write_pair<D, NT, SCORED>(p, pair, lane, st);
         } else {
-            const int i = 2 * warp + (last && run > 1 ? 1 : 0);
+            // the first run where it is not whole begins this warp's share; any other reaches its end
+            const int i = 2 * warp + (j - (end - begin) > 0 ? 1 : 0);
             put_state<D, NT>(state_at(i), lane, st);
             if (lane == 0)
                 state_pair[i] = pair;
         }
-    };
-    int end = 0, pages = 0;  // the current run's end (page of its row) and its row's pages
-    for (int j = 0; j < n; ++j) {
-        const int src = j & 31;
-        if (src == 0 && j > 0) {
-            cur = next;
-            next = locate(w0 + j + 32 + lane);
-        }
-        const int g_pair = __shfl_sync(0xffffffffu, cur.pair, src);
-        const int g_index = __shfl_sync(0xffffffffu, cur.index, src);
-        const int g_len = __shfl_sync(0xffffffffu, cur.len, src);
-        if (g_pair != pair) {
-            if (pair >= 0)
-                finish(end, pages, false);
-            pair = g_pair;
-            begin = g_index;
-            ++run;
-            load_q<D, NT>(p, pair, lane, st);
-        }
-        end = g_index + 1;
-        pages = (g_len + kPage - 1) / kPage;
-        const int s = j % C::kStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * s, (j / C::kStages) & 1, p.ws_error));
-        if (!ok) {
-            // give up on the pair, but not before the copies in flight had their time to land
-            for (int k = j + 1; k < min(n, j + C::kStages); ++k)
-                mbar_wait(bars + 8 * (k % C::kStages), (k / C::kStages) & 1, p.ws_error);
-            break;
-        }
-        const int nvalid = min(kPage, g_len - g_index * kPage);
-        float *logits = nullptr;
-        int heads = 0;
-        if constexpr (SCORED) {
-            heads = (p.G + 1) & ~1;
-            logits = p.logits + ((int64_t)pair * capacity + (int64_t)g_index * kPage) * heads;
-        }
-        attend_record<D, NT, SCORED>(ring + s * R::kBytes, nvalid, lane, st, logits, heads, [&]() {
-            __syncwarp();
-            const int k = j + C::kStages;  // the page that takes this one's place
-            if (k < n && lane == (k & 31))
-                issue((k >> 5) == (j >> 5) ? cur : next, k);
-        });
     }
     grid_launch_dependents();
-    if (n > 0 && ok)
-        finish(end, pages, true);
     __syncthreads();
 
     // ---- merge the states of pairs that the warps share ----
+    // Lane k of every warp looks at state k: which are there, and where a new
+    // pair begins among them (the states of one pair are neighbours).
     constexpr int D4 = D / 4;
     const int G = p.G;
-    int open[2] = {-1, -1};  // pairs that reach into other blocks
-    for (int i = 0; i < 2 * kWarps;) {
-        const int which = state_pair[i];
-        int next_i = i + 1;
-        if (which < 0) {
-            i = next_i;
-            continue;
-        }
-        while (next_i < 2 * kWarps && (state_pair[next_i] == which || state_pair[next_i] < 0))
-            ++next_i;
-        const int row = which / p.H_kv;
-        const int row_pages = prefix[row + 1] - prefix[row];
-        const int64_t P0 = (int64_t)prefix[row] * p.H_kv + (int64_t)(which % p.H_kv) * row_pages;
-        const bool whole = P0 >= u0 && P0 + row_pages <= u1;
-        const int slot = 2 * blockIdx.x + (P0 > u0 ? 1 : 0);
-        if (!whole)
-            open[P0 > u0 ? 1 : 0] = which;
-        for (int e = tid; e < G * D4; e += kDecodeThreads) {
-            const int g = e / D4, d4 = (e % D4) * 4;
-            float M = -INFINITY, L = 0.f;
-            for (int k = i; k < next_i; ++k)
-                if (state_pair[k] == which)
-                    M = fmaxf(M, state_at(k)[C::kHeads * (D + 4) + g]);
-            const float base = M == -INFINITY ? 0.f : M;
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = i; k < next_i; ++k) {
-                if (state_pair[k] != which)
-                    continue;
-                const float *sk = state_at(k);
-                const float w = exp2_approx(sk[C::kHeads * (D + 4) + g] - base);
-                L = fmaf(sk[C::kHeads * (D + 4) + C::kHeads + g], w, L);
-                O = fma4(*reinterpret_cast<const float4 *>(sk + g * (D + 4) + d4), w, O);
+    float *weight = reinterpret_cast<float *>(smem + C::kWeightOff);  // [head][state]
+    float *pair_m = weight + 16 * 32, *pair_l = pair_m + 16 * 32;     // [head][a pair's first state]
+    const int my_pair = lane < 2 * kWarps ? state_pair[lane] : -1;
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t there = __ballot_sync(0xffffffffu, my_pair >= 0);
+    const int before = 31 - __clz(there & below);  // the state before this one, or -1
+    const int pair_before = __shfl_sync(0xffffffffu, my_pair, before & 31);
+    const uint32_t starts = __ballot_sync(0xffffffffu, my_pair >= 0 && (before < 0 || pair_before != my_pair));
+    if (there == 0)
+        return;
+    auto members = [&](uint32_t start) {  // the states of the pair that begins at this bit
+        const uint32_t later = starts & ~((start << 1) - 1u);
+        return there & ~(start - 1u) & (later ? (later & (0u - later)) - 1u : ~0u);
+    };
+    for (int g = warp; g < G; g += kWarps) {
+        const float *sk = state_at(lane) + C::kHeads * (D + 4) + g;
+        const float m = my_pair >= 0 ? sk[0] : -INFINITY, l = my_pair >= 0 ? sk[C::kHeads] : 0.f;
+        for (uint32_t left = starts; left; left &= left - 1u) {
+            const uint32_t start = left & (0u - left);
+            const bool mine = (members(start) >> lane) & 1u;
+            float M = mine ? m : -INFINITY;
+            for (int o = 16; o > 0; o >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            const float w = exp2_approx(m - (M == -INFINITY ? 0.f : M));
+            float L = mine ? l * w : 0.f;
+            for (int o = 16; o > 0; o >>= 1)
+                L += __shfl_xor_sync(0xffffffffu, L, o);
+            if (mine)
+                weight[g * 32 + lane] = w;
+            if (start >> lane == 1u) {
+                pair_m[g * 32 + lane] = M;
+                pair_l[g * 32 + lane] = L;
             }
+        }
+    }
+    __syncthreads();
+    // Where a pair's pages lie on the line.
+    auto pair_begin = [&](int which, uint32_t &pages) {
+        const int row = which / p.H_kv;
+        pages = prefix[row + 1] - prefix[row];
+        return (uint32_t)prefix[row] * p.H_kv + (uint32_t)(which - row * p.H_kv) * pages;
+    };
+    for (uint32_t left = starts; left; left &= left - 1u) {
+        const int first = __ffs(left) - 1;
+        const uint32_t in = members(1u << first);
+        const int which = state_pair[first];
+        uint32_t pages;
+        const uint32_t P0 = pair_begin(which, pages);
+        const bool whole = P0 >= u0 && P0 + pages <= u1;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (P0 > u0 ? 1 : 0);
+        for (int e = tid; e < G * D4; e += kThreads) {
+            const int g = e / D4, d4 = (e % D4) * 4;
+            const float *col = state_at(0) + g * (D + 4) + d4;  // of a first state; a last one's lies at the same offset
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (uint32_t rest = in; rest; rest &= rest - 1u) {
+                const int k = __ffs(rest) - 1;
+                O = fma4(*reinterpret_cast<const float4 *>(col + (state_at(k) - state_at(0))), weight[g * 32 + k], O);
+            }
+            const float L = pair_l[g * 32 + first];
             if (whole) {
                 store_bf16x4(p.out + ((int64_t)which * G + g) * D + d4, scale4(O, L == 0.f ? 0.f : 1.f / L));
                 if (SCORED && d4 == 0) {
-                    p.fin_m[(int64_t)which * G + g] = M;
+                    p.fin_m[(int64_t)which * G + g] = pair_m[g * 32 + first];
                     p.fin_l[(int64_t)which * G + g] = L;
                 }
             } else {
-                const int64_t at = (int64_t)slot * G + g;
+                const int64_t at = slot * G + g;
                 *reinterpret_cast<float4 *>(p.ws_acc + at * D + d4) = O;
                 if (d4 == 0) {
-                    p.ws_m[at] = M;
+                    p.ws_m[at] = pair_m[g * 32 + first];
                     p.ws_l[at] = L;
                 }
             }
         }
-        i = next_i;
     }
-    if (open[0] < 0 && open[1] < 0)
-        return;
 
     // ---- pairs that span blocks: the last block to finish one merges its states ----
-    __syncthreads();
-    int64_t first_block[2] = {0, 0};
-    int slots[2] = {0, 0};
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        if (open[k] < 0)
-            continue;
-        const int row = open[k] / p.H_kv;
-        const int row_pages = prefix[row + 1] - prefix[row];
-        const int64_t P0 = (int64_t)prefix[row] * p.H_kv + (int64_t)(open[k] % p.H_kv) * row_pages;
-        first_block[k] = share_of(U, T, P0);
-        slots[k] = (int)(share_of(U, T, P0 + row_pages - 1) - first_block[k]) + 1;
-        first_block[k] = 2 * first_block[k] + (share_begin(U, T, first_block[k]) == P0 ? 0 : 1);  // its slot
+    // Only the block's first and last pair can reach beyond it.
+    auto settle = [&](int which) {
+        uint32_t pages;
+        const uint32_t P0 = pair_begin(which, pages);
+        if (P0 >= u0 && P0 + pages <= u1)
+            return;
+        const uint32_t first_block = blocks.owner(P0);
+        const int count = (int)(blocks.owner(P0 + pages - 1) - first_block) + 1;
+        // the first block's state is its last pair's unless its share begins with the pair
+        const uint32_t first_slot = 2 * first_block + (blocks.begin(first_block) == P0 ? 0 : 1);
+        __syncthreads();
         if (tid == 0)
-            misc[k] = ticket_acq_rel(p.ws_counters + open[k]) == (uint32_t)(slots[k] - 1);
-    }
-    __syncthreads();
-    for (int k = 0; k < 2; ++k) {
-        if (open[k] < 0 || !misc[k])
-            continue;
-        const int which = open[k], count = slots[k];
-        // slot of the i-th state: the pair's first block holds it as its first or last unfinished pair, the
-        // others as their first
-        const int64_t first = first_block[k];
-        auto slot_of = [&](int i) { return i == 0 ? first : 2 * (first / 2 + i); };
-        float *weight = reinterpret_cast<float *>(smem);        // [count][G]
-        float *norm = weight + (count * G + 3) / 4 * 4;         // [16]
-        float *parts = norm + 16;                               // [kDecodeThreads][4], 16-byte aligned
+            misc[0] = ticket_acq_rel(p.ws_counters + which) == (uint32_t)(count - 1);
+        __syncthreads();
+        if (!misc[0])
+            return;
+        auto slot_of = [&](int i) { return i == 0 ? first_slot : 2 * (first_block + i); };
+        float *wt = reinterpret_cast<float *>(smem);   // [count][G]
+        float *norm = wt + (count * G + 3) / 4 * 4;    // [16]
+        float *parts = norm + 16;                      // [kThreads][4], 16-byte aligned
         for (int g = warp; g < G; g += kWarps) {
-            float M = -INFINITY;
-            for (int i = lane; i < count; i += 32)
-                M = fmaxf(M, p.ws_m[slot_of(i) * G + g]);
-            for (int sh = 16; sh > 0; sh >>= 1)
-                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
+            float m0 = -INFINITY, l0 = 0.f;
+            if (lane < count) {
+                m0 = __ldcg(p.ws_m + slot_of(lane) * G + g);
+                l0 = __ldcg(p.ws_l + slot_of(lane) * G + g);
+            }
+            float M = m0;
+            for (int i = lane + 32; i < count; i += 32)
+                M = fmaxf(M, __ldcg(p.ws_m + slot_of(i) * G + g));
+            for (int o = 16; o > 0; o >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
             const float base = M == -INFINITY ? 0.f : M;
             float L = 0.f;
-            for (int i = lane; i < count; i += 32) {
-                const int64_t at = slot_of(i) * G + g;
-                const float w = exp2_approx(p.ws_m[at] - base);
-                weight[i * G + g] = w;
-                L = fmaf(p.ws_l[at], w, L);
+            if (lane < count) {
+                const float w = exp2_approx(m0 - base);
+                wt[lane * G + g] = w;
+                L = l0 * w;
             }
-            for (int sh = 16; sh > 0; sh >>= 1)
-                L += __shfl_xor_sync(0xffffffffu, L, sh);
+            for (int i = lane + 32; i < count; i += 32) {
+                const float w = exp2_approx(__ldcg(p.ws_m + slot_of(i) * G + g) - base);
+                wt[i * G + g] = w;
+                L = fmaf(__ldcg(p.ws_l + slot_of(i) * G + g), w, L);
+            }
+            for (int o = 16; o > 0; o >>= 1)
+                L += __shfl_xor_sync(0xffffffffu, L, o);
             if (lane == 0) {
                 norm[g] = L == 0.f ? 0.f : 1.f / L;
                 if (SCORED) {
@@ -1075,24 +1133,24 @@ __global__ void __launch_bounds__(kDecodeThreads, (DCfg<D, NT>::kPerSM)) mx4_dec
         __syncthreads();
         // few columns: several threads share one, each over a run of the states
         const int tasks = G * D4;
-        const int split = tasks < kDecodeThreads ? kDecodeThreads / tasks : 1;
-        for (int e0 = 0; e0 < tasks; e0 += kDecodeThreads) {
+        const int split = tasks < kThreads ? kThreads / tasks : 1;
+        for (int e0 = 0; e0 < tasks; e0 += kThreads) {
             const int e = split > 1 ? tid % tasks : e0 + tid, part = split > 1 ? tid / tasks : 0;
             float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
             if (e < tasks && part < split) {
                 const int g = e / D4, d4 = (e % D4) * 4;
                 const int i1 = count * (part + 1) / split;
-#pragma unroll 4
+#pragma unroll 6
                 for (int i = count * part / split; i < i1; ++i)
-                    O = fma4(__ldcg(reinterpret_cast<const float4 *>(p.ws_acc + (slot_of(i) * G + g) * D + d4)),
-                             weight[i * G + g], O);
+                    O = fma4(__ldcg(reinterpret_cast<const float4 *>(p.ws_acc + ((int64_t)slot_of(i) * G + g) * D + d4)),
+                             wt[i * G + g], O);
             }
             if (split > 1) {
                 reinterpret_cast<float4 *>(parts)[tid] = O;
                 __syncthreads();
                 if (part == 0)
-                    for (int k2 = 1; k2 < split; ++k2)
-                        O = fma4(reinterpret_cast<const float4 *>(parts)[k2 * tasks + e], 1.f, O);
+                    for (int k = 1; k < split; ++k)
+                        O = fma4(reinterpret_cast<const float4 *>(parts)[k * tasks + e], 1.f, O);
             }
             if (e < tasks && part == 0)
                 store_bf16x4(p.out + ((int64_t)which * G + e / D4) * D + (e % D4) * 4, scale4(O, norm[e / D4]));
@@ -1100,7 +1158,11 @@ __global__ void __launch_bounds__(kDecodeThreads, (DCfg<D, NT>::kPerSM)) mx4_dec
         if (tid == 0)
             p.ws_counters[which] = 0u;  // ready for the next call
         __syncthreads();
-    }
+    };
+    const int head_pair = state_pair[__ffs(starts) - 1], tail_pair = state_pair[31 - __clz(starts)];
+    settle(head_pair);
+    if (tail_pair != head_pair)
+        settle(tail_pair);
 }
 
 // ---------------------------------------------------------------------------
@@ -1159,11 +1221,10 @@ cudaError_t launch_mx4(const DecodeParams &p, cudaStream_t st, bool pdl)
     using C = DCfg<D, NT>;
     auto kernel = mx4_decode_kernel<D, NT, SCORED>;
     const size_t smem = (size_t)C::kPrefixOff + (size_t)(p.B + 1) * 4;
-    static_assert(C::kPrefixOff + (kMaxRows + 1) * 4 <= 227 * 1024, "shared memory of a block");
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess)
         return e;
-    return launch_kernel(kernel, (unsigned)p.blocks, kDecodeThreads, smem, st, pdl, p);
+    return launch_kernel(kernel, (unsigned)p.blocks, C::kThreads, smem, st, pdl, p);
 }
 
 unsigned token_grid(int64_t rows, int lanes)
