@@ -96,10 +96,10 @@ struct __align__(64) Params {
     int32_t device_fill;      // WORK_QUEUE: every block derives its own item from the device lengths
     int32_t fill_blocks;      // ... of the queue whose chunk fills one wave of this many blocks
     // scored decode (PKV_FLAG_SCORES): the logits in the log2 domain, [pair][max_pages * P][logit_heads], and each
-    // pair's first state slot and slot count, both for the weights kernel that follows
+    // pair's state slots, both for the weights kernel that follows
     float *logits;
-    int2 *slot_range;
-    int32_t logit_heads;      // G rounded up to even, so that a lane's two heads are one 8-byte store
+    SlotRange *slot_range;
+    int32_t logit_heads;
 #ifdef PKV_TRACE
     int32_t trace_epoch;
 #endif
@@ -1555,7 +1555,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, (NST >= 12 ? 2 : 3)) split_kern
 
     if constexpr (SCORED) {
         if (tid == 0 && my_slot == slot0)
-            p.slot_range[pair] = make_int2(slot0, nslots);
+            p.slot_range[pair] = SlotRange{slot0, nslots, slot0, 1};
     }
     PKV_TRACE_POINT(4);
     if (CL) {
@@ -3106,7 +3106,7 @@ int paged_decode_impl(const void *q, const void *k_pool, const void *v_pool, con
     prm.fill_blocks = device_fill ? pl.num_splits : 0;
     if (scores) {
         prm.logits = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + ws.logits_off);
-        prm.slot_range = reinterpret_cast<int2 *>(static_cast<uint8_t *>(workspace) + ws.range_off);
+        prm.slot_range = reinterpret_cast<SlotRange *>(static_cast<uint8_t *>(workspace) + ws.range_off);
         prm.logit_heads = logit_heads(prm.G);
     }
 #ifdef PKV_TRACE
@@ -3153,7 +3153,7 @@ int paged_decode_impl(const void *q, const void *k_pool, const void *v_pool, con
         w.logits = prm.logits;
         w.m = prm.ws_m;
         w.l = prm.ws_l;
-        w.slot_range = prm.slot_range;
+        w.ranges = prm.slot_range;
         w.seq_lens = seq_lens;
         w.scores = scores->scores;
         w.stride_row = scores->stride_row;

@@ -352,11 +352,18 @@ struct ScoreArgs {
     int64_t stride_row, stride_head;
 };
 
+// The state slots of one (row, KV head): slot(0) = first, slot(i) = base + step * i.
+// `count` 0: none (no tokens, or a work item that was refused).
+struct __align__(16) SlotRange {
+    int32_t first, count, base, step;
+    __device__ int64_t slot(int i) const { return i == 0 ? first : base + (int64_t)step * i; }
+};
+
 // Arguments of the weights kernel (pkv_scores.cu).
 struct WeightParams {
     const float *logits;       // [pair][capacity][logit_heads(G)], log2 domain
     const float *m, *l;        // [slot][G] states: running max (log2 domain) and denominator
-    const int2 *slot_range;    // {first slot, slots} of each pair, or NULL: slot = pair
+    const SlotRange *ranges;   // per pair
     const int32_t *seq_lens;
     float *scores;
     int64_t stride_row, stride_head;
@@ -366,8 +373,95 @@ struct WeightParams {
 };
 
 // Blocks of the weights kernel: kWeightTokens tokens of one pair each.
+constexpr int kWeightThreads = 256;
 constexpr int kWeightTokens = 1024;
 inline int64_t weight_blocks(int64_t pairs, int64_t capacity) { return pairs * ceil_div(capacity, kWeightTokens); }
+
+// One block's part of the weights kernel, after the kernel before it has
+// completed: adds the weights of tokens [chunk * kWeightTokens, + kWeightTokens)
+// of a pair to its scores.  LH = logit_heads(G).  The token's logits and
+// scores are loaded before the pair's maximum and sum are known, all at once.
+template <int LH>
+__device__ __forceinline__ void add_weights(const WeightParams &p, int pair, int chunk, float *s_m, float *s_inv)
+{
+    constexpr int kTokens = kWeightTokens / kWeightThreads;
+    const int row = pair / p.H_kv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t0 = (int64_t)chunk * kWeightTokens + threadIdx.x;
+    const SlotRange range = p.ranges[pair];
+    int64_t n = __ldg(p.seq_lens + row);
+    n = n < 0 ? 0 : (n > p.capacity ? p.capacity : n);
+    if ((int64_t)chunk * kWeightTokens >= n)
+        return;
+    float *out = p.scores + (int64_t)row * p.stride_row + (int64_t)(pair % p.H_kv) * p.stride_head;
+    const float *x = p.logits + (int64_t)pair * p.capacity * LH;
+    float v[kTokens][LH], old[kTokens];
+#pragma unroll
+    for (int k = 0; k < kTokens; ++k) {
+        const int64_t t = t0 + k * kWeightThreads;
+        old[k] = 0.f;
+        if (t < n) {
+            old[k] = out[t];
+            if constexpr (LH == 2) {
+                const float2 a = __ldcg(reinterpret_cast<const float2 *>(x + t * LH));
+                v[k][0] = a.x, v[k][1] = a.y;
+            } else {
+#pragma unroll
+                for (int g = 0; g < LH; g += 4) {
+                    const float4 a = __ldcg(reinterpret_cast<const float4 *>(x + t * LH + g));
+                    v[k][g] = a.x, v[k][g + 1] = a.y, v[k][g + 2] = a.z, v[k][g + 3] = a.w;
+                }
+            }
+        }
+    }
+    // a decode block that refused a malformed work item leaves no usable range
+    if (range.first < 0 || range.count < 1 || range.first >= p.n_slots || range.slot(range.count - 1) >= p.n_slots)
+        return;
+    for (int g = warp; g < LH; g += kWeightThreads / 32) {
+        float m = -INFINITY, l = 0.f;
+        if (g < p.G) {
+            float m0 = -INFINITY, l0 = 0.f;
+            if (lane < range.count) {
+                m0 = __ldcg(p.m + range.slot(lane) * p.G + g);
+                l0 = __ldcg(p.l + range.slot(lane) * p.G + g);
+            }
+            m = m0;
+            for (int k = lane + 32; k < range.count; k += 32)
+                m = fmaxf(m, __ldcg(p.m + range.slot(k) * p.G + g));
+#pragma unroll
+            for (int sh = 16; sh > 0; sh >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, sh));
+            m = m == -INFINITY ? 0.f : m;
+            l = l0 * exp2_approx(m0 - m);
+            for (int k = lane + 32; k < range.count; k += 32)
+                l = fmaf(__ldcg(p.l + range.slot(k) * p.G + g), exp2_approx(__ldcg(p.m + range.slot(k) * p.G + g) - m), l);
+#pragma unroll
+            for (int sh = 16; sh > 0; sh >>= 1)
+                l += __shfl_xor_sync(0xffffffffu, l, sh);
+        }
+        if (lane == 0) {
+            s_m[g] = m == -INFINITY ? 0.f : m;
+            s_inv[g] = l == 0.f ? 0.f : 1.f / l;  // no weight where every logit is -inf; NaN stays NaN
+        }
+    }
+    __syncthreads();
+    float w[kTokens] = {};
+#pragma unroll
+    for (int g = 0; g < LH; ++g) {
+        if (g >= p.G)
+            break;
+        const float m = s_m[g], inv = s_inv[g];
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k)
+            w[k] = fmaf(exp2_approx(v[k][g] - m), inv, w[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kTokens; ++k) {
+        const int64_t t = t0 + k * kWeightThreads;
+        if (t < n)
+            out[t] = old[k] + w[k];
+    }
+}
 
 cudaError_t launch_add_weights(const WeightParams &w, int64_t pairs, cudaStream_t st, bool pdl);
 

@@ -30,15 +30,15 @@ struct WsLayout {
     size_t m_off = 0;        // float m[slot][G]  (running max, log2 domain)
     size_t l_off = 0;        // float l[slot][G]
     size_t acc_off = 0;      // float acc[slot][G][D]
-    size_t range_off = 0;    // PKV_FLAG_SCORES: {first slot, slots} per pair
+    size_t range_off = 0;    // PKV_FLAG_SCORES: the pair's slots, as int4 (SlotRange)
     size_t logits_off = 0;   // PKV_FLAG_SCORES: float logits[pair][max_pages * P][logit_heads(G)]
     size_t total = 0;
     int64_t n_slots = 0;
 };
 
-// Heads a token's stored logits are laid out for: G rounded up to even, so
-// that two heads' logits are one aligned 8-byte store.
-inline int32_t logit_heads(int64_t G) { return (int32_t)((G + 1) & ~int64_t(1)); }
+// Heads a token's stored logits are laid out for: the power of two from 2 up that
+// holds G, so that they are whole aligned vectors.
+inline int32_t logit_heads(int64_t G) { return G <= 2 ? 2 : G <= 4 ? 4 : G <= 8 ? 8 : 16; }
 
 inline WsLayout ws_layout(const pkv_shape &s, const pkv_plan &p, int32_t n_items)
 {
@@ -63,7 +63,7 @@ inline WsLayout ws_layout(const pkv_shape &s, const pkv_plan &p, int32_t n_items
     off += round_up((size_t)(w.n_slots * G * s.head_dim) * 4, kWsAlign);
     if (scores) {
         w.range_off = off;
-        off += round_up((size_t)pairs * 8, kWsAlign);
+        off += round_up((size_t)pairs * 16, kWsAlign);
         w.logits_off = off;
         off += round_up((size_t)pairs * s.max_pages_per_seq * s.page_size * logit_heads(G) * 4, kWsAlign);
     }

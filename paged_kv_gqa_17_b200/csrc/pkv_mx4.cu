@@ -295,11 +295,11 @@ __global__ void __launch_bounds__(kTokenThreads) mx4_read_kernel(const __grid_co
 //     eight steps below it take the same product in bf16, whose exponents
 //     reach everywhere.
 // A pair within one warp's run is finished by the warp; a pair that spans warps
-// is merged in shared memory, one that spans blocks by the last block to
-// finish it (an atomic ticket), in ascending order: results are deterministic.
+// is merged in shared memory, one that spans blocks by the kernel that
+// follows, always in ascending order: results are deterministic.
 
 constexpr int kMaxRows = 4096;       // rows whose page offsets a block keeps in shared memory
-constexpr int kMaxBlocks = 1024;     // a merge keeps a weight per block and head in shared memory
+constexpr int kMaxBlocks = 1024;
 constexpr float kPShift = 15.f;      // P is held times 2^15: the top of f16's range
 
 struct DecodeParams {
@@ -309,10 +309,14 @@ struct DecodeParams {
     int64_t stride_page, stride_head;
     const int32_t *block_table;
     const int32_t *seq_lens;
-    float *ws_m, *ws_l, *ws_acc;  // [2 T][G], [2 T][G], [2 T][G][D]: a block's first and last unfinished pair
-    uint32_t *ws_counters;        // tickets per pair
+    // State slots: 2 b and 2 b + 1 hold block b's first and last pair where they reach into other blocks,
+    // 2 T + pair (m and l alone, scored decodes) a pair that one block finished.
+    float *ws_m, *ws_l, *ws_acc;
+    SlotRange *spans;  // [T]: the slots of the pair that begins in block b and reaches beyond it
+    int32_t *span_pair;  // [T]: that pair, or -1
     uint32_t *ws_error;
-    float *logits, *fin_m, *fin_l;  // scored decode: logits, and every pair's final state
+    float *logits;       // scored decode: [pair][max_pages * P][logit_heads(G)]
+    SlotRange *ranges;   // scored decode: every pair's slots
     float scale_log2;
     int32_t B, H_q, H_kv, G, max_pages, num_pool_pages, blocks;
 };
@@ -331,12 +335,10 @@ struct DCfg {
     static_assert(kState * 4 <= kWarpRing, "a warp's last state takes the place of its ring");
     static constexpr int kFirstOff = kWarps * kWarpRing;  // the states of the warps' first runs
     static constexpr int kBarOff = kFirstOff + kWarps * kState * 4;
-    static constexpr int kPairOff = kBarOff + kWarps * kStages * 8;  // pair of each of the 2 kWarps states
-    static constexpr int kMiscOff = kPairOff + 2 * kWarps * 4;
-    static constexpr int kScanOff = kMiscOff + 32;
+    static constexpr int kPairOff = kBarOff + kWarps * kStages * 8;  // pair of each of the 2 kWarps states, and
+    static constexpr int kScanOff = kPairOff + 4 * kWarps * 4;       // where the n-th of those present lies
     static constexpr int kWeightOff = kScanOff + 64;                // the block's merge: weights, maxima and sums
     static constexpr int kPrefixOff = kWeightOff + 3 * 16 * 32 * 4;  // int32 [B + 1]
-    static_assert((kMaxBlocks * kHeads + 4 + 16 + 4 * kThreads) * 4 <= kBarOff, "a merge's weights and partial sums");
     static_assert(kWarpRing % 16 == 0 && kBarOff % 8 == 0, "alignment of the copies and their barriers");
     static_assert(kPrefixOff + (kMaxRows + 1) * 4 <= 227 * 1024, "shared memory of a block");
 };
@@ -802,8 +804,11 @@ __device__ __forceinline__ void write_pair(const DecodeParams &p, int pair, int 
                                          st.o[2 * b + 1][nt][j] * inv * f, st.o[2 * b + 1][nt][2 + j] * inv * f));
             }
             if (SCORED && r == 0) {
-                p.fin_m[(int64_t)pair * p.G + g] = kPShift - st.nb[nt][j];
-                p.fin_l[(int64_t)pair * p.G + g] = l;
+                const int64_t at = (int64_t)(2 * p.blocks + pair) * p.G + g;
+                p.ws_m[at] = kPShift - st.nb[nt][j];
+                p.ws_l[at] = l;
+                if (g == 0)
+                    p.ranges[pair] = SlotRange{2 * p.blocks + pair, 1, 0, 0};
             }
         }
 }
@@ -816,7 +821,6 @@ __global__ void __launch_bounds__(DCfg<D, NT>::kThreads, 1) mx4_decode_kernel(co
     constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
     extern __shared__ __align__(128) uint8_t smem[];
     int32_t *state_pair = reinterpret_cast<int32_t *>(smem + C::kPairOff);
-    volatile int32_t *misc = reinterpret_cast<volatile int32_t *>(smem + C::kMiscOff);
     int32_t *scan = reinterpret_cast<int32_t *>(smem + C::kScanOff);
     int32_t *prefix = reinterpret_cast<int32_t *>(smem + C::kPrefixOff);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -877,6 +881,8 @@ __global__ void __launch_bounds__(DCfg<D, NT>::kThreads, 1) mx4_decode_kernel(co
             dst[i] = make_uint4(0, 0, 0, 0);
     }
     const uint32_t T = max(1u, min((uint32_t)p.blocks, (U + C::kMinPages - 1) / C::kMinPages));
+    if (tid == 0)
+        p.span_pair[blockIdx.x] = -1;
     if (blockIdx.x >= T || U == 0)
         return;
     const Shares blocks(U, T);
@@ -961,7 +967,7 @@ __global__ void __launch_bounds__(DCfg<D, NT>::kThreads, 1) mx4_decode_kernel(co
             float *logits = nullptr;
             int heads = 0;
             if constexpr (SCORED) {
-                heads = (p.G + 1) & ~1;
+                heads = p.G <= 2 ? 2 : p.G <= 4 ? 4 : p.G <= 8 ? 8 : 16;  // logit_heads(G)
                 logits = p.logits + ((int64_t)pair * capacity + (int64_t)index * kPage) * heads;
             }
             attend_record<D, NT, SCORED>(ring + stage * R::kBytes, min(kPage, len - index * kPage), lane, st, logits,
@@ -1000,197 +1006,205 @@ __global__ void __launch_bounds__(DCfg<D, NT>::kThreads, 1) mx4_decode_kernel(co
     // pair begins among them (the states of one pair are neighbours).
     constexpr int D4 = D / 4;
     const int G = p.G;
-    float *weight = reinterpret_cast<float *>(smem + C::kWeightOff);  // [head][state]
-    float *pair_m = weight + 16 * 32, *pair_l = pair_m + 16 * 32;     // [head][a pair's first state]
+    float *weight = reinterpret_cast<float *>(smem + C::kWeightOff);  // [head][n-th state]
+    float *pair_m = weight + 16 * 32, *pair_l = pair_m + 16 * 32;     // [head][n-th state, a pair's first]
     const int my_pair = lane < 2 * kWarps ? state_pair[lane] : -1;
-    const uint32_t below = (1u << lane) - 1u;
     const uint32_t there = __ballot_sync(0xffffffffu, my_pair >= 0);
+    if (there == 0)
+        return;
+    const uint32_t below = (1u << lane) - 1u;
     const int before = 31 - __clz(there & below);  // the state before this one, or -1
     const int pair_before = __shfl_sync(0xffffffffu, my_pair, before & 31);
     const uint32_t starts = __ballot_sync(0xffffffffu, my_pair >= 0 && (before < 0 || pair_before != my_pair));
-    if (there == 0)
-        return;
-    auto members = [&](uint32_t start) {  // the states of the pair that begins at this bit
-        const uint32_t later = starts & ~((start << 1) - 1u);
-        return there & ~(start - 1u) & (later ? (later & (0u - later)) - 1u : ~0u);
+    const int nth = __popc(there & below);
+    // the states of the pair that begins with state `first`: the n-th to the one before `end`
+    auto end_of = [&](int first) {
+        const uint32_t later = starts & ~((2u << first) - 1u);
+        return __popc(later ? there & ((later & (0u - later)) - 1u) : there);
     };
     for (int g = warp; g < G; g += kWarps) {
         const float *sk = state_at(lane) + C::kHeads * (D + 4) + g;
         const float m = my_pair >= 0 ? sk[0] : -INFINITY, l = my_pair >= 0 ? sk[C::kHeads] : 0.f;
         for (uint32_t left = starts; left; left &= left - 1u) {
-            const uint32_t start = left & (0u - left);
-            const bool mine = (members(start) >> lane) & 1u;
+            const int first = __ffs(left) - 1;
+            const bool mine = my_pair >= 0 && lane >= first && nth < end_of(first);
             float M = mine ? m : -INFINITY;
+#pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
             const float w = exp2_approx(m - (M == -INFINITY ? 0.f : M));
             float L = mine ? l * w : 0.f;
+#pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 L += __shfl_xor_sync(0xffffffffu, L, o);
             if (mine)
-                weight[g * 32 + lane] = w;
-            if (start >> lane == 1u) {
-                pair_m[g * 32 + lane] = M;
-                pair_l[g * 32 + lane] = L;
+                weight[g * 32 + nth] = w;
+            if (lane == first) {
+                pair_m[g * 32 + nth] = M;
+                pair_l[g * 32 + nth] = L;
             }
         }
     }
+    if (warp == 0 && my_pair >= 0)
+        state_pair[2 * kWarps + nth] = (int)(state_at(lane) - reinterpret_cast<float *>(smem));  // where the n-th lies
     __syncthreads();
-    // Where a pair's pages lie on the line.
-    auto pair_begin = [&](int which, uint32_t &pages) {
-        const int row = which / p.H_kv;
-        pages = prefix[row + 1] - prefix[row];
-        return (uint32_t)prefix[row] * p.H_kv + (uint32_t)(which - row * p.H_kv) * pages;
-    };
     for (uint32_t left = starts; left; left &= left - 1u) {
         const int first = __ffs(left) - 1;
-        const uint32_t in = members(1u << first);
+        const int n0 = __popc(there & ((1u << first) - 1u)), n1 = end_of(first);
         const int which = state_pair[first];
-        uint32_t pages;
-        const uint32_t P0 = pair_begin(which, pages);
+        const int row = which / p.H_kv;
+        const uint32_t pages = prefix[row + 1] - prefix[row];
+        const uint32_t P0 = (uint32_t)prefix[row] * p.H_kv + (uint32_t)(which - row * p.H_kv) * pages;
         const bool whole = P0 >= u0 && P0 + pages <= u1;
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (P0 > u0 ? 1 : 0);
+        const int slot = whole ? 2 * p.blocks + which : 2 * (int)blockIdx.x + (P0 > u0 ? 1 : 0);
+        if (tid == 0 && P0 >= u0 && P0 + pages > u1) {
+            // the pair begins here and reaches beyond this block
+            const int count = (int)(blocks.owner(P0 + pages - 1) - blockIdx.x) + 1;
+            const SlotRange span{slot, count, 2 * (int)blockIdx.x, 2};
+            p.spans[blockIdx.x] = span;
+            p.span_pair[blockIdx.x] = which;
+            if (SCORED)
+                p.ranges[which] = span;
+        }
+        if (SCORED && tid == 0 && whole)
+            p.ranges[which] = SlotRange{slot, 1, 0, 0};
         for (int e = tid; e < G * D4; e += kThreads) {
             const int g = e / D4, d4 = (e % D4) * 4;
-            const float *col = state_at(0) + g * (D + 4) + d4;  // of a first state; a last one's lies at the same offset
+            const float *col = reinterpret_cast<float *>(smem) + g * (D + 4) + d4;
             float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (uint32_t rest = in; rest; rest &= rest - 1u) {
-                const int k = __ffs(rest) - 1;
-                O = fma4(*reinterpret_cast<const float4 *>(col + (state_at(k) - state_at(0))), weight[g * 32 + k], O);
-            }
-            const float L = pair_l[g * 32 + first];
-            if (whole) {
+#pragma unroll 4
+            for (int k = n0; k < n1; ++k)
+                O = fma4(*reinterpret_cast<const float4 *>(col + state_pair[2 * kWarps + k]), weight[g * 32 + k], O);
+            const float L = pair_l[g * 32 + n0];
+            const int64_t at = (int64_t)slot * G + g;
+            if (whole)
                 store_bf16x4(p.out + ((int64_t)which * G + g) * D + d4, scale4(O, L == 0.f ? 0.f : 1.f / L));
-                if (SCORED && d4 == 0) {
-                    p.fin_m[(int64_t)which * G + g] = pair_m[g * 32 + first];
-                    p.fin_l[(int64_t)which * G + g] = L;
-                }
-            } else {
-                const int64_t at = slot * G + g;
+            else
                 *reinterpret_cast<float4 *>(p.ws_acc + at * D + d4) = O;
-                if (d4 == 0) {
-                    p.ws_m[at] = pair_m[g * 32 + first];
-                    p.ws_l[at] = L;
-                }
+            if (d4 == 0 && (SCORED || !whole)) {
+                p.ws_m[at] = pair_m[g * 32 + n0];
+                p.ws_l[at] = L;
             }
         }
     }
+}
 
-    // ---- pairs that span blocks: the last block to finish one merges its states ----
-    // Only the block's first and last pair can reach beyond it.
-    auto settle = [&](int which) {
-        uint32_t pages;
-        const uint32_t P0 = pair_begin(which, pages);
-        if (P0 >= u0 && P0 + pages <= u1)
-            return;
-        const uint32_t first_block = blocks.owner(P0);
-        const int count = (int)(blocks.owner(P0 + pages - 1) - first_block) + 1;
-        // the first block's state is its last pair's unless its share begins with the pair
-        const uint32_t first_slot = 2 * first_block + (blocks.begin(first_block) == P0 ? 0 : 1);
-        __syncthreads();
-        if (tid == 0)
-            misc[0] = ticket_acq_rel(p.ws_counters + which) == (uint32_t)(count - 1);
-        __syncthreads();
-        if (!misc[0])
-            return;
-        auto slot_of = [&](int i) { return i == 0 ? first_slot : 2 * (first_block + i); };
-        float *wt = reinterpret_cast<float *>(smem);   // [count][G]
-        float *norm = wt + (count * G + 3) / 4 * 4;    // [16]
-        float *parts = norm + 16;                      // [kThreads][4], 16-byte aligned
-        for (int g = warp; g < G; g += kWarps) {
-            float m0 = -INFINITY, l0 = 0.f;
-            if (lane < count) {
-                m0 = __ldcg(p.ws_m + slot_of(lane) * G + g);
-                l0 = __ldcg(p.ws_l + slot_of(lane) * G + g);
-            }
-            float M = m0;
-            for (int i = lane + 32; i < count; i += 32)
-                M = fmaxf(M, __ldcg(p.ws_m + slot_of(i) * G + g));
-            for (int o = 16; o > 0; o >>= 1)
-                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            const float base = M == -INFINITY ? 0.f : M;
-            float L = 0.f;
-            if (lane < count) {
-                const float w = exp2_approx(m0 - base);
-                wt[lane * G + g] = w;
-                L = l0 * w;
-            }
-            for (int i = lane + 32; i < count; i += 32) {
-                const float w = exp2_approx(__ldcg(p.ws_m + slot_of(i) * G + g) - base);
-                wt[i * G + g] = w;
-                L = fmaf(__ldcg(p.ws_l + slot_of(i) * G + g), w, L);
-            }
-            for (int o = 16; o > 0; o >>= 1)
-                L += __shfl_xor_sync(0xffffffffu, L, o);
-            if (lane == 0) {
-                norm[g] = L == 0.f ? 0.f : 1.f / L;
-                if (SCORED) {
-                    p.fin_m[(int64_t)which * G + g] = M;
-                    p.fin_l[(int64_t)which * G + g] = L;
-                }
-            }
+// ---------------------------------------------------------------------------
+// What follows the decode kernel: one block per (decode block, head) merges the
+// pair that begins there and reaches beyond, in ascending order of its blocks;
+// with scores, further blocks add the weights.  A launch of its own costs less
+// than letting the last of a pair's blocks merge: the tickets alone took that
+// kernel 1.3 us, and the merges ran one after another on one SM.
+
+constexpr int kFinishThreads = 256;
+static_assert(kFinishThreads == kWeightThreads, "one grid runs both");
+
+struct FinishParams {
+    WeightParams w;  // m, l, G; the rest for scores
+    const float *acc;
+    const SlotRange *spans;
+    const int32_t *span_pair;
+    __nv_bfloat16 *out;
+    int32_t blocks, chunks;
+};
+
+// LH = logit_heads(G), 0: no scores.
+template <int D, int LH>
+__global__ void __launch_bounds__(kFinishThreads) mx4_finish_kernel(const __grid_constant__ FinishParams p)
+{
+    constexpr int D4 = D / 4, kParts = kFinishThreads / D4;
+    __shared__ float4 s_o[kParts][D4];
+    __shared__ float s_m[LH > 0 ? LH : 1], s_inv[LH > 0 ? LH : 1];
+    const int G = p.w.G;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (LH > 0 && (int)blockIdx.x >= p.blocks * G) {
+        const int i = blockIdx.x - p.blocks * G;
+        add_weights<(LH > 0 ? LH : 2)>(p.w, i / p.chunks, i % p.chunks, s_m, s_inv);
+        return;
+    }
+    const int b = blockIdx.x / G, g = blockIdx.x % G;
+    const SlotRange span = p.spans[b];
+    const int pair = __ldcg(p.span_pair + b);
+    if (pair < 0)
+        return;
+    const int lane = threadIdx.x & 31, col = threadIdx.x % D4, part = threadIdx.x / D4;
+    const int i0 = span.count * part / kParts, i1 = span.count * (part + 1) / kParts;
+    // this thread's first states load while the weights are worked out
+    constexpr int kAhead = 4;
+    float4 ahead[kAhead];
+    float m_ahead[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+        if (i0 + k < i1) {
+            ahead[k] = __ldcg(reinterpret_cast<const float4 *>(p.acc + (span.slot(i0 + k) * G + g) * D) + col);
+            m_ahead[k] = __ldcg(p.w.m + span.slot(i0 + k) * G + g);
         }
-        __syncthreads();
-        // few columns: several threads share one, each over a run of the states
-        const int tasks = G * D4;
-        const int split = tasks < kThreads ? kThreads / tasks : 1;
-        for (int e0 = 0; e0 < tasks; e0 += kThreads) {
-            const int e = split > 1 ? tid % tasks : e0 + tid, part = split > 1 ? tid / tasks : 0;
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (e < tasks && part < split) {
-                const int g = e / D4, d4 = (e % D4) * 4;
-                const int i1 = count * (part + 1) / split;
-#pragma unroll 6
-                for (int i = count * part / split; i < i1; ++i)
-                    O = fma4(__ldcg(reinterpret_cast<const float4 *>(p.ws_acc + ((int64_t)slot_of(i) * G + g) * D + d4)),
-                             wt[i * G + g], O);
-            }
-            if (split > 1) {
-                reinterpret_cast<float4 *>(parts)[tid] = O;
-                __syncthreads();
-                if (part == 0)
-                    for (int k = 1; k < split; ++k)
-                        O = fma4(reinterpret_cast<const float4 *>(parts)[k * tasks + e], 1.f, O);
-            }
-            if (e < tasks && part == 0)
-                store_bf16x4(p.out + ((int64_t)which * G + e / D4) * D + (e % D4) * 4, scale4(O, norm[e / D4]));
-        }
-        if (tid == 0)
-            p.ws_counters[which] = 0u;  // ready for the next call
-        __syncthreads();
-    };
-    const int head_pair = state_pair[__ffs(starts) - 1], tail_pair = state_pair[31 - __clz(starts)];
-    settle(head_pair);
-    if (tail_pair != head_pair)
-        settle(tail_pair);
+    float m0 = -INFINITY, l0 = 0.f;
+    if (lane < span.count) {
+        m0 = __ldcg(p.w.m + span.slot(lane) * G + g);
+        l0 = __ldcg(p.w.l + span.slot(lane) * G + g);
+    }
+    float M = m0;
+    for (int i = lane + 32; i < span.count; i += 32)
+        M = fmaxf(M, __ldcg(p.w.m + span.slot(i) * G + g));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    M = M == -INFINITY ? 0.f : M;
+    float L = l0 * exp2_approx(m0 - M);
+    for (int i = lane + 32; i < span.count; i += 32)
+        L = fmaf(__ldcg(p.w.l + span.slot(i) * G + g), exp2_approx(__ldcg(p.w.m + span.slot(i) * G + g) - M), L);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        L += __shfl_xor_sync(0xffffffffu, L, o);
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+        if (i0 + k < i1)
+            O = fma4(ahead[k], exp2_approx(m_ahead[k] - M), O);
+    for (int i = i0 + kAhead; i < i1; ++i)
+        O = fma4(__ldcg(reinterpret_cast<const float4 *>(p.acc + (span.slot(i) * G + g) * D) + col),
+                 exp2_approx(__ldcg(p.w.m + span.slot(i) * G + g) - M), O);
+    s_o[part][col] = O;
+    __syncthreads();
+    if (part != 0)
+        return;
+#pragma unroll
+    for (int k = 1; k < kParts; ++k)
+        O = fma4(s_o[k][col], 1.f, O);
+    store_bf16x4(p.out + ((int64_t)pair * G + g) * D + col * 4, scale4(O, L == 0.f ? 0.f : 1.f / L));
 }
 
 // ---------------------------------------------------------------------------
 // Host side
 
-// Workspace of a 4-bit decode plan: the error word, tickets, two states per
-// block and, with PKV_FLAG_SCORES, the pairs' final states and the logits.
+// Workspace of a 4-bit decode plan: the error word, the blocks' states and
+// spans and, with PKV_FLAG_SCORES, the pairs' slots and the logits.
 struct Mx4Layout {
-    size_t counters_off, m_off, l_off, acc_off, fin_m_off, fin_l_off, logits_off, total;
+    size_t m_off, l_off, acc_off, spans_off, span_pair_off, ranges_off, logits_off, total;
+    int64_t n_slots;
 };
 
 Mx4Layout mx4_layout(const pkv_shape &s, const pkv_plan &p)
 {
     Mx4Layout w{};
-    const size_t pairs = (size_t)s.B * s.H_kv, G = (size_t)(s.H_q / s.H_kv), slots = 2 * (size_t)p.num_splits;
+    const bool scores = (p.flags & PKV_FLAG_SCORES) != 0;
+    const size_t pairs = (size_t)s.B * s.H_kv, G = (size_t)(s.H_q / s.H_kv), T = (size_t)p.num_splits;
+    w.n_slots = (int64_t)(2 * T + (scores ? pairs : 0));
     size_t off = kWsAlign;
     auto take = [&](size_t bytes) {
         const size_t at = off;
         off += round_up(bytes, kWsAlign);
         return at;
     };
-    w.counters_off = take(pairs * 4);
-    w.m_off = take(slots * G * 4);
-    w.l_off = take(slots * G * 4);
-    w.acc_off = take(slots * G * s.head_dim * 4);
-    if (p.flags & PKV_FLAG_SCORES) {
-        w.fin_m_off = take(pairs * G * 4);
-        w.fin_l_off = take(pairs * G * 4);
+    w.m_off = take((size_t)w.n_slots * G * 4);
+    w.l_off = take((size_t)w.n_slots * G * 4);
+    w.acc_off = take(2 * T * G * s.head_dim * 4);
+    w.spans_off = take(T * sizeof(SlotRange));
+    w.span_pair_off = take(T * 4);
+    if (scores) {
+        w.ranges_off = take(pairs * sizeof(SlotRange));
         w.logits_off = take(pairs * s.max_pages_per_seq * s.page_size * logit_heads((int64_t)G) * 4);
     }
     w.total = off;
@@ -1226,6 +1240,30 @@ cudaError_t launch_mx4(const DecodeParams &p, cudaStream_t st, bool pdl)
         return e;
     return launch_kernel(kernel, (unsigned)p.blocks, C::kThreads, smem, st, pdl, p);
 }
+
+template <int D>
+cudaError_t launch_decode(const DecodeParams &p, bool scores, cudaStream_t st, bool pdl)
+{
+    if (p.G <= 8)
+        return scores ? launch_mx4<D, 1, true>(p, st, pdl) : launch_mx4<D, 1, false>(p, st, pdl);
+    return scores ? launch_mx4<D, 2, true>(p, st, pdl) : launch_mx4<D, 2, false>(p, st, pdl);
+}
+
+template <int D>
+cudaError_t launch_finish(const FinishParams &p, bool scores, int64_t grid, cudaStream_t st, bool pdl)
+{
+    const unsigned n = (unsigned)grid;
+    switch (scores ? logit_heads(p.w.G) : 0) {
+    case 0: return launch_kernel(mx4_finish_kernel<D, 0>, n, kFinishThreads, 0, st, pdl, p);
+    case 2: return launch_kernel(mx4_finish_kernel<D, 2>, n, kFinishThreads, 0, st, pdl, p);
+    case 4: return launch_kernel(mx4_finish_kernel<D, 4>, n, kFinishThreads, 0, st, pdl, p);
+    case 8: return launch_kernel(mx4_finish_kernel<D, 8>, n, kFinishThreads, 0, st, pdl, p);
+    default: return launch_kernel(mx4_finish_kernel<D, 16>, n, kFinishThreads, 0, st, pdl, p);
+    }
+}
+
+// Pages below which a decode of this tile is one block's: nothing to merge.
+int min_pages(int G) { return G <= 8 ? DCfg<128, 1>::kMinPages : DCfg<128, 2>::kMinPages; }
 
 unsigned token_grid(int64_t rows, int lanes)
 {
@@ -1359,7 +1397,8 @@ int pkv_mx4_decode(const void *q, const void *pool, const int32_t *block_table, 
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(pool, 16) || !aligned(block_table, 4) ||
         !aligned(seq_lens, 4) || !aligned(scores, 4) || !aligned(workspace, 256))
         return PKV_ERR_UNSUPPORTED;
-    if (scores && weight_blocks(pairs, capacity) > INT32_MAX)
+    const int64_t merges = (int64_t)plan->num_splits * G;
+    if (scores && weight_blocks(pairs, capacity) + merges > INT32_MAX)
         return PKV_ERR_UNSUPPORTED;
     const Mx4Layout w = mx4_layout(s, *plan);
     if (workspace_bytes < w.total)
@@ -1374,10 +1413,11 @@ int pkv_mx4_decode(const void *q, const void *pool, const int32_t *block_table, 
     p.block_table = block_table;
     p.seq_lens = seq_lens;
     p.ws_error = reinterpret_cast<uint32_t *>(ws);
-    p.ws_counters = reinterpret_cast<uint32_t *>(ws + w.counters_off);
     p.ws_m = reinterpret_cast<float *>(ws + w.m_off);
     p.ws_l = reinterpret_cast<float *>(ws + w.l_off);
     p.ws_acc = reinterpret_cast<float *>(ws + w.acc_off);
+    p.spans = reinterpret_cast<SlotRange *>(ws + w.spans_off);
+    p.span_pair = reinterpret_cast<int32_t *>(ws + w.span_pair_off);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.B = s.B;
     p.H_q = s.H_q;
@@ -1387,37 +1427,45 @@ int pkv_mx4_decode(const void *q, const void *pool, const int32_t *block_table, 
     p.num_pool_pages = s.num_pool_pages;
     p.blocks = plan->num_splits;
     if (scores) {
-        p.fin_m = reinterpret_cast<float *>(ws + w.fin_m_off);
-        p.fin_l = reinterpret_cast<float *>(ws + w.fin_l_off);
+        p.ranges = reinterpret_cast<SlotRange *>(ws + w.ranges_off);
         p.logits = reinterpret_cast<float *>(ws + w.logits_off);
     }
     const cudaStream_t st = (cudaStream_t)stream;
     const bool pdl = (plan->flags & PKV_FLAG_NO_PDL) == 0;
-    cudaError_t e;
-    if (s.head_dim == 128)
-        e = G <= 8 ? (scores ? launch_mx4<128, 1, true>(p, st, pdl) : launch_mx4<128, 1, false>(p, st, pdl))
-                   : (scores ? launch_mx4<128, 2, true>(p, st, pdl) : launch_mx4<128, 2, false>(p, st, pdl));
-    else
-        e = G <= 8 ? (scores ? launch_mx4<64, 1, true>(p, st, pdl) : launch_mx4<64, 1, false>(p, st, pdl))
-                   : (scores ? launch_mx4<64, 2, true>(p, st, pdl) : launch_mx4<64, 2, false>(p, st, pdl));
+    cudaError_t e = s.head_dim == 128 ? launch_decode<128>(p, scores != nullptr, st, pdl)
+                                      : launch_decode<64>(p, scores != nullptr, st, pdl);
     if (e != cudaSuccess)
         return PKV_ERR_CUDA;
+    // a batch that can never fill one block's share leaves nothing to merge
+    if (!scores && (plan->num_splits == 1 || pairs * s.max_pages_per_seq <= min_pages(G)))
+        return PKV_OK;
+    FinishParams f{};
+    f.w.m = p.ws_m;
+    f.w.l = p.ws_l;
+    f.w.G = G;
+    f.acc = p.ws_acc;
+    f.spans = p.spans;
+    f.span_pair = p.span_pair;
+    f.out = p.out;
+    f.blocks = p.blocks;
+    f.chunks = 1;
     if (scores) {
-        WeightParams x{};
-        x.logits = p.logits;
-        x.m = p.fin_m;
-        x.l = p.fin_l;
-        x.seq_lens = seq_lens;
-        x.scores = scores;
-        x.stride_row = score_stride_row;
-        x.stride_head = score_stride_head;
-        x.H_kv = s.H_kv;
-        x.G = G;
-        x.capacity = capacity;
-        x.n_slots = pairs;
-        if (launch_add_weights(x, pairs, st, pdl) != cudaSuccess)
-            return PKV_ERR_CUDA;
+        f.w.logits = p.logits;
+        f.w.ranges = p.ranges;
+        f.w.seq_lens = seq_lens;
+        f.w.scores = scores;
+        f.w.stride_row = score_stride_row;
+        f.w.stride_head = score_stride_head;
+        f.w.H_kv = s.H_kv;
+        f.w.capacity = capacity;
+        f.w.n_slots = w.n_slots;
+        f.chunks = (int32_t)weight_blocks(1, capacity);
     }
+    const int64_t grid = merges + (scores ? weight_blocks(pairs, capacity) : 0);
+    e = s.head_dim == 128 ? launch_finish<128>(f, scores != nullptr, grid, st, pdl)
+                          : launch_finish<64>(f, scores != nullptr, grid, st, pdl);
+    if (e != cudaSuccess)
+        return PKV_ERR_CUDA;
     return PKV_OK;
 }
 
