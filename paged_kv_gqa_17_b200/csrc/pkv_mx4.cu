@@ -300,7 +300,10 @@ __global__ void __launch_bounds__(kTokenThreads) mx4_read_kernel(const __grid_co
 
 constexpr int kMaxRows = 4096;       // rows whose page offsets a block keeps in shared memory
 constexpr int kMaxBlocks = 1024;
-constexpr float kPShift = 15.f;      // P is held times 2^15: the top of f16's range
+// P is held times 2^kPShift relative to the reference max and may grow to
+// 2^kPTop, the top of f16's range, before the reference has to move.
+constexpr float kPShift = 8.f, kPTop = 15.f;
+constexpr float kPUnit = 0x1p-8f;    // 2^-kPShift
 
 struct DecodeParams {
     const __nv_bfloat16 *q;
@@ -330,8 +333,9 @@ struct DCfg {
     static constexpr int kMinPages = 2 * kWarps;  // a smaller share costs more in merging than it saves
     static constexpr int kHeads = 8 * NT;
     static constexpr int kState = kHeads * (D + 4) + 2 * kHeads;  // floats: o (rows padded), m, l
-    static constexpr int kStages = D == 128 && NT == 1 ? 4 : 6;
-    static constexpr int kWarpRing = kStages * Rec<D>::kBytes;
+    static constexpr int kStages = D == 128 && NT == 1 ? 2 : 3;  // of two pages each
+    static constexpr int kStageBytes = 2 * Rec<D>::kBytes;
+    static constexpr int kWarpRing = kStages * kStageBytes;
     static_assert(kState * 4 <= kWarpRing, "a warp's last state takes the place of its ring");
     static constexpr int kFirstOff = kWarps * kWarpRing;  // the states of the warps' first runs
     static constexpr int kBarOff = kFirstOff + kWarps * kState * 4;
@@ -378,12 +382,12 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
 }
 
 // A warp's running state for one pair: heads 8 nt + 2 c + {0, 1}.  o is in units of
-// 2^(vref(b) - 142) for its block b of 32 dims, l in units of 2^-15.
+// 2^(vref(b) - 127 - kPShift) for its block b of 32 dims, l in units of 2^-kPShift.
 template <int D, int NT>
 struct State {
     uint32_t qf[D / 16][NT][2];  // q as the MMA's B operand
     float sl[NT][2];             // logit = product * sl (log2 domain)
-    float nb[NT][2];             // 15 - m, with m the reference max (log2 domain): P is 2^(logit + nb)
+    float nb[NT][2];             // kPShift - m, with m the reference max (log2 domain): P is 2^(logit + nb)
     float l[NT][2];
     float o[D / 16][NT][4];
     uint32_t vlow;               // per block the lower end of its window of V's scales, 0 .. 247; ~0: none yet
@@ -474,31 +478,28 @@ __device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t
 }
 
 // The largest scale byte (255 aside) of block b over the valid tokens, for the whole warp.
-__device__ __forceinline__ int top_scale(const uint32_t (&vs)[4], const int (&vt)[4], int nvalid, int b)
+__device__ __forceinline__ int top_scale(const uint32_t (&vs)[4], int lane, int nvalid, int b)
 {
     int top = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int e = (vs[i] >> (8 * b)) & 255;
-        if (vt[i] < nvalid && e < 255)
+        if (2 * (lane & 3) + (i & 1) + 4 * (i & 2) < nvalid && e < 255)
             top = max(top, e);
     }
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     return max(top, __shfl_xor_sync(0xffffffffu, top, 2));
 }
 
-// One page in shared memory (rec) into the state.  `release` runs once the
-// record has been read.
-template <int D, int NT, bool SCORED, typename F>
-__device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, int lane, State<D, NT> &st,
-                                              float *logits, int logit_heads, F release)
+// S^T = K q^T of one page, each block of 32 dims under its tokens' scales:
+// rows are tokens r and r + 8, columns heads 8 nt + 2c and 2c + 1.
+template <int D, int NT>
+__device__ __forceinline__ void page_products(const uint8_t *rec, int lane, const State<D, NT> &st, float (&s)[NT][4])
 {
     using R = Rec<D>;
     constexpr int kBlocks = D / 32;
     const int r = lane >> 2, c = lane & 3;
-    // K codes of tokens r and r + 8, V codes of tokens 2c, 2c + 1, 2c + 8, 2c + 9, their scales
-    uint32_t ka[kBlocks], kb[kBlocks], vw[4][kBlocks / 2], ksa, ksb, vs[4];
-    const int vt[4] = {2 * c, 2 * c + 1, 2 * c + 8, 2 * c + 9};
+    uint32_t ka[kBlocks], kb[kBlocks], ksa, ksb;
     if constexpr (D == 128) {
         const uint4 a4 = *reinterpret_cast<const uint4 *>(rec + r * R::kRow + c * 16);
         const uint4 b4 = *reinterpret_cast<const uint4 *>(rec + (r + 8) * R::kRow + c * 16);
@@ -506,16 +507,6 @@ __device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, in
         kb[0] = b4.x, kb[1] = b4.y, kb[2] = b4.z, kb[3] = b4.w;
         ksa = *reinterpret_cast<const uint32_t *>(rec + R::kKs + r * 4);
         ksb = *reinterpret_cast<const uint32_t *>(rec + R::kKs + (r + 8) * 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint2 v2 = *reinterpret_cast<const uint2 *>(rec + R::kV + vt[i] * R::kRow + r * 8);
-            vw[i][0] = v2.x, vw[i][1] = v2.y;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            const uint2 s2 = *reinterpret_cast<const uint2 *>(rec + R::kVs + vt[i] * 4);
-            vs[i] = s2.x, vs[i + 1] = s2.y;
-        }
     } else {
         const uint2 a2 = *reinterpret_cast<const uint2 *>(rec + r * R::kRow + c * 8);
         const uint2 b2 = *reinterpret_cast<const uint2 *>(rec + (r + 8) * R::kRow + c * 8);
@@ -523,19 +514,7 @@ __device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, in
         kb[0] = b2.x, kb[1] = b2.y;
         ksa = *reinterpret_cast<const uint16_t *>(rec + R::kKs + r * 2);
         ksb = *reinterpret_cast<const uint16_t *>(rec + R::kKs + (r + 8) * 2);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            vw[i][0] = *reinterpret_cast<const uint32_t *>(rec + R::kV + vt[i] * R::kRow + r * 4);
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            const uint32_t s2 = *reinterpret_cast<const uint32_t *>(rec + R::kVs + vt[i] * 2);
-            vs[i] = s2 & 0xffffu, vs[i + 1] = s2 >> 16;
-        }
     }
-    release();
-
-    // ---- S^T = K q^T, each block of 32 dims under its tokens' scales ----
-    float s[NT][4];
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
         uint32_t fa[4], fb[4];
@@ -552,147 +531,101 @@ __device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, in
                 s[nt][i] = b == 0 ? part[i] * (i < 2 ? sa : sb) : fmaf(part[i], i < 2 ? sa : sb, s[nt][i]);
         }
     }
+}
 
-    // ---- softmax against the reference max ----
-    const bool lo_ok = r < nvalid, hi_ok = r + 8 < nvalid;
-    float t[NT][4], top = -INFINITY;
+// V codes of tokens 2c, 2c + 1, 2c + 8, 2c + 9 of a page for dims of row r of
+// V^T, two tokens side by side (even dims, odd dims), and the tokens' scales.
+template <int D>
+__device__ __forceinline__ void load_values(const uint8_t *rec, int lane, uint32_t (&ve)[2][D / 64],
+                                            uint32_t (&vo)[2][D / 64])
+{
+    using R = Rec<D>;
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint8_t *a = rec + R::kV + (2 * c + 8 * i) * R::kRow + r * (D / 16);
+        if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(a), y = *reinterpret_cast<const uint2 *>(a + R::kRow);
+            interleave(x.x, y.x, ve[i][0], vo[i][0]);
+            interleave(x.y, y.y, ve[i][1], vo[i][1]);
+        } else {
+            interleave(*reinterpret_cast<const uint32_t *>(a), *reinterpret_cast<const uint32_t *>(a + R::kRow),
+                       ve[i][0], vo[i][0]);
+        }
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void load_value_scales(const uint8_t *rec, int lane, uint32_t (&vs)[4])
+{
+    using R = Rec<D>;
+    const int c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const uint8_t *a = rec + R::kVs + (2 * c + 4 * i) * R::kScaleRow;
+        if constexpr (D == 128) {
+            const uint2 s2 = *reinterpret_cast<const uint2 *>(a);
+            vs[i] = s2.x, vs[i + 1] = s2.y;
+        } else {
+            const uint32_t s2 = *reinterpret_cast<const uint32_t *>(a);
+            vs[i] = s2 & 0xffffu, vs[i + 1] = s2 >> 16;
+        }
+    }
+}
+
+// O^T += V^T (P V-scale)^T of one page whose scales lie in their windows, d
+// steps (a byte per block) above the lower ends: P times 2^(d - 7) in f16.
+template <int D, int NT>
+__device__ __forceinline__ void add_values(const uint8_t *rec, int lane, State<D, NT> &st, const float (&pr)[NT][4],
+                                           const uint32_t (&d)[4])
+{
+    uint32_t ve[2][D / 64], vo[2][D / 64], pt[NT][2];
+    load_values<D>(rec, lane, ve, vo);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+        pt[nt][0] = movmatrix_trans(pack_f16(pr[nt][0], pr[nt][1]));
+        pt[nt][1] = movmatrix_trans(pack_f16(pr[nt][2], pr[nt][3]));
+    }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // an infinite product comes of a NaN scale (255): + 0 * s makes it NaN
-            t[nt][i] = fmaf(s[nt][i], 0.f, fmaf(s[nt][i], st.sl[nt][i & 1], st.nb[nt][i & 1]));
-        }
-        if constexpr (SCORED) {
-            const int g = 8 * nt + 2 * c;
-            if (g < logit_heads) {
-                float x[4];
+    for (int w = 0; w < D / 64; ++w) {
+        uint32_t e0[4], o0[4], e1[4], o1[4];
+        codes_to_half2(ve[0][w], e0);
+        codes_to_half2(vo[0][w], o0);
+        codes_to_half2(ve[1][w], e1);
+        codes_to_half2(vo[1][w], o1);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[i] = fmaf(s[nt][i], 0.f, s[nt][i] * st.sl[nt][i & 1]);
-                if (lo_ok)
-                    *reinterpret_cast<float2 *>(logits + r * logit_heads + g) = make_float2(x[0], x[1]);
-                if (hi_ok)
-                    *reinterpret_cast<float2 *>(logits + (r + 8) * logit_heads + g) = make_float2(x[2], x[3]);
+        for (int k = 0; k < 2; ++k) {
+            const int b = 2 * w + k;
+            // two tokens' steps of block b as the high bytes of two halves (a byte below 128
+            // replicates a zero sign into the low ones), then 2^(step - 7) by its exponent field
+            const uint32_t sel = (uint32_t)((8 | b) | b << 4 | (8 | 4 | b) << 8 | (4 | b) << 12);
+            uint32_t f0, f1;
+            asm("prmt.b32 %0, %1, %2, %3;" : "=r"(f0) : "r"(d[0]), "r"(d[1]), "r"(sel));
+            asm("prmt.b32 %0, %1, %2, %3;" : "=r"(f1) : "r"(d[2]), "r"(d[3]), "r"(sel));
+            f0 = f0 * 4u + 0x20002000u;
+            f1 = f1 * 4u + 0x20002000u;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t p0 = mul_f16x2(pt[nt][0], f0), p1 = mul_f16x2(pt[nt][1], f1);
+                mma_f16(st.o[2 * b][nt], e0[2 * k], o0[2 * k], e1[2 * k], o1[2 * k], p0, p1);
+                mma_f16(st.o[2 * b + 1][nt], e0[2 * k + 1], o0[2 * k + 1], e1[2 * k + 1], o1[2 * k + 1], p0, p1);
             }
         }
     }
-    if (nvalid < kPage) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (!(i < 2 ? lo_ok : hi_ok))
-                    t[nt][i] = -INFINITY;
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-        top = fmaxf(top, fmaxf(fmaxf(t[nt][0], t[nt][1]), fmaxf(t[nt][2], t[nt][3])));
-    if (__any_sync(0xffffffffu, top > kPShift)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float x0 = fmaf(s[nt][j], 0.f, s[nt][j] * st.sl[nt][j]);
-                float x1 = fmaf(s[nt][2 + j], 0.f, s[nt][2 + j] * st.sl[nt][j]);
-                x0 = lo_ok ? x0 : -INFINITY;
-                x1 = hi_ok ? x1 : -INFINITY;
-                const float old = kPShift - st.nb[nt][j];
-                float mx = fmaxf(fmaxf(x0, x1), old);
-#pragma unroll
-                for (int sh = 4; sh < 32; sh <<= 1)
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-                // a head with nothing but NaN so far: -inf - -inf, NaN as its sums are
-                const float al = exp2_approx(old - mx);
-                st.nb[nt][j] = kPShift - mx;
-                t[nt][j] = x0 + st.nb[nt][j];
-                t[nt][2 + j] = x1 + st.nb[nt][j];
-                st.l[nt][j] *= al;
-#pragma unroll
-                for (int mt = 0; mt < D / 16; ++mt) {
-                    st.o[mt][nt][j] *= al;
-                    st.o[mt][nt][2 + j] *= al;
-                }
-            }
-    }
-    float pr[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            pr[nt][i] = exp2_approx(t[nt][i]);
-        st.l[nt][0] += pr[nt][0] + pr[nt][2];
-        st.l[nt][1] += pr[nt][1] + pr[nt][3];
-    }
+}
 
-    // ---- O^T += V^T (P V-scale)^T ----
-    if (st.vlow == ~0u) {
-        // the pair's first page sets each block's window, up to two steps above its largest scale
-        st.vlow = 0;
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-            st.vlow |= (uint32_t)min(max(top_scale(vs, vt, nvalid, b) - 5, 0), 247) << (8 * b);
-    }
-    uint32_t ve[2][kBlocks / 2], vo[2][kBlocks / 2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int w = 0; w < kBlocks / 2; ++w)
-            interleave(vw[2 * i][w], vw[2 * i + 1][w], ve[i][w], vo[i][w]);
-    // Steps of the tokens' scales above the windows' lower ends, a byte per
-    // block: in their windows iff every byte is 0 .. 7.  (A byte below its
-    // window borrows, but is itself at least 256 - 247 then.)
-    uint32_t d[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        d[i] = vs[i] - st.vlow;
-    if (nvalid < kPage) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (vt[i] >= nvalid)
-                d[i] = 0;
-    }
-    if (!__any_sync(0xffffffffu, ((d[0] | d[1] | d[2] | d[3]) & 0xf8f8f8f8u) != 0)) {
-        uint32_t pt[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            pt[nt][0] = movmatrix_trans(pack_f16(pr[nt][0], pr[nt][1]));
-            pt[nt][1] = movmatrix_trans(pack_f16(pr[nt][2], pr[nt][3]));
-        }
-#pragma unroll
-        for (int w = 0; w < kBlocks / 2; ++w) {
-            uint32_t e0[4], o0[4], e1[4], o1[4];
-            codes_to_half2(ve[0][w], e0);
-            codes_to_half2(vo[0][w], o0);
-            codes_to_half2(ve[1][w], e1);
-            codes_to_half2(vo[1][w], o1);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int b = 2 * w + k;
-                // two tokens' steps of block b as the high bytes of two halves (a byte below 128
-                // replicates a zero sign into the low ones), then 2^(step - 7) by its exponent field
-                const uint32_t sel = (uint32_t)((8 | b) | b << 4 | (8 | 4 | b) << 8 | (4 | b) << 12);
-                uint32_t f0, f1;
-                asm("prmt.b32 %0, %1, %2, %3;" : "=r"(f0) : "r"(d[0]), "r"(d[1]), "r"(sel));
-                asm("prmt.b32 %0, %1, %2, %3;" : "=r"(f1) : "r"(d[2]), "r"(d[3]), "r"(sel));
-                f0 = f0 * 4u + 0x20002000u;
-                f1 = f1 * 4u + 0x20002000u;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint32_t p0 = mul_f16x2(pt[nt][0], f0), p1 = mul_f16x2(pt[nt][1], f1);
-                    mma_f16(st.o[2 * b][nt], e0[2 * k], o0[2 * k], e1[2 * k], o1[2 * k], p0, p1);
-                    mma_f16(st.o[2 * b + 1][nt], e0[2 * k + 1], o0[2 * k + 1], e1[2 * k + 1], o1[2 * k + 1], p0, p1);
-                }
-            }
-        }
-        return;
-    }
-    // Some scale lies outside its window.  A larger one moves the window up;
-    // then bf16 takes the product: e2m1 as f16 bits shifted down by three is
-    // the same value times 2^-112 in bf16, and P 2^(scale - vref + 127) undoes that.
+// The same where some scale lies outside its window.  A larger one moves the
+// window up; then bf16 takes the product: e2m1 as f16 bits shifted down by
+// three is the same value times 2^-112 in bf16, which P 2^(scale - vref + 112) undoes.
+template <int D, int NT>
+__device__ __forceinline__ void add_values_wide(const uint8_t *rec, int nvalid, int lane, State<D, NT> &st,
+                                                const float (&pr)[NT][4], const uint32_t (&vs)[4])
+{
+    constexpr int kBlocks = D / 32;
+    const int r = lane >> 2;
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
-        const int top_b = top_scale(vs, vt, nvalid, b);
+        const int top_b = top_scale(vs, lane, nvalid, b);
         if (top_b > st.vref(b)) {
             const int up = top_b - st.vref(b);  // 1 .. 247
             const float f = up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23);
@@ -710,6 +643,8 @@ __device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, in
     const uint32_t even_lo = __shfl_sync(0xffffffffu, vs[0], r >> 1), odd_lo = __shfl_sync(0xffffffffu, vs[1], r >> 1);
     const uint32_t even_hi = __shfl_sync(0xffffffffu, vs[2], r >> 1), odd_hi = __shfl_sync(0xffffffffu, vs[3], r >> 1);
     const uint32_t vs_lo = r & 1 ? odd_lo : even_lo, vs_hi = r & 1 ? odd_hi : even_hi;
+    uint32_t ve[2][D / 64], vo[2][D / 64];
+    load_values<D>(rec, lane, ve, vo);
 #pragma unroll
     for (int w = 0; w < kBlocks / 2; ++w) {
         uint32_t a[4][4];
@@ -731,10 +666,11 @@ __device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, in
                        : e == 255u              ? __uint_as_float(0x7fc00000u)
                                                 : __uint_as_float((uint32_t)x << 23);
             };
-            const float f0 = factor((vs_lo >> (8 * b)) & 255u, lo_ok), f1 = factor((vs_hi >> (8 * b)) & 255u, hi_ok);
+            const float f0 = factor((vs_lo >> (8 * b)) & 255u, r < nvalid);
+            const float f1 = factor((vs_hi >> (8 * b)) & 255u, r + 8 < nvalid);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                // P holds 2^15 too much for bf16's top: 2^-15 first, then the factor
+                // P reaches 2^15: 2^-15 first, then the factor, up to 2^127
                 const float q0 = pr[nt][0] * 0x1p-15f * f0, q1 = pr[nt][1] * 0x1p-15f * f0;
                 const float q2 = pr[nt][2] * 0x1p-15f * f1, q3 = pr[nt][3] * 0x1p-15f * f1;
                 const uint32_t p0 = movmatrix_trans(pack_bf16(q0, q1)), p1 = movmatrix_trans(pack_bf16(q2, q3));
@@ -744,6 +680,225 @@ __device__ __forceinline__ void attend_record(const uint8_t *rec, int nvalid, in
             }
         }
     }
+}
+
+// Two neighbouring pages of a stage (records rec and rec + 17 D) into the
+// state, nv[h] valid tokens each (0: not this pair's page; whatever the record
+// holds is masked).  Two at once share the vote on the reference max, the
+// loop and its barriers, and give the scheduler independent products.
+template <int D, int NT, bool SCORED>
+__device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)[2], int lane, State<D, NT> &st,
+                                             float *logits, int logit_heads)
+{
+    using R = Rec<D>;
+    constexpr int kBlocks = D / 32;
+    const int r = lane >> 2, c = lane & 3;
+    float s[2][NT][4], t[2][NT][4], top = -INFINITY;
+    const bool full = nv[0] == kPage && nv[1] == kPage;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        page_products<D, NT>(rec + h * R::kBytes, lane, st, s[h]);
+
+    // ---- softmax against the reference max ----
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                // an infinite product comes of a NaN scale (255): + 0 * s makes it NaN
+                t[h][nt][i] = fmaf(s[h][nt][i], 0.f, fmaf(s[h][nt][i], st.sl[nt][i & 1], st.nb[nt][i & 1]));
+            if constexpr (SCORED) {
+                const int g = 8 * nt + 2 * c;
+                if (g < logit_heads) {
+                    float x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[i] = fmaf(s[h][nt][i], 0.f, s[h][nt][i] * st.sl[nt][i & 1]);
+                    float *dst = logits + (h * kPage + r) * logit_heads + g;
+                    if (r < nv[h])
+                        *reinterpret_cast<float2 *>(dst) = make_float2(x[0], x[1]);
+                    if (r + 8 < nv[h])
+                        *reinterpret_cast<float2 *>(dst + 8 * logit_heads) = make_float2(x[2], x[3]);
+                }
+            }
+        }
+    if (!full) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (r + (i < 2 ? 0 : 8) >= nv[h])
+                        t[h][nt][i] = -INFINITY;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                top = fmaxf(top, t[h][nt][i]);
+    if (__any_sync(0xffffffffu, top > kPTop)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float old = kPShift - st.nb[nt][j];
+                float x[2][2], mx = old;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float v = s[h][nt][2 * k + j];
+                        x[h][k] = r + 8 * k < nv[h] ? fmaf(v, 0.f, v * st.sl[nt][j]) : -INFINITY;
+                        mx = fmaxf(mx, x[h][k]);
+                    }
+#pragma unroll
+                for (int sh = 4; sh < 32; sh <<= 1)
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+                // a head with nothing but NaN so far: -inf - -inf, NaN as its sums are
+                const float al = exp2_approx(old - mx);
+                st.nb[nt][j] = kPShift - mx;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        t[h][nt][2 * k + j] = x[h][k] + st.nb[nt][j];
+                st.l[nt][j] *= al;
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt) {
+                    st.o[mt][nt][j] *= al;
+                    st.o[mt][nt][2 + j] *= al;
+                }
+            }
+    }
+    // the exponentials take the logits' place
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                t[h][nt][i] = exp2_approx(t[h][nt][i]);
+            st.l[nt][0] += t[h][nt][0] + t[h][nt][2];
+            st.l[nt][1] += t[h][nt][1] + t[h][nt][3];
+        }
+
+    // ---- the values ----
+    uint32_t vs[2][4], d[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        load_value_scales<D>(rec + h * R::kBytes, lane, vs[h]);
+    if (st.vlow == ~0u) {
+        // the pair's first pages set each block's window, up to two steps above its largest scale
+        st.vlow = 0;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            const int top_b = max(top_scale(vs[0], lane, nv[0], b), top_scale(vs[1], lane, nv[1], b));
+            st.vlow |= (uint32_t)min(max(top_b - 5, 0), 247) << (8 * b);
+        }
+    }
+    // Steps of the tokens' scales above the windows' lower ends, a byte per
+    // block: in their windows iff every byte is 0 .. 7.  (A byte below its
+    // window borrows, but is itself at least 256 - 247 then.)
+    uint32_t out_of = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            d[h][i] = vs[h][i] - st.vlow;
+    if (!full) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (2 * c + (i & 1) + 4 * (i & 2) >= nv[h])
+                    d[h][i] = 0;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        out_of |= d[h][0] | d[h][1] | d[h][2] | d[h][3];
+    if (!__any_sync(0xffffffffu, (out_of & 0xf8f8f8f8u) != 0)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            add_values<D, NT>(rec + h * R::kBytes, lane, st, t[h], d[h]);
+    } else {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            float pr[NT][4];
+            uint32_t v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = h ? vs[1][i] : vs[0][i];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    pr[nt][i] = h ? t[1][nt][i] : t[0][nt][i];
+            }
+            add_values_wide<D, NT>(rec + h * R::kBytes, h ? nv[1] : nv[0], lane, st, pr, v);
+        }
+    }
+}
+
+// The same for two whole pages whose logits stay in reach of the reference
+// max and whose V scales lie in their windows, as nearly all do: no masks, no
+// rescaling.  False, with the state unchanged, where they do not.
+template <int D, int NT, bool SCORED>
+__device__ __forceinline__ bool attend_whole_pages(const uint8_t *rec, int lane, State<D, NT> &st, float *logits,
+                                                   int logit_heads)
+{
+    using R = Rec<D>;
+    const int r = lane >> 2, c = lane & 3;
+    float t[2][NT][4], top = -INFINITY;
+    uint32_t out_of = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        page_products<D, NT>(rec + h * R::kBytes, lane, st, t[h]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (SCORED) {
+                const int g = 8 * nt + 2 * c;
+                if (g < logit_heads) {
+                    float x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[i] = fmaf(t[h][nt][i], 0.f, t[h][nt][i] * st.sl[nt][i & 1]);
+                    float *dst = logits + (h * kPage + r) * logit_heads + g;
+                    *reinterpret_cast<float2 *>(dst) = make_float2(x[0], x[1]);
+                    *reinterpret_cast<float2 *>(dst + 8 * logit_heads) = make_float2(x[2], x[3]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                t[h][nt][i] = fmaf(t[h][nt][i], 0.f, fmaf(t[h][nt][i], st.sl[nt][i & 1], st.nb[nt][i & 1]));
+                top = fmaxf(top, t[h][nt][i]);
+            }
+        }
+        uint32_t vs[4];
+        load_value_scales<D>(rec + h * R::kBytes, lane, vs);
+        out_of |= (vs[0] - st.vlow) | (vs[1] - st.vlow) | (vs[2] - st.vlow) | (vs[3] - st.vlow);
+    }
+    if (__any_sync(0xffffffffu, top > kPTop || (out_of & 0xf8f8f8f8u) != 0))
+        return false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                t[h][nt][i] = exp2_approx(t[h][nt][i]);
+            st.l[nt][0] += t[h][nt][0] + t[h][nt][2];
+            st.l[nt][1] += t[h][nt][1] + t[h][nt][3];
+        }
+        uint32_t d[4];
+        load_value_scales<D>(rec + h * R::kBytes, lane, d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            d[i] -= st.vlow;
+        add_values<D, NT>(rec + h * R::kBytes, lane, st, t[h], d);
+    }
+    return true;
 }
 
 // A warp's finished state to shared memory, in true units: o [head][D + 4], m, l per head.
@@ -764,15 +919,15 @@ __device__ __forceinline__ void put_state(float *dst, int lane, const State<D, N
                 l += __shfl_xor_sync(0xffffffffu, l, sh);
             if (r == 0) {
                 dm[g] = kPShift - st.nb[nt][j];
-                dl[g] = l * 0x1p-15f;
+                dl[g] = l * kPUnit;
             }
 #pragma unroll
             for (int b = 0; b < D / 32; ++b) {
-                // 2^(vref - 142) in two steps: 2^-15, then the exponent byte itself
+                // 2^(vref - 127 - kPShift) in two steps, the exponent byte itself the second
                 const float f = __uint_as_float((uint32_t)st.vref(b) << 23);
                 *reinterpret_cast<float4 *>(dst + g * (D + 4) + 32 * b + 4 * r) =
-                    make_float4(st.o[2 * b][nt][j] * 0x1p-15f * f, st.o[2 * b][nt][2 + j] * 0x1p-15f * f,
-                                st.o[2 * b + 1][nt][j] * 0x1p-15f * f, st.o[2 * b + 1][nt][2 + j] * 0x1p-15f * f);
+                    make_float4(st.o[2 * b][nt][j] * kPUnit * f, st.o[2 * b][nt][2 + j] * kPUnit * f,
+                                st.o[2 * b + 1][nt][j] * kPUnit * f, st.o[2 * b + 1][nt][2 + j] * kPUnit * f);
             }
         }
 }
@@ -793,8 +948,8 @@ __device__ __forceinline__ void write_pair(const DecodeParams &p, int pair, int 
                 l += __shfl_xor_sync(0xffffffffu, l, sh);
             if (g >= p.G)
                 continue;
-            l *= 0x1p-15f;
-            const float inv = (l == 0.f ? 0.f : 1.f / l) * 0x1p-15f;
+            l *= kPUnit;
+            const float inv = (l == 0.f ? 0.f : 1.f / l) * kPUnit;
             __nv_bfloat16 *dst = p.out + ((int64_t)pair * p.G + g) * D;
 #pragma unroll
             for (int b = 0; b < D / 32; ++b) {
@@ -920,14 +1075,16 @@ __global__ void __launch_bounds__(DCfg<D, NT>::kThreads, 1) mx4_decode_kernel(co
         }
         src = p.pool + (int64_t)phys * p.stride_page + (int64_t)head * p.stride_head;
     };
-    auto issue = [&](const uint8_t *src, int s) {
-        mbar_expect_tx(bars + 8 * s, R::kBytes);
-        bulk_g2s(ring_addr + s * R::kBytes, src, R::kBytes, bars + 8 * s);
+    // stage s: pages 2 k and 2 k + 1 (the last stage may hold one), each copied by the lane that holds it
+    auto issue = [&](const uint8_t *src, int j, int s) {
+        if ((j & 1) == 0)
+            mbar_expect_tx(bars + 8 * s, j + 1 < n ? C::kStageBytes : R::kBytes);
+        bulk_g2s(ring_addr + s * C::kStageBytes + (j & 1) * R::kBytes, src, R::kBytes, bars + 8 * s);
     };
     locate(lane, cur_src, cur_pair);
     __syncwarp();  // the barriers' initialisation
-    if (lane < C::kStages && lane < n)
-        issue(cur_src, lane);
+    if (lane < 2 * C::kStages && lane < n)
+        issue(cur_src, lane, lane >> 1);
     if (n > 32)
         locate(32 + lane, next_src, next_pair);
     first_index = __shfl_sync(0xffffffffu, first_index, 0);
@@ -942,44 +1099,58 @@ __global__ void __launch_bounds__(DCfg<D, NT>::kThreads, 1) mx4_decode_kernel(co
     State<D, NT> st;
     int stage = 0, phase = 0;
     bool ok = true;
-    for (int j = 0; j < n && ok;) {
+    for (int j = 0; j < n && ok;) {  // a pair's run of pages
         const int pair = __shfl_sync(0xffffffffu, cur_pair, j & 31);
         const int row = pair / p.H_kv;
         const int len = row_len(row, false);
         const int pages = prefix[row + 1] - prefix[row];
         const int begin = j == 0 ? first_index : 0;
         const int end = min(pages, begin + n - j);
+        const int run = j;
         load_q<D, NT>(p, pair, lane, st);
-        for (int index = begin; index < end; ++index) {
-            const uint32_t bar = bars + 8 * stage;
-            if (!mbar_try_wait(bar, phase))
-                ok = mbar_wait(bar, phase, p.ws_error);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) {
-                // give up on the pair, but not before the copies in flight had their time to land
-                for (int k = 1; k < C::kStages && j + k < n; ++k) {
-                    stage = stage + 1 == C::kStages ? 0 : stage + 1;
-                    phase ^= stage == 0;
-                    mbar_wait(bars + 8 * stage, phase, p.ws_error);
+        for (int index = begin; index < end;) {
+            // the stage's first page is index - at; one that begins inside a stage finds it landed already
+            const int at = j & 1;
+            if (at == 0 || j == run) {
+                const uint32_t bar = bars + 8 * stage;
+                if (!mbar_try_wait(bar, phase))
+                    ok = mbar_wait(bar, phase, p.ws_error);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) {
+                    // give up on the pair, but not before the copies in flight had their time to land
+                    for (int k = 1; k < C::kStages && (j & ~1) + 2 * k < n; ++k) {
+                        stage = stage + 1 == C::kStages ? 0 : stage + 1;
+                        phase ^= stage == 0;
+                        mbar_wait(bars + 8 * stage, phase, p.ws_error);
+                    }
+                    break;
                 }
-                break;
             }
+            const int take = min(2 - at, end - index);
+            const int tokens = len - index * kPage;  // left in the row
+            const int nv[2] = {at ? 0 : min(kPage, tokens),
+                               at ? min(kPage, tokens) : take == 2 ? min(kPage, tokens - kPage) : 0};
             float *logits = nullptr;
             int heads = 0;
             if constexpr (SCORED) {
                 heads = p.G <= 2 ? 2 : p.G <= 4 ? 4 : p.G <= 8 ? 8 : 16;  // logit_heads(G)
-                logits = p.logits + ((int64_t)pair * capacity + (int64_t)index * kPage) * heads;
+                logits = p.logits + ((int64_t)pair * capacity + (int64_t)(index - at) * kPage) * heads;
             }
-            attend_record<D, NT, SCORED>(ring + stage * R::kBytes, min(kPage, len - index * kPage), lane, st, logits,
-                                         heads, [&]() {
-                __syncwarp();
-                const int k = j + C::kStages;  // the page that takes this one's place
-                if (lane == (k & 31) && k < n)
-                    issue(((k ^ j) & ~31) == 0 ? cur_src : next_src, stage);
-            });
+            const uint8_t *rec = ring + stage * C::kStageBytes;
+            if (nv[0] < kPage || nv[1] < kPage || st.vlow == ~0u ||
+                !attend_whole_pages<D, NT, SCORED>(rec, lane, st, logits, heads))
+                attend_pages<D, NT, SCORED>(rec, nv, lane, st, logits, heads);
+            index += take;
+            j += take;
+            if ((j & 1) && j < n)
+                continue;  // the stage's second page is another pair's
+            __syncwarp();
+            // the pages that take this stage's place
+            const int k = ((j + 1) & ~1) + 2 * (C::kStages - 1);
+            if ((lane & ~1) == (k & 31) && k + (lane & 1) < n)
+                issue(((k ^ (j - 1)) & ~31) == 0 ? cur_src : next_src, k + (lane & 1), stage);
             stage = stage + 1 == C::kStages ? 0 : stage + 1;
             phase ^= stage == 0;
-            ++j;
             if ((j & 31) == 0) {
                 cur_src = next_src;
                 cur_pair = next_pair;
@@ -992,7 +1163,7 @@ __global__ void __launch_bounds__(DCfg<D, NT>::kThreads, 1) mx4_decode_kernel(co
             write_pair<D, NT, SCORED>(p, pair, lane, st);
         } else {
             // the first run where it is not whole begins this warp's share; any other reaches its end
-            const int i = 2 * warp + (j - (end - begin) > 0 ? 1 : 0);
+            const int i = 2 * warp + (run > 0 ? 1 : 0);
             put_state<D, NT>(state_at(i), lane, st);
             if (lane == 0)
                 state_pair[i] = pair;
