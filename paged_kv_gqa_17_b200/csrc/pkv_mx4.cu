@@ -145,72 +145,117 @@ struct ReadParams {
 
 constexpr int kTokenThreads = 256;
 
-// Quantises K and V of the new tokens into their slots.  D/8 lanes work on one
-// row (K or V of a token's head), eight dims each: a 16-byte load, the block's
-// largest magnitude by two shuffles among its four lanes, the scale from that
-// magnitude's exponent field (its largest value lands in [4, 8) and saturates
-// at 6), and the products by a power of two, which are exact.  Memory-bound:
-// 4 D bytes in, 17 D / 16 out per token and head.
-template <int D>
+// Both token kernels: D/8 lanes take one row (K or V of a token's head), eight
+// dims each; a warp takes 32 / (D/4) heads at a time, K and V side by side,
+// ROUNDS times over before it uses the first, so that the many small rows
+// keep the memory busy.  Meanwhile one lane per (token, head) finds its record.
+template <int D, int ROUNDS>
+struct TokenTile {
+    static constexpr int kLanes = D / 8;               // per row
+    static constexpr int kHeads = 32 / (2 * kLanes);   // (token, head) items per round: 1 or 2
+    static constexpr int kItems = kHeads * ROUNDS;     // per warp and pass
+    static_assert(kItems <= 32, "a lane per item");
+};
+
+// The item of one lane: its token, head, record and slot (record NULL as token_record).
+struct TokenItem {
+    uint32_t j, head;
+    uint8_t *rec;
+    int slot;
+};
+
+// Lane l < kItems looks up item base + l.
+template <int D, int ROUNDS>
+__device__ __forceinline__ void locate_item(TokenItem &t, const TokenMap &m, uint8_t *pool, int64_t stride_page,
+                                            int64_t stride_head, uint32_t base, uint32_t items, int lane)
+{
+    t.rec = nullptr;
+    t.slot = 0;
+    if (lane >= TokenTile<D, ROUNDS>::kItems || base + lane >= items)
+        return;
+    t.rec = token_record(m, pool, stride_page, (int)t.j, t.head == 0, t.slot);
+    if (t.rec)
+        t.rec += (int64_t)t.head * stride_head;
+}
+
+__device__ __forceinline__ uint8_t *shfl_pointer(uint8_t *x, int src)
+{
+    return reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, (unsigned long long)x, src));
+}
+
+// V's two bytes per (block, r) of lane (b, c): rows r = 2c and 2c + 1 of block
+// b; with the neighbour block's lane (b ^ 1) they become four bytes of one r.
+// The exchange is its own inverse.
+__device__ __forceinline__ uint32_t pair_blocks(uint32_t codes, int b)
+{
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, codes, 4);
+    return b & 1 ? __byte_perm(codes, other, 0x3276) : __byte_perm(codes, other, 0x5410);
+}
+
+// Quantises K and V of the new tokens into their slots.  Per row: the largest
+// magnitude of each block by two shuffles among its four lanes, the scale from
+// that magnitude's exponent field (its largest value lands in [4, 8) and
+// saturates at 6), and the products by a power of two, which are exact.
+// Memory-bound: 4 D bytes in, 17 D / 16 out per token and head.
+template <int D, int ROUNDS>
 __global__ void __launch_bounds__(kTokenThreads) mx4_write_kernel(const __grid_constant__ WriteParams p)
 {
     using R = Rec<D>;
-    constexpr int kLanes = D / 8;
+    using T = TokenTile<D, ROUNDS>;
+    const int lane = threadIdx.x & 31;
+    const int sub = lane % T::kLanes, is_v = (lane / T::kLanes) & 1, part = lane / (2 * T::kLanes);
+    const int b = sub >> 2, c = sub & 3;
+    const uint32_t items = (uint32_t)p.n_tokens * p.H_kv;  // below 2^31 (checked on the host)
+    const __nv_bfloat16 *in = (is_v ? p.v : p.k) + sub * 8;
+    const int64_t in_token = is_v ? p.v_token : p.k_token, in_head = is_v ? p.v_head : p.k_head;
+    const int at = is_v ? R::kV + (2 * c + (b & 1)) * (D / 16) + 4 * (b >> 1) : c * (D / 8) + 4 * b;
+    const int scale_at = (is_v ? R::kVs : R::kKs) + b;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t rows = (int64_t)p.n_tokens * p.H_kv * 2;
-    const int sub = threadIdx.x % kLanes;  // b = sub / 4, c = sub % 4
-    const int b = sub >> 2, c = sub & 3;
-    for (int64_t base = (int64_t)blockIdx.x * (kTokenThreads / kLanes); base < rows;
-         base += (int64_t)gridDim.x * (kTokenThreads / kLanes)) {
-        const int64_t at = base + threadIdx.x / kLanes;
-        if (at >= rows)
-            continue;
-        const int is_v = (int)(at & 1);
-        const int head = (int)((at >> 1) % p.H_kv);
-        const int j = (int)((at >> 1) / p.H_kv);
-        const uint32_t lanes = 0xfu << (threadIdx.x & 28);  // the four lanes of this scale block
-        int slot = 0;
-        uint8_t *rec = token_record(p.map, p.pool, p.stride_page, j, sub == 0 && head == 0 && !is_v, slot);
-        const __nv_bfloat16 *src = is_v ? p.v + j * p.v_token + head * p.v_head : p.k + j * p.k_token + head * p.k_head;
-        const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(src) + sub);
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-        float x[8];
-        uint32_t amax = 0;
+    const uint32_t step = gridDim.x * (kTokenThreads / 32) * T::kItems;
+    for (uint32_t base = (blockIdx.x * (kTokenThreads / 32) + threadIdx.x / 32) * T::kItems; base < items; base += step) {
+        TokenItem mine;
+        mine.j = (base + lane) / p.H_kv;
+        mine.head = base + lane - mine.j * p.H_kv;
+        uint4 raw[ROUNDS];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            // magnitudes order like their bits, infinities and NaN above every number
-            amax = max(amax, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+        for (int i = 0; i < ROUNDS; ++i) {
+            const uint32_t j = __shfl_sync(0xffffffffu, mine.j, i * T::kHeads + part);
+            const uint32_t head = __shfl_sync(0xffffffffu, mine.head, i * T::kHeads + part);
+            raw[i] = make_uint4(0, 0, 0, 0);
+            if (base + i * T::kHeads + part < items)
+                raw[i] = __ldg(reinterpret_cast<const uint4 *>(in + j * in_token + head * in_head));
         }
-        amax = max(amax, __shfl_xor_sync(lanes, amax, 1));
-        amax = max(amax, __shfl_xor_sync(lanes, amax, 2));
-        int scale = max((int)(amax >> 23) - 2, 1);
-        float mul = __uint_as_float((uint32_t)(254 - scale) << 23);  // 2^(127 - scale)
-        if (amax == 0)
-            scale = 0;
-        const bool bad = amax >= 0x7f800000u;  // the block reads back as NaN
-        if (bad) {
-            scale = 255;
-            mul = 0.f;
-        }
+        locate_item<D, ROUNDS>(mine, p.map, p.pool, p.stride_page, p.stride_head, base, items, lane);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x[i] = bad ? 0.f : x[i] * mul;
-        const uint32_t codes = floats_to_codes(x);
-        if (!rec)
-            continue;
-        rec += (int64_t)head * p.stride_head;
-        if (is_v) {
-            uint8_t *row = rec + R::kV + slot * R::kRow + 2 * b;
-            *reinterpret_cast<uint16_t *>(row + (2 * c) * (D / 16)) = (uint16_t)codes;
-            *reinterpret_cast<uint16_t *>(row + (2 * c + 1) * (D / 16)) = (uint16_t)(codes >> 16);
-        } else {
-            *reinterpret_cast<uint32_t *>(rec + slot * R::kRow + c * (D / 8) + 4 * b) = codes;
+        for (int i = 0; i < ROUNDS; ++i) {
+            uint8_t *rec = shfl_pointer(mine.rec, i * T::kHeads + part);
+            const int slot = __shfl_sync(0xffffffffu, mine.slot, i * T::kHeads + part);
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            // bf16 magnitudes order like their bits, infinities and NaN above every number
+            uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                    __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            top = max(top & 0xffffu, top >> 16);  // bf16 bits of the block's largest magnitude
+            const bool bad = top >= 0x7f80u;      // the block reads back as NaN
+            int scale = max((int)(top >> 7) - 2, 1);
+            const float mul = __uint_as_float((uint32_t)(254 - scale) << 23);  // 2^(127 - scale)
+            scale = bad ? 255 : top == 0 ? 0 : scale;
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[2 * k] = __uint_as_float(w[k] << 16) * mul;
+                x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * mul;
+            }
+            const uint32_t codes = bad ? 0u : floats_to_codes(x);
+            const uint32_t paired = pair_blocks(codes, b);
+            if (!rec)
+                continue;
+            *reinterpret_cast<uint32_t *>(rec + slot * R::kRow + at) = is_v ? paired : codes;
+            if (c == 0)
+                rec[scale_at + slot * R::kScaleRow] = (uint8_t)scale;
         }
-        if (c == 0)
-            rec[(is_v ? R::kVs : R::kKs) + slot * R::kScaleRow + b] = (uint8_t)scale;
     }
 }
 
@@ -220,52 +265,55 @@ __device__ __forceinline__ float scale_value(uint32_t s)
     return __uint_as_float(s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23);
 }
 
-// The stored values as bf16, exactly (e2m1 has two significant bits).  Lanes
-// as in mx4_write_kernel.
-template <int D>
+// The stored values as bf16, exactly (e2m1 has two significant bits).
+template <int D, int ROUNDS>
 __global__ void __launch_bounds__(kTokenThreads) mx4_read_kernel(const __grid_constant__ ReadParams p)
 {
     using R = Rec<D>;
-    constexpr int kLanes = D / 8;
+    using T = TokenTile<D, ROUNDS>;
+    const int lane = threadIdx.x & 31;
+    const int sub = lane % T::kLanes, is_v = (lane / T::kLanes) & 1, part = lane / (2 * T::kLanes);
+    const int b = sub >> 2, c = sub & 3;
+    const uint32_t items = (uint32_t)p.n_tokens * p.H_kv;  // below 2^31 (checked on the host)
+    __nv_bfloat16 *out = (is_v ? p.v : p.k) + sub * 8;
+    const int at = is_v ? R::kV + (2 * c + (b & 1)) * (D / 16) + 4 * (b >> 1) : c * (D / 8) + 4 * b;
+    const int scale_at = (is_v ? R::kVs : R::kKs) + b;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t rows = (int64_t)p.n_tokens * p.H_kv * 2;
-    const int sub = threadIdx.x % kLanes;
-    const int b = sub >> 2, c = sub & 3;
-    for (int64_t base = (int64_t)blockIdx.x * (kTokenThreads / kLanes); base < rows;
-         base += (int64_t)gridDim.x * (kTokenThreads / kLanes)) {
-        const int64_t at = base + threadIdx.x / kLanes;
-        if (at >= rows)
-            continue;
-        const int is_v = (int)(at & 1);
-        const int head = (int)((at >> 1) % p.H_kv);
-        const int j = (int)((at >> 1) / p.H_kv);
-        int slot = 0;
-        const uint8_t *rec = token_record(p.map, const_cast<uint8_t *>(p.pool), p.stride_page, j,
-                                          sub == 0 && head == 0 && !is_v, slot);
-        __nv_bfloat16 *dst = (is_v ? p.v : p.k) + ((int64_t)j * p.H_kv + head) * D;
-        if (!rec) {
-            reinterpret_cast<uint4 *>(dst)[sub] = make_uint4(0, 0, 0, 0);
-            continue;
-        }
-        rec += (int64_t)head * p.stride_head;
-        uint32_t codes;
-        if (is_v) {
-            const uint8_t *row = rec + R::kV + slot * R::kRow + 2 * b;
-            codes = *reinterpret_cast<const uint16_t *>(row + (2 * c) * (D / 16)) |
-                    (uint32_t) * reinterpret_cast<const uint16_t *>(row + (2 * c + 1) * (D / 16)) << 16;
-        } else {
-            codes = *reinterpret_cast<const uint32_t *>(rec + slot * R::kRow + c * (D / 8) + 4 * b);
-        }
-        const float s = scale_value(rec[(is_v ? R::kVs : R::kKs) + slot * R::kScaleRow + b]);
-        uint32_t h[4], o[4];
-        codes_to_half2(codes, h);
+    const uint32_t step = gridDim.x * (kTokenThreads / 32) * T::kItems;
+    for (uint32_t base = (blockIdx.x * (kTokenThreads / 32) + threadIdx.x / 32) * T::kItems; base < items; base += step) {
+        TokenItem mine;
+        mine.j = (base + lane) / p.H_kv;
+        mine.head = base + lane - mine.j * p.H_kv;
+        locate_item<D, ROUNDS>(mine, p.map, const_cast<uint8_t *>(p.pool), p.stride_page, p.stride_head, base, items,
+                               lane);
+        uint32_t codes[ROUNDS], scale[ROUNDS];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-            o[i] = pack_bf16(f.x * s, f.y * s);
+        for (int i = 0; i < ROUNDS; ++i) {
+            const uint8_t *rec = shfl_pointer(mine.rec, i * T::kHeads + part);
+            const int slot = __shfl_sync(0xffffffffu, mine.slot, i * T::kHeads + part);
+            codes[i] = 0;  // a skipped token reads as zeros
+            scale[i] = 127;
+            if (rec) {
+                codes[i] = *reinterpret_cast<const uint32_t *>(rec + slot * R::kRow + at);
+                scale[i] = rec[scale_at + slot * R::kScaleRow];
+            }
         }
-        reinterpret_cast<uint4 *>(dst)[sub] = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+        for (int i = 0; i < ROUNDS; ++i) {
+            const uint32_t paired = pair_blocks(codes[i], b);
+            const float s = scale_value(scale[i]);
+            uint32_t h[4], o[4];
+            codes_to_half2(is_v ? paired : codes[i], h);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
+                o[k] = pack_bf16(f.x * s, f.y * s);
+            }
+            const uint32_t item = base + i * T::kHeads + part;
+            if (item < items)
+                __stcs(reinterpret_cast<uint4 *>(out + (int64_t)item * D), make_uint4(o[0], o[1], o[2], o[3]));
+        }
     }
 }
 
@@ -324,13 +372,14 @@ struct DecodeParams {
     int32_t B, H_q, H_kv, G, max_pages, num_pool_pages, blocks;
 };
 
-// One block per SM: 16 warps of at most 128 registers, or 8 where the 16-head
-// tile needs more.
+// One block per SM.  12 warps: 16 (128 registers, some spilled) took 76.6 us
+// and 8 72.9 us where 12 took 69.2 us (32 ragged rows, 1.1 M token-heads, G = 8).
+// The 16-head tile's registers allow 8.
 template <int D, int NT>
 struct DCfg {
-    static constexpr int kWarps = NT == 1 ? 16 : 8;
+    static constexpr int kWarps = NT == 1 ? 12 : 8;
     static constexpr int kThreads = kWarps * 32;
-    static constexpr int kMinPages = 2 * kWarps;  // a smaller share costs more in merging than it saves
+    static constexpr int kMinPages = NT == 1 ? 32 : 16;  // a smaller share costs more in merging than it saves
     static constexpr int kHeads = 8 * NT;
     static constexpr int kState = kHeads * (D + 4) + 2 * kHeads;  // floats: o (rows padded), m, l
     static constexpr int kStages = D == 128 && NT == 1 ? 2 : 3;  // of two pages each
@@ -682,10 +731,48 @@ __device__ __forceinline__ void add_values_wide(const uint8_t *rec, int nvalid, 
     }
 }
 
+// Moves the reference max to the largest logit so far (s: products, nv[h]
+// valid tokens per page), rescaling the state.  Out of line of the common
+// path: a pair's first pages come here, later ones only when a logit
+// outgrows the reference by 2^(kPTop - kPShift).
+template <int NT, int D>
+__device__ __forceinline__ void move_reference(const float (&s)[2][NT][4], const int (&nv)[2], int lane, State<D, NT> &st)
+{
+    const int r = lane >> 2;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float old = kPShift - st.nb[nt][j];
+            float mx = old;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float v = s[h][nt][2 * k + j];
+                    if (r + 8 * k < nv[h])
+                        mx = fmaxf(mx, fmaf(v, 0.f, v * st.sl[nt][j]));
+                }
+#pragma unroll
+            for (int sh = 4; sh < 32; sh <<= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+            // a head with nothing but NaN so far: -inf - -inf, NaN as its sums are
+            const float al = exp2_approx(old - mx);
+            st.nb[nt][j] = kPShift - mx;
+            st.l[nt][j] *= al;
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+                st.o[mt][nt][j] *= al;
+                st.o[mt][nt][2 + j] *= al;
+            }
+        }
+}
+
 // Two neighbouring pages of a stage (records rec and rec + 17 D) into the
 // state, nv[h] valid tokens each (0: not this pair's page; whatever the record
-// holds is masked).  Two at once share the vote on the reference max, the
-// loop and its barriers, and give the scheduler independent products.
+// holds is masked).  Two at once share the votes, the loop and its barriers,
+// and give the scheduler independent products.  Masks, a moving reference and
+// scales outside their windows are branches that whole pages rarely take.
 template <int D, int NT, bool SCORED>
 __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)[2], int lane, State<D, NT> &st,
                                              float *logits, int logit_heads)
@@ -693,22 +780,16 @@ __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)
     using R = Rec<D>;
     constexpr int kBlocks = D / 32;
     const int r = lane >> 2, c = lane & 3;
-    float s[2][NT][4], t[2][NT][4], top = -INFINITY;
     const bool full = nv[0] == kPage && nv[1] == kPage;
+    float s[2][NT][4], t[2][NT][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
         page_products<D, NT>(rec + h * R::kBytes, lane, st, s[h]);
-
-    // ---- softmax against the reference max ----
+    if constexpr (SCORED) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                // an infinite product comes of a NaN scale (255): + 0 * s makes it NaN
-                t[h][nt][i] = fmaf(s[h][nt][i], 0.f, fmaf(s[h][nt][i], st.sl[nt][i & 1], st.nb[nt][i & 1]));
-            if constexpr (SCORED) {
+            for (int nt = 0; nt < NT; ++nt) {
                 const int g = 8 * nt + 2 * c;
                 if (g < logit_heads) {
                     float x[4];
@@ -722,59 +803,41 @@ __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)
                         *reinterpret_cast<float2 *>(dst + 8 * logit_heads) = make_float2(x[2], x[3]);
                 }
             }
-        }
-    if (!full) {
+    }
+
+    // ---- softmax against the reference max ----
+    if (st.vlow == ~0u) {
+        // the pair's first pages set the reference, and each block's window of V's scales
+        move_reference(s, nv, lane, st);
+        // from its first token's scales (any token's would do: what lies outside takes the wide path)
+        uint32_t v[4];
+        load_value_scales<D>(rec + (nv[0] > 0 ? 0 : R::kBytes), lane, v);
+        const uint32_t first = __shfl_sync(0xffffffffu, v[0], 0);
+        st.vlow = 0;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+            st.vlow |= (uint32_t)min(max((int)((first >> (8 * b)) & 255u) - 4, 0), 247) << (8 * b);
+    }
+    auto exponents = [&]() {
+        float top = -INFINITY;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (r + (i < 2 ? 0 : 8) >= nv[h])
+                for (int i = 0; i < 4; ++i) {
+                    // an infinite product comes of a NaN scale (255): + 0 * s makes it NaN
+                    t[h][nt][i] = fmaf(s[h][nt][i], 0.f, fmaf(s[h][nt][i], st.sl[nt][i & 1], st.nb[nt][i & 1]));
+                    if (!full && r + (i < 2 ? 0 : 8) >= nv[h])
                         t[h][nt][i] = -INFINITY;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                top = fmaxf(top, t[h][nt][i]);
-    if (__any_sync(0xffffffffu, top > kPTop)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float old = kPShift - st.nb[nt][j];
-                float x[2][2], mx = old;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float v = s[h][nt][2 * k + j];
-                        x[h][k] = r + 8 * k < nv[h] ? fmaf(v, 0.f, v * st.sl[nt][j]) : -INFINITY;
-                        mx = fmaxf(mx, x[h][k]);
-                    }
-#pragma unroll
-                for (int sh = 4; sh < 32; sh <<= 1)
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-                // a head with nothing but NaN so far: -inf - -inf, NaN as its sums are
-                const float al = exp2_approx(old - mx);
-                st.nb[nt][j] = kPShift - mx;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        t[h][nt][2 * k + j] = x[h][k] + st.nb[nt][j];
-                st.l[nt][j] *= al;
-#pragma unroll
-                for (int mt = 0; mt < D / 16; ++mt) {
-                    st.o[mt][nt][j] *= al;
-                    st.o[mt][nt][2 + j] *= al;
+                    top = fmaxf(top, t[h][nt][i]);
                 }
-            }
+        return top;
+    };
+    if (__any_sync(0xffffffffu, exponents() > kPTop)) {
+        move_reference(s, nv, lane, st);
+        exponents();
     }
-    // the exponentials take the logits' place
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -787,39 +850,21 @@ __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)
         }
 
     // ---- the values ----
-    uint32_t vs[2][4], d[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        load_value_scales<D>(rec + h * R::kBytes, lane, vs[h]);
-    if (st.vlow == ~0u) {
-        // the pair's first pages set each block's window, up to two steps above its largest scale
-        st.vlow = 0;
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            const int top_b = max(top_scale(vs[0], lane, nv[0], b), top_scale(vs[1], lane, nv[1], b));
-            st.vlow |= (uint32_t)min(max(top_b - 5, 0), 247) << (8 * b);
-        }
-    }
     // Steps of the tokens' scales above the windows' lower ends, a byte per
     // block: in their windows iff every byte is 0 .. 7.  (A byte below its
     // window borrows, but is itself at least 256 - 247 then.)
-    uint32_t out_of = 0;
+    uint32_t d[2][4], out_of = 0;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+        load_value_scales<D>(rec + h * R::kBytes, lane, d[h]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            d[h][i] = vs[h][i] - st.vlow;
-    if (!full) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (2 * c + (i & 1) + 4 * (i & 2) >= nv[h])
-                    d[h][i] = 0;
+        for (int i = 0; i < 4; ++i) {
+            d[h][i] -= st.vlow;
+            if (!full && 2 * c + (i & 1) + 4 * (i & 2) >= nv[h])
+                d[h][i] = 0;
+            out_of |= d[h][i];
+        }
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        out_of |= d[h][0] | d[h][1] | d[h][2] | d[h][3];
     if (!__any_sync(0xffffffffu, (out_of & 0xf8f8f8f8u) != 0)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -828,77 +873,16 @@ __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
             float pr[NT][4];
-            uint32_t v[4];
+            uint32_t vs[4];
+            load_value_scales<D>(rec + h * R::kBytes, lane, vs);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = h ? vs[1][i] : vs[0][i];
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                     pr[nt][i] = h ? t[1][nt][i] : t[0][nt][i];
-            }
-            add_values_wide<D, NT>(rec + h * R::kBytes, h ? nv[1] : nv[0], lane, st, pr, v);
+            add_values_wide<D, NT>(rec + h * R::kBytes, h ? nv[1] : nv[0], lane, st, pr, vs);
         }
     }
-}
-
-// The same for two whole pages whose logits stay in reach of the reference
-// max and whose V scales lie in their windows, as nearly all do: no masks, no
-// rescaling.  False, with the state unchanged, where they do not.
-template <int D, int NT, bool SCORED>
-__device__ __forceinline__ bool attend_whole_pages(const uint8_t *rec, int lane, State<D, NT> &st, float *logits,
-                                                   int logit_heads)
-{
-    using R = Rec<D>;
-    const int r = lane >> 2, c = lane & 3;
-    float t[2][NT][4], top = -INFINITY;
-    uint32_t out_of = 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        page_products<D, NT>(rec + h * R::kBytes, lane, st, t[h]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (SCORED) {
-                const int g = 8 * nt + 2 * c;
-                if (g < logit_heads) {
-                    float x[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[i] = fmaf(t[h][nt][i], 0.f, t[h][nt][i] * st.sl[nt][i & 1]);
-                    float *dst = logits + (h * kPage + r) * logit_heads + g;
-                    *reinterpret_cast<float2 *>(dst) = make_float2(x[0], x[1]);
-                    *reinterpret_cast<float2 *>(dst + 8 * logit_heads) = make_float2(x[2], x[3]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                t[h][nt][i] = fmaf(t[h][nt][i], 0.f, fmaf(t[h][nt][i], st.sl[nt][i & 1], st.nb[nt][i & 1]));
-                top = fmaxf(top, t[h][nt][i]);
-            }
-        }
-        uint32_t vs[4];
-        load_value_scales<D>(rec + h * R::kBytes, lane, vs);
-        out_of |= (vs[0] - st.vlow) | (vs[1] - st.vlow) | (vs[2] - st.vlow) | (vs[3] - st.vlow);
-    }
-    if (__any_sync(0xffffffffu, top > kPTop || (out_of & 0xf8f8f8f8u) != 0))
-        return false;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                t[h][nt][i] = exp2_approx(t[h][nt][i]);
-            st.l[nt][0] += t[h][nt][0] + t[h][nt][2];
-            st.l[nt][1] += t[h][nt][1] + t[h][nt][3];
-        }
-        uint32_t d[4];
-        load_value_scales<D>(rec + h * R::kBytes, lane, d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            d[i] -= st.vlow;
-        add_values<D, NT>(rec + h * R::kBytes, lane, st, t[h], d);
-    }
-    return true;
 }
 
 // A warp's finished state to shared memory, in true units: o [head][D + 4], m, l per head.
@@ -1137,9 +1121,7 @@ __global__ void __launch_bounds__(DCfg<D, NT>::kThreads, 1) mx4_decode_kernel(co
                 logits = p.logits + ((int64_t)pair * capacity + (int64_t)(index - at) * kPage) * heads;
             }
             const uint8_t *rec = ring + stage * C::kStageBytes;
-            if (nv[0] < kPage || nv[1] < kPage || st.vlow == ~0u ||
-                !attend_whole_pages<D, NT, SCORED>(rec, lane, st, logits, heads))
-                attend_pages<D, NT, SCORED>(rec, nv, lane, st, logits, heads);
+            attend_pages<D, NT, SCORED>(rec, nv, lane, st, logits, heads);
             index += take;
             j += take;
             if ((j & 1) && j < n)
@@ -1436,10 +1418,21 @@ cudaError_t launch_finish(const FinishParams &p, bool scores, int64_t grid, cuda
 // Pages below which a decode of this tile is one block's: nothing to merge.
 int min_pages(int G) { return G <= 8 ? DCfg<128, 1>::kMinPages : DCfg<128, 2>::kMinPages; }
 
-unsigned token_grid(int64_t rows, int lanes)
+// Rounds of a token kernel: eight where every warp of a full GPU then has a
+// pass (enough rows in flight to stream), else one, for the shortest way
+// through a few tokens.
+constexpr int kManyRounds = 8;
+constexpr int kTokenBlocks = 148 * 8;  // of 256 threads: a full GPU
+
+bool many_rounds(int64_t items) { return items >= (int64_t)kTokenBlocks * (kTokenThreads / 32) * kManyRounds / 2; }
+
+template <typename P>
+cudaError_t launch_tokens(void (*many)(P), void (*few)(P), int heads, const P &p, cudaStream_t st)
 {
-    const int64_t blocks = ceil_div(rows * lanes, kTokenThreads);
-    return (unsigned)std::min<int64_t>(blocks, 148 * 8);
+    const int64_t items = (int64_t)p.n_tokens * p.H_kv;
+    const bool m = many_rounds(items);
+    const int64_t blocks = ceil_div(items, (int64_t)heads * (m ? kManyRounds : 1) * (kTokenThreads / 32));
+    return launch_kernel(m ? many : few, (unsigned)std::min<int64_t>(blocks, kTokenBlocks), kTokenThreads, 0, st, true, p);
 }
 
 int check_tokens(const pkv_shape *shape, const void *pool, const int32_t *block_table, const int32_t *seq_lens,
@@ -1455,6 +1448,8 @@ int check_tokens(const pkv_shape *shape, const void *pool, const int32_t *block_
     if (!pool || !block_table || !seq_lens || !workspace || shape->max_pages_per_seq < 1 || shape->num_pool_pages < 1 ||
         (!indptr && n_tokens != shape->B))
         return PKV_ERR_INVALID;
+    if ((int64_t)n_tokens * shape->H_kv > INT32_MAX / 2)
+        return PKV_ERR_UNSUPPORTED;
     if (!aligned(pool, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(indptr, 4) ||
         !aligned(workspace, 4))
         return PKV_ERR_UNSUPPORTED;
@@ -1495,10 +1490,10 @@ int pkv_mx4_append(const void *k, const void *v, int64_t k_stride_token, int64_t
     p.stride_head = s.kv_stride_head;
     p.n_tokens = n_tokens;
     p.H_kv = s.H_kv;
-    const unsigned grid = token_grid((int64_t)n_tokens * s.H_kv * 2, s.head_dim / 8);
-    const cudaError_t e =
-        s.head_dim == 128 ? launch_kernel(mx4_write_kernel<128>, grid, kTokenThreads, 0, (cudaStream_t)stream, true, p)
-                          : launch_kernel(mx4_write_kernel<64>, grid, kTokenThreads, 0, (cudaStream_t)stream, true, p);
+    const cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = s.head_dim == 128
+                              ? launch_tokens(mx4_write_kernel<128, kManyRounds>, mx4_write_kernel<128, 1>, 1, p, st)
+                              : launch_tokens(mx4_write_kernel<64, kManyRounds>, mx4_write_kernel<64, 1>, 2, p, st);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -1522,10 +1517,10 @@ int pkv_mx4_read(const void *pool, const int32_t *block_table, const int32_t *se
     p.stride_head = s.kv_stride_head;
     p.n_tokens = n_tokens;
     p.H_kv = s.H_kv;
-    const unsigned grid = token_grid((int64_t)n_tokens * s.H_kv * 2, s.head_dim / 8);
-    const cudaError_t e =
-        s.head_dim == 128 ? launch_kernel(mx4_read_kernel<128>, grid, kTokenThreads, 0, (cudaStream_t)stream, true, p)
-                          : launch_kernel(mx4_read_kernel<64>, grid, kTokenThreads, 0, (cudaStream_t)stream, true, p);
+    const cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = s.head_dim == 128
+                              ? launch_tokens(mx4_read_kernel<128, kManyRounds>, mx4_read_kernel<128, 1>, 1, p, st)
+                              : launch_tokens(mx4_read_kernel<64, kManyRounds>, mx4_read_kernel<64, 1>, 2, p, st);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
