@@ -661,45 +661,75 @@ def paged_decode_noalloc(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Te
     return out
 
 
-def _on(device, stream):
-    """Context in which a call's kernels and allocations belong to `stream` (default: the current stream of
-    `device`), whatever device is current."""
+# The current stream's handle of a device as an integer, without the Stream
+# object (a fifth of a microsecond instead of two).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on(index: int, stream):
+    """Context in which a call's kernels and allocations belong to `stream` (default: the current stream of CUDA
+    device `index`), whatever device is current."""
     if stream is None:
-        return torch.cuda.device(device)
-    if stream.device != device:
-        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+        return torch.cuda.device(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to cuda:{index}")
     return torch.cuda.stream(stream)
 
 
-def _cuda_device(name: str, t: torch.Tensor) -> torch.device:
-    if t.device.type != "cuda":
+def _launch(fn, what: str, index: int, stream, *args):
+    """fn(*args, stream handle) with CUDA device `index` current; raises on an error status."""
+    if stream is None and torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
+    else:
+        with _on(index, stream):
+            rc = fn(*args, _raw_stream(index))
+    if rc != 0:
+        raise PkvError(rc, what)
+
+
+def _empty(shape, dtype, index: int, stream) -> torch.Tensor:
+    """A new tensor on CUDA device `index` that belongs to the call's stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=index)
+    with _on(index, stream):
+        return torch.empty(shape, dtype=dtype, device=index)
+
+
+def _cuda_index(name: str, t: torch.Tensor) -> int:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be on a CUDA device, not {t.device}")
-    return t.device
+    return index
 
 
-def _check_tensor(name: str, t: torch.Tensor, dtype, device, contiguous: bool = True):
-    if t.dtype != dtype:
+def _check_tensor(name: str, t: torch.Tensor, dtype, index: int, contiguous: bool = True):
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, not {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, not {t.device}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _check_scores(name: str, t: torch.Tensor, dtype, B: int, H_kv: int, max_pages: int, device):
-    """[B][H_kv][>= max_pages * 16] with contiguous tokens, no two elements in one place."""
-    _check_tensor(name, t, dtype, device, contiguous=False)
-    if t.dim() != 3 or t.shape[0] != B or t.shape[1] != H_kv or t.shape[2] < max_pages * 16:
-        raise ValueError(f"{name} must be [{B}][{H_kv}][>= {max_pages * 16}], got {list(t.shape)}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+def _check_scores(name: str, t: torch.Tensor, dtype, B: int, H_kv: int, max_pages: int, index: int) -> tuple:
+    """[B][H_kv][>= max_pages * 16] with contiguous tokens, no two elements in one place; returns the strides."""
+    _check_tensor(name, t, dtype, index, contiguous=False)
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != B or shape[1] != H_kv or shape[2] < max_pages * 16:
+        raise ValueError(f"{name} must be [{B}][{H_kv}][>= {max_pages * 16}], got {list(shape)}")
+    st = t.stride()
+    if st[2] != 1 and shape[2] > 1:
         raise ValueError(f"{name}'s tokens must be contiguous")
-    _check_no_overlap(name, t)
+    if st[1] < shape[2] or st[0] < st[1] * H_kv:  # not nested in the plain order
+        _check_no_overlap(name, shape, st)
+    return st
 
 
-def _check_no_overlap(name: str, t: torch.Tensor):
+def _check_no_overlap(name: str, shape, strides):
     """Reject views (expanded, overlapping) in which two elements share memory: they would be written twice."""
     reach = 1
-    for size, stride in sorted(((s, st) for s, st in zip(t.shape, t.stride()) if s > 1), key=lambda x: x[1]):
+    for size, stride in sorted(((s, st) for s, st in zip(shape, strides) if s > 1), key=lambda x: x[1]):
         if stride < reach:
             raise ValueError(f"{name} has elements that share memory")
         reach = stride * (size - 1) + reach
@@ -717,29 +747,30 @@ def paged_decode_scored(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
     the input of evict_tokens.  `plan` comes from plan_decode(..., scores=True); elements past a row's length
     are left alone.  Everything else as paged_decode."""
     L = lib()
-    device = _cuda_device("q", q)
-    with _on(device, stream):
-        if plan is None:
-            shape = shape_of(q, k_pool, block_table, layout, v_pool)
-            host = seq_lens_host if seq_lens_host is not None else seq_lens.detach().cpu()
-            plan = plan_decode(host, shape, device, rules, scores=True)
-        shape = plan.shape
-        if not plan.plan.flags & FLAG_SCORES:
-            raise ValueError("the plan was not made for scores: plan_decode(..., scores=True)")
-        if out is None:
-            out = torch.empty_like(q)
-        _check_decode_tensors(q, k_pool, v_pool, block_table, seq_lens, out, shape)
-        _check_scores("scores", scores, torch.float32, shape.B, shape.H_kv, shape.max_pages_per_seq, device)
-        if plan.device_queue and not plan.plan.flags & FLAG_DEVICE_FILL and plan.plan.mode == WORK_QUEUE:
-            build_fill_queue_device(seq_lens, shape, plan.fill_blocks, plan.items, plan.indptr, plan.workspace)
-        rc = L.pkv_paged_decode_scored(q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
-                                       seq_lens.data_ptr(), page_size, float(scale), out.data_ptr(),
-                                       scores.data_ptr(), scores.stride(0), scores.stride(1), ctypes.byref(shape),
-                                       ctypes.byref(plan.plan),
-                                       plan.items.data_ptr() if plan.items is not None else None,
-                                       plan.indptr.data_ptr() if plan.indptr is not None else None, plan.n_items,
-                                       plan.workspace.data_ptr(), plan.workspace.numel(), _stream_ptr())
-    _check(rc, "pkv_paged_decode_scored")
+    index = _cuda_index("q", q)
+    if plan is None:
+        shape = shape_of(q, k_pool, block_table, layout, v_pool)
+        host = seq_lens_host if seq_lens_host is not None else seq_lens.detach().cpu()
+        with _on(index, stream):
+            plan = plan_decode(host, shape, q.device, rules, scores=True)
+    shape = plan.shape
+    if not plan.plan.flags & FLAG_SCORES:
+        raise ValueError("the plan was not made for scores: plan_decode(..., scores=True)")
+    if out is None:
+        out = _empty(q.shape, torch.bfloat16, index, stream)
+    _check_decode_tensors(q, k_pool, v_pool, block_table, seq_lens, out, shape)
+    st = _check_scores("scores", scores, torch.float32, shape.B, shape.H_kv, shape.max_pages_per_seq, index)
+    ws = plan.workspace
+    items = indptr = None
+    if plan.items is not None:
+        items, indptr = plan.items.data_ptr(), plan.indptr.data_ptr()
+        if plan.device_queue:
+            _launch(L.pkv_build_fill_queue_device, "pkv_build_fill_queue_device", index, stream, seq_lens.data_ptr(),
+                    ctypes.byref(shape), plan.fill_blocks, items, int(plan.items.shape[0]), indptr, ws.data_ptr())
+    _launch(L.pkv_paged_decode_scored, "pkv_paged_decode_scored", index, stream, q.data_ptr(), k_pool.data_ptr(),
+            v_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), page_size, scale, out.data_ptr(),
+            scores.data_ptr(), st[0], st[1], ctypes.byref(shape), ctypes.byref(plan.plan), items, indptr, plan.n_items,
+            ws.data_ptr(), ws.numel())
     return out
 
 
@@ -777,55 +808,59 @@ def evict_tokens(scores: torch.Tensor, planes: Sequence[torch.Tensor], block_tab
     dtype, any strides with a contiguous last axis: (k_pool, v_pool), or mx4_planes(pool).  Pages that rows share
     must be copied first: the call moves tokens within every row's pages.  `seq_lens` is not changed."""
     L = lib()
-    device = _cuda_device("scores", scores)
-    B, max_pages = (int(x) for x in block_table.shape)
-    H_kv = int(scores.shape[1])
-    planes = list(planes)
+    index = _cuda_index("scores", scores)
+    B, max_pages = block_table.shape
+    H_kv = scores.shape[1] if scores.dim() == 3 else 0
     if layout not in ("HND", "NHD"):
         raise ValueError(layout)
-    if not planes or len(planes) > EVICT_MAX_PLANES:
+    if not 1 <= len(planes) <= EVICT_MAX_PLANES:
         raise ValueError(f"between 1 and {EVICT_MAX_PLANES} planes, got {len(planes)}")
     if not 0 <= recent <= budget or budget > INT32_MAX:
         raise ValueError(f"0 <= recent <= budget, got recent {recent}, budget {budget}")
-    with _on(device, stream):
-        if plan is None:
-            plan = plan_evict(B, H_kv, max_pages, device)
-        if (plan.shape.B, plan.shape.H_kv, plan.shape.max_pages_per_seq) != (B, H_kv, max_pages):
-            raise ValueError("the plan was made for another batch (B, H_kv or max_pages)")
-        if out is None:
-            out = torch.empty(B, dtype=torch.int32, device=device)
-        _check_scores("scores", scores, torch.float32, B, H_kv, max_pages, device)
-        if positions is not None:
-            _check_scores("positions", positions, torch.int32, B, H_kv, max_pages, device)
-        for name, t in (("block_table", block_table), ("seq_lens", seq_lens), ("out", out)):
-            _check_tensor(name, t, torch.int32, device)
-        if seq_lens.numel() < B or out.numel() < B:
-            raise ValueError(f"seq_lens and out must hold {B} lengths")
-        if out.data_ptr() < seq_lens.data_ptr() + 4 * B and seq_lens.data_ptr() < out.data_ptr() + 4 * B:
-            raise ValueError("out must not share memory with seq_lens")
-        pages = int(planes[0].shape[0])
-        head_axis, token_axis = (1, 2) if layout == "HND" else (2, 1)
-        arr = (Plane * len(planes))()
-        for i, t in enumerate(planes):
-            if t.device != device:
-                raise ValueError(f"plane {i} must be on {device}, not {t.device}")
-            if t.dim() != 4 or t.shape[0] != pages or t.shape[head_axis] != H_kv or t.shape[token_axis] != 16:
-                raise ValueError(f"plane {i}'s shape {list(t.shape)} is not {pages} {layout} pages of {H_kv} heads "
-                                 "and 16 tokens")
-            if t.shape[3] < 1 or (t.shape[3] > 1 and t.stride(3) != 1):
-                raise ValueError(f"plane {i}'s last axis must be contiguous")
-            _check_no_overlap(f"plane {i}", t)
-            size = t.element_size()
-            arr[i] = Plane(t.data_ptr(), t.stride(0) * size, t.stride(head_axis) * size, t.stride(token_axis) * size,
-                           int(t.shape[3]) * size, 0)
-        shape = make_shape(B, H_kv, H_kv, 128, 16, max_pages, pages)
-        rc = L.pkv_evict_tokens(scores.data_ptr(), scores.stride(0), scores.stride(1),
-                                positions.data_ptr() if positions is not None else None,
-                                positions.stride(0) if positions is not None else 0,
-                                positions.stride(1) if positions is not None else 0, arr, len(planes),
-                                block_table.data_ptr(), seq_lens.data_ptr(), int(budget), int(recent), out.data_ptr(),
-                                ctypes.byref(shape), plan.workspace.data_ptr(), plan.workspace.numel(), _stream_ptr())
-    _check(rc, "pkv_evict_tokens")
+    score_st = _check_scores("scores", scores, torch.float32, B, H_kv, max_pages, index)
+    if plan is None:
+        with _on(index, stream):
+            plan = plan_evict(B, H_kv, max_pages, index)
+    shape = plan.shape
+    if shape.B != B or shape.H_kv != H_kv or shape.max_pages_per_seq != max_pages:
+        raise ValueError("the plan was made for another batch (B, H_kv or max_pages)")
+    pos_ptr, pos_st = None, (0, 0)
+    if positions is not None:
+        pos_st = _check_scores("positions", positions, torch.int32, B, H_kv, max_pages, index)
+        pos_ptr = positions.data_ptr()
+    if out is None:
+        out = _empty(B, torch.int32, index, stream)
+    for name, t in (("block_table", block_table), ("seq_lens", seq_lens), ("out", out)):
+        _check_tensor(name, t, torch.int32, index)
+    lens_ptr, out_ptr = seq_lens.data_ptr(), out.data_ptr()
+    if seq_lens.numel() < B or out.numel() < B:
+        raise ValueError(f"seq_lens and out must hold {B} lengths")
+    if out_ptr < lens_ptr + 4 * B and lens_ptr < out_ptr + 4 * B:
+        raise ValueError("out must not share memory with seq_lens")
+    pages = planes[0].shape[0]
+    head_axis, token_axis = (1, 2) if layout == "HND" else (2, 1)
+    arr = (Plane * len(planes))()
+    for i, t in enumerate(planes):
+        dims, st = t.shape, t.stride()
+        if t.get_device() != index:
+            raise ValueError(f"plane {i} must be on cuda:{index}, not {t.device}")
+        if len(dims) != 4 or dims[0] != pages or dims[head_axis] != H_kv or dims[token_axis] != 16:
+            raise ValueError(f"plane {i}'s shape {list(dims)} is not {pages} {layout} pages of {H_kv} heads "
+                             "and 16 tokens")
+        if dims[3] < 1 or (dims[3] > 1 and st[3] != 1):
+            raise ValueError(f"plane {i}'s last axis must be contiguous")
+        if st[2] < dims[3] or st[1] < st[2] * dims[2] or st[0] < st[1] * dims[1]:  # not nested in the plain order
+            _check_no_overlap(f"plane {i}", dims, st)
+        size = t.element_size()
+        p = arr[i]
+        p.base = t.data_ptr()
+        p.stride_page, p.stride_head, p.stride_token = st[0] * size, st[head_axis] * size, st[token_axis] * size
+        p.row_bytes = dims[3] * size
+    shape = Shape.from_buffer_copy(shape)  # the plan may serve several calls at once
+    shape.num_pool_pages = pages
+    _launch(L.pkv_evict_tokens, "pkv_evict_tokens", index, stream, scores.data_ptr(), score_st[0], score_st[1], pos_ptr,
+            pos_st[0], pos_st[1], arr, len(planes), block_table.data_ptr(), lens_ptr, budget, recent, out_ptr,
+            ctypes.byref(shape), plan.workspace.data_ptr(), plan.workspace.numel())
     return out
 
 
@@ -840,18 +875,22 @@ def mx4_pool(pages: int, H_kv: int, head_dim: int, device) -> torch.Tensor:
 def _mx4_head_dim(pool: torch.Tensor) -> int:
     if pool.dim() != 3 or pool.shape[2] not in (17 * 64, 17 * 128):
         raise ValueError(f"a 4-bit pool is [pages][H_kv][17 * head_dim], head_dim 64 or 128, got {list(pool.shape)}")
-    return int(pool.shape[2]) // 17
+    return pool.shape[2] // 17
 
 
 def mx4_planes(pool: torch.Tensor) -> tuple:
     """The four arrays of a 4-bit pool as views [pages][H_kv][16][...]: K codes, V codes, K scales, V scales (the
     planes of evict_tokens)."""
     D = _mx4_head_dim(pool)
-    parts, at = [], 0
-    for n in (D // 2, D // 2, D // 32, D // 32):
-        parts.append(pool[:, :, at:at + 16 * n].unflatten(2, (16, n)))
-        at += 16 * n
-    return tuple(parts)
+    pages, H_kv = pool.shape[:2]
+    page, head, byte = pool.stride()
+    if byte != 1:
+        raise ValueError("the pool's records must be contiguous")
+    at, c, s = pool.storage_offset(), D // 2, D // 32
+    return (pool.as_strided((pages, H_kv, 16, c), (page, head, c, 1), at),
+            pool.as_strided((pages, H_kv, 16, c), (page, head, c, 1), at + 16 * c),
+            pool.as_strided((pages, H_kv, 16, s), (page, head, s, 1), at + 32 * c),
+            pool.as_strided((pages, H_kv, 16, s), (page, head, s, 1), at + 32 * c + 16 * s))
 
 
 def mx4_shape(pool: torch.Tensor, block_table: torch.Tensor, q_heads: Optional[int] = None) -> Shape:
@@ -861,7 +900,7 @@ def mx4_shape(pool: torch.Tensor, block_table: torch.Tensor, q_heads: Optional[i
     B, max_pages = (int(x) for x in block_table.shape)
     if pool.stride(2) != 1:
         raise ValueError("the pool's records must be contiguous")
-    _check_no_overlap("pool", pool)
+    _check_no_overlap("pool", pool.shape, pool.stride())
     head = pool.stride(1) if H_kv > 1 else 17 * D
     page = pool.stride(0) if pages > 1 else H_kv * head
     return Shape(B, H_kv if q_heads is None else q_heads, H_kv, D, 16, max_pages, pages, 0, page, head, D // 2)
@@ -890,32 +929,52 @@ def plan_mx4(shape: Shape, device, scores: bool = False, blocks: Optional[int] =
     return Mx4Plan(shape, plan, torch.zeros(n.value, dtype=torch.uint8, device=device))
 
 
-def _check_mx4(pool, block_table, seq_lens, shape: Shape) -> torch.device:
-    device = _cuda_device("pool", pool)
-    _check_tensor("pool", pool, torch.uint8, device, contiguous=False)
-    if _mx4_head_dim(pool) != shape.head_dim or pool.shape[1] != shape.H_kv or pool.shape[0] < shape.num_pool_pages:
-        raise ValueError(f"pool {list(pool.shape)} differs from the plan's shape")
-    if (pool.stride(2) != 1 or (pool.shape[1] > 1 and pool.stride(1) != shape.kv_stride_head)
-            or (pool.shape[0] > 1 and pool.stride(0) != shape.kv_stride_page)):
-        raise ValueError("the pool's strides differ from the plan's shape")
-    _check_tensor("block_table", block_table, torch.int32, device)
-    _check_tensor("seq_lens", seq_lens, torch.int32, device)
+def _check_mx4(pool, block_table, seq_lens, shape: Shape) -> int:
+    """The pool, table and lengths of a call against its plan's shape; one combined test passes every well-formed
+    call, the itemised ones name what is wrong with another.  Returns the device index."""
+    index = pool.get_device()
+    dims, st = pool.shape, pool.stride()
+    if (index >= 0 and pool.dtype is torch.uint8 and block_table.dtype is torch.int32
+            and seq_lens.dtype is torch.int32 and block_table.get_device() == index and seq_lens.get_device() == index
+            and len(dims) == 3 and dims[0] >= shape.num_pool_pages and dims[1] == shape.H_kv
+            and dims[2] == 17 * shape.head_dim and st[2] == 1 and (st[1] == shape.kv_stride_head or dims[1] == 1)
+            and (st[0] == shape.kv_stride_page or dims[0] == 1)
+            and block_table.shape == (shape.B, shape.max_pages_per_seq) and block_table.is_contiguous()
+            and seq_lens.numel() >= shape.B and seq_lens.is_contiguous()):
+        return index
+    _cuda_index("pool", pool)
+    _check_tensor("pool", pool, torch.uint8, index, contiguous=False)
+    if _mx4_head_dim(pool) != shape.head_dim or dims[1] != shape.H_kv or dims[0] < shape.num_pool_pages:
+        raise ValueError(f"pool {list(dims)} differs from the plan's shape")
+    _check_tensor("block_table", block_table, torch.int32, index)
+    _check_tensor("seq_lens", seq_lens, torch.int32, index)
     if tuple(block_table.shape) != (shape.B, shape.max_pages_per_seq):
         raise ValueError(f"block_table must be [{shape.B}][{shape.max_pages_per_seq}], got {list(block_table.shape)}")
     if seq_lens.numel() < shape.B:
         raise ValueError(f"seq_lens holds {seq_lens.numel()} lengths for {shape.B} rows")
-    return device
+    raise ValueError("the pool's strides differ from the plan's shape")
 
 
-def _check_indptr(indptr, n_tokens: int, shape: Shape, device):
+def _check_indptr(indptr, n_tokens: int, shape: Shape, index: int):
     if indptr is None:
         if n_tokens != shape.B:
             raise ValueError(f"without indptr there is one token per row: {n_tokens} tokens for {shape.B} rows")
         return None
-    _check_tensor("indptr", indptr, torch.int32, device)
+    _check_tensor("indptr", indptr, torch.int32, index)
     if indptr.numel() != shape.B + 1:
         raise ValueError(f"indptr must hold {shape.B + 1} offsets, got {indptr.numel()}")
     return indptr.data_ptr()
+
+
+def _check_token_rows(name: str, t: torch.Tensor, n: int, shape: Shape, index: int) -> tuple:
+    """bf16 [n][H_kv][D] with contiguous D; returns the token and head strides."""
+    _check_tensor(name, t, torch.bfloat16, index, contiguous=False)
+    dims, st = t.shape, t.stride()
+    if len(dims) != 3 or dims[0] != n or dims[1] != shape.H_kv or dims[2] != shape.head_dim:
+        raise ValueError(f"{name} must be [{n}][{shape.H_kv}][{shape.head_dim}], got {list(dims)}")
+    if st[2] != 1:
+        raise ValueError(f"{name}'s head_dim axis must be contiguous")
+    return (st[0] if n > 1 else 0), (st[1] if dims[1] > 1 else 0)
 
 
 def mx4_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor,
@@ -929,25 +988,16 @@ def mx4_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, block_table
     (workspace_status(plan))."""
     L = lib()
     if plan is None:
-        plan = plan_mx4(mx4_shape(pool, block_table), _cuda_device("pool", pool))
+        plan = plan_mx4(mx4_shape(pool, block_table), _cuda_index("pool", pool))
     shape = plan.shape
-    device = _check_mx4(pool, block_table, seq_lens, shape)
-    for name, t in (("k", k), ("v", v)):
-        _check_tensor(name, t, torch.bfloat16, device, contiguous=False)
-        if t.dim() != 3 or tuple(t.shape[1:]) != (shape.H_kv, shape.head_dim):
-            raise ValueError(f"{name} must be [n][{shape.H_kv}][{shape.head_dim}], got {list(t.shape)}")
-        if t.stride(2) != 1:
-            raise ValueError(f"{name}'s head_dim axis must be contiguous")
-    n = int(k.shape[0])
-    if v.shape[0] != n:
-        raise ValueError(f"k has {n} tokens, v {v.shape[0]}")
-    ptr = _check_indptr(indptr, n, shape, device)
-    ks, vs = ([t.stride(0) if n > 1 else 0, t.stride(1) if shape.H_kv > 1 else 0] for t in (k, v))
-    with _on(device, stream):
-        rc = L.pkv_mx4_append(k.data_ptr(), v.data_ptr(), *ks, *vs, pool.data_ptr(), block_table.data_ptr(),
-                              seq_lens.data_ptr(), ptr, n, ctypes.byref(shape), plan.workspace.data_ptr(),
-                              _stream_ptr())
-    _check(rc, "pkv_mx4_append")
+    index = _check_mx4(pool, block_table, seq_lens, shape)
+    n = k.shape[0]
+    k_token, k_head = _check_token_rows("k", k, n, shape, index)
+    v_token, v_head = _check_token_rows("v", v, n, shape, index)
+    ptr = _check_indptr(indptr, n, shape, index)
+    _launch(L.pkv_mx4_append, "pkv_mx4_append", index, stream, k.data_ptr(), v.data_ptr(), k_token, k_head, v_token,
+            v_head, pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), ptr, n, ctypes.byref(shape),
+            plan.workspace.data_ptr())
 
 
 def mx4_read(pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, n_tokens: int, *,
@@ -957,25 +1007,25 @@ def mx4_read(pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tens
     indptr wrote.  Exact.  `out` = (k, v) is written in place; tokens that the append skips get zeros."""
     L = lib()
     if plan is None:
-        plan = plan_mx4(mx4_shape(pool, block_table), _cuda_device("pool", pool))
+        plan = plan_mx4(mx4_shape(pool, block_table), _cuda_index("pool", pool))
     shape = plan.shape
-    device = _check_mx4(pool, block_table, seq_lens, shape)
+    index = _check_mx4(pool, block_table, seq_lens, shape)
     n = int(n_tokens)
     if n < 0:
         raise ValueError(f"n_tokens must be >= 0, got {n}")
-    ptr = _check_indptr(indptr, n, shape, device)
-    with _on(device, stream):
-        if out is None:
-            out = tuple(torch.empty(n, shape.H_kv, shape.head_dim, dtype=torch.bfloat16, device=device)
-                        for _ in range(2))
-        for name, t in zip(("k", "v"), out):
-            _check_tensor(f"out's {name}", t, torch.bfloat16, device)
-            if tuple(t.shape) != (n, shape.H_kv, shape.head_dim):
-                raise ValueError(f"out's {name} must be [{n}][{shape.H_kv}][{shape.head_dim}], got {list(t.shape)}")
-        rc = L.pkv_mx4_read(pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), ptr, n, out[0].data_ptr(),
-                            out[1].data_ptr(), ctypes.byref(shape), plan.workspace.data_ptr(), _stream_ptr())
-    _check(rc, "pkv_mx4_read")
-    return tuple(out)
+    ptr = _check_indptr(indptr, n, shape, index)
+    dims = (n, shape.H_kv, shape.head_dim)
+    if out is None:
+        k, v = _empty(dims, torch.bfloat16, index, stream), _empty(dims, torch.bfloat16, index, stream)
+    else:
+        k, v = out
+        for name, t in (("k", k), ("v", v)):
+            _check_tensor(f"out's {name}", t, torch.bfloat16, index)
+            if t.shape != dims:
+                raise ValueError(f"out's {name} must be {list(dims)}, got {list(t.shape)}")
+    _launch(L.pkv_mx4_read, "pkv_mx4_read", index, stream, pool.data_ptr(), block_table.data_ptr(),
+            seq_lens.data_ptr(), ptr, n, k.data_ptr(), v.data_ptr(), ctypes.byref(shape), plan.workspace.data_ptr())
+    return k, v
 
 
 def mx4_decode(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -987,29 +1037,28 @@ def mx4_decode(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, s
     a captured call can be replayed after seq_lens changed on the device."""
     L = lib()
     if plan is None:
-        plan = plan_mx4(mx4_shape(pool, block_table, int(q.shape[1])), _cuda_device("pool", pool), scores is not None)
+        plan = plan_mx4(mx4_shape(pool, block_table, int(q.shape[1])), _cuda_index("pool", pool), scores is not None)
     shape = plan.shape
-    device = _check_mx4(pool, block_table, seq_lens, shape)
-    _check_tensor("q", q, torch.bfloat16, device)
-    if tuple(q.shape) != (shape.B, shape.H_q, shape.head_dim):
+    index = _check_mx4(pool, block_table, seq_lens, shape)
+    _check_tensor("q", q, torch.bfloat16, index)
+    if q.shape != (shape.B, shape.H_q, shape.head_dim):
         raise ValueError(f"q must be [{shape.B}][{shape.H_q}][{shape.head_dim}], got {list(q.shape)}")
     if (scores is not None) != bool(plan.plan.flags & FLAG_SCORES):
         raise ValueError("scores go with a plan made for them, plan_mx4(..., scores=True), and only with it")
+    score_ptr, st = None, (0, 0)
     if scores is not None:
-        _check_scores("scores", scores, torch.float32, shape.B, shape.H_kv, shape.max_pages_per_seq, device)
-    with _on(device, stream):
-        if out is None:
-            out = torch.empty_like(q)
-        _check_tensor("out", out, torch.bfloat16, device)
+        st = _check_scores("scores", scores, torch.float32, shape.B, shape.H_kv, shape.max_pages_per_seq, index)
+        score_ptr = scores.data_ptr()
+    if out is None:
+        out = _empty(q.shape, torch.bfloat16, index, stream)
+    else:
+        _check_tensor("out", out, torch.bfloat16, index)
         if out.shape != q.shape:
             raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
-        rc = L.pkv_mx4_decode(q.data_ptr(), pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), page_size,
-                              float(scale), out.data_ptr(), scores.data_ptr() if scores is not None else None,
-                              scores.stride(0) if scores is not None else 0,
-                              scores.stride(1) if scores is not None else 0, ctypes.byref(shape),
-                              ctypes.byref(plan.plan), plan.workspace.data_ptr(), plan.workspace.numel(),
-                              _stream_ptr())
-    _check(rc, "pkv_mx4_decode")
+    ws = plan.workspace
+    _launch(L.pkv_mx4_decode, "pkv_mx4_decode", index, stream, q.data_ptr(), pool.data_ptr(), block_table.data_ptr(),
+            seq_lens.data_ptr(), page_size, scale, out.data_ptr(), score_ptr, st[0], st[1], ctypes.byref(shape),
+            ctypes.byref(plan.plan), ws.data_ptr(), ws.numel())
     return out
 
 

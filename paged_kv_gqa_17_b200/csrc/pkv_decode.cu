@@ -2735,24 +2735,6 @@ int pool_tensor_map(CUtensorMap *out, const void *base, const pkv_shape &s)
 // Largest dynamic shared memory a block may request (227 KiB on sm_100).
 constexpr int kMaxDynSmem = 227 * 1024;
 
-// cudaFuncSetAttribute is per kernel and per device; `done_mask` (one per
-// kernel instantiation) remembers the devices already configured.
-template <typename K>
-cudaError_t set_smem(K kernel, int bytes, std::atomic<uint64_t> &done_mask)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess)
-        return e;
-    const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
-    if (bit && (done_mask.load() & bit))
-        return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && bit)
-        done_mask.fetch_or(bit);
-    return e;
-}
-
 // Launch geometry of one kernel instantiation on one device: its blocks
 // per SM at its own shared-memory size, the SM count and the shared memory
 // an SM offers (per-block reservation included).
@@ -2839,7 +2821,7 @@ cudaError_t launch_split(const Params &prm, int64_t grid, cudaStream_t st, bool 
     using C = Cfg<D, NT, kNW, NST>;
     static std::atomic<uint64_t> configured{0};
     auto kernel = split_kernel<D, NT, kNW, NST, CL, FILL, SCORED>;
-    cudaError_t e = set_smem(kernel, kMaxDynSmem, configured);
+    cudaError_t e = allow_smem(kernel, kMaxDynSmem, configured);
     if (e != cudaSuccess)
         return e;
     if (CL && cluster > 8) {
@@ -2893,7 +2875,7 @@ cudaError_t launch_balanced(const Params &prm, int64_t grid, cudaStream_t st, bo
     using C = BCfg<D, NT, kNW, NST>;
     static std::atomic<uint64_t> configured{0};
     auto kernel = balanced_kernel<D, NT, kNW, NST>;
-    cudaError_t e = set_smem(kernel, kMaxDynSmem, configured);
+    cudaError_t e = allow_smem(kernel, kMaxDynSmem, configured);
     if (e != cudaSuccess)
         return e;
     static std::atomic<uint64_t> occ_cache[64] = {};
@@ -2919,7 +2901,7 @@ cudaError_t launch_prefix(const Params &prm, int64_t grid, cudaStream_t st, bool
     using C = Cfg<D, 2, kNW, NST>;
     static std::atomic<uint64_t> configured{0};
     auto kernel = prefix_kernel<D, kNW, NST>;
-    cudaError_t e = set_smem(kernel, kMaxDynSmem, configured);
+    cudaError_t e = allow_smem(kernel, kMaxDynSmem, configured);
     if (e != cudaSuccess)
         return e;
     static std::atomic<uint64_t> occ_cache[64] = {};

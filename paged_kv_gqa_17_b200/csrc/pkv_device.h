@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "pkv_internal.h"
@@ -342,6 +343,23 @@ cudaError_t launch_kernel(void (*kernel)(P), unsigned grid, unsigned block, size
     cfg.numAttrs = n;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, params);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel and device (`done`: one per kernel).
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
+    if (bit && (done.load() & bit))
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && bit)
+        done.fetch_or(bit);
+    return e;
 }
 
 inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

@@ -373,8 +373,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
 template <int CS>
 cudaError_t launch_evict(const EvictParams &p, int64_t pairs, int keys, cudaStream_t st)
 {
-    const cudaError_t e =
-        cudaFuncSetAttribute(evict_kernel<CS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
+    static std::atomic<uint64_t> configured{0};
+    const cudaError_t e = allow_smem(evict_kernel<CS>, kMaxKeys * 4, configured);
     if (e != cudaSuccess)
         return e;
     return launch_kernel(evict_kernel<CS>, (unsigned)(pairs * CS), kEvictThreads, (size_t)keys * 4, st, true, p, CS);

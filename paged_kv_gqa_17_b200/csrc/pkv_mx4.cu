@@ -17,7 +17,6 @@
 #include "pkv_device.h"
 
 #include <algorithm>
-#include <atomic>
 #include <climits>
 #include <cstring>
 
@@ -1388,7 +1387,8 @@ cudaError_t launch_mx4(const DecodeParams &p, cudaStream_t st, bool pdl)
     using C = DCfg<D, NT>;
     auto kernel = mx4_decode_kernel<D, NT, SCORED>;
     const size_t smem = (size_t)C::kPrefixOff + (size_t)(p.B + 1) * 4;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    static std::atomic<uint64_t> configured{0};
+    const cudaError_t e = allow_smem(kernel, 227 * 1024, configured);
     if (e != cudaSuccess)
         return e;
     return launch_kernel(kernel, (unsigned)p.blocks, C::kThreads, smem, st, pdl, p);
