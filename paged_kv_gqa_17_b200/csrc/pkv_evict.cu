@@ -13,25 +13,31 @@
 // are filled instead of everything behind the first one being moved up: for a
 // row one page over its budget that is 16 + recent rows instead of nearly all.
 //
-// One thread-block cluster works on each (row, KV head); its blocks own
-// contiguous, ascending shares of [0, M).
-//   1. Scores become 32-bit keys in the order of the floats, kept in shared
-//      memory (read again from L2 past kMaxKeys per block), and a radix select
-//      finds the A-th largest key T in four 8-bit digits: each block counts
-//      its keys per digit value, the blocks' counts are added through
-//      distributed shared memory, and every block finds the digit itself.
+// One thread-block cluster works on each (row, KV head).
+//   1. Scores become 32-bit keys in the order of the floats, held in shared
+//      memory, and a radix select finds the A-th largest key T in four 8-bit
+//      digits: count the keys per digit value, then every warp finds the digit
+//      for itself from the counts (three count buffers in turn, so that one
+//      barrier per digit is enough).
 //   2. Each warp counts its segment's keys above T and equal to T; prefix sums
-//      over warps and blocks give every key its rank, so which equals stay and
-//      which hole meets which mover follow without another sort.  The two
-//      ascending lists go to the workspace.
-//   3. The moves are copied unit by unit (16 bytes, or less where a row is
-//      shorter) over all threads of the cluster.  Their sources lie at or
-//      behind A and their destinations before it, so their order is free.
-//   4. After a cluster barrier the recent tokens move down: a barrier between
-//      a batch's loads and its stores keeps overlapping ranges apart.
+//      give every key its rank, so which equals stay and which hole meets which
+//      mover follow without another sort.
+//   3. The moves are copied over all threads of the cluster, each thread one
+//      copy unit (16 bytes, or less where a row is shorter) of a token per
+//      step.  A move's source lies at or behind A and its destination before
+//      it, so their order is free.
+//   4. The recent tokens' first batch is loaded beside the moves; after a
+//      cluster barrier (every mover read, every batch loaded) it is stored.
+//      Longer windows repeat load, barrier, store.
+// Up to kLocalKeys tokens every block of the cluster selects for itself, over
+// all keys: a few thousand keys cost less than the cluster barriers that
+// sharing them takes (64 pairs of 2064 tokens: 24.4 us with shared selection).
+// Above, the blocks own contiguous shares of [0, M), add their counts through
+// distributed shared memory and hand the two lists over through the workspace.
 // Every write has one writer, so results are deterministic.
 #include "pkv_device.h"
 
+#include <algorithm>
 #include <climits>
 #include <cstring>
 
@@ -41,11 +47,13 @@ namespace {
 
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kMaxKeys = 16384;  // keys a block holds in shared memory
+constexpr int kLocalKeys = 8192;    // capacity up to which every block selects for itself
+constexpr int kMaxKeys = 16384;     // shared selection: keys a block holds (the rest is read again)
+constexpr int kMaxTable = 2048;     // block-table entries a block holds
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 256;
 constexpr int kMaxPlanes = PKV_EVICT_MAX_PLANES;
-constexpr int kBatch = 4;        // units a thread copies at once
+constexpr int kBatch = 4;           // units a thread has in flight
 
 // One array that moves with the tokens.  Paged: row bytes at
 // base + page * s0 + head * s1 + slot_in_page * s2; dense (scores,
@@ -69,6 +77,7 @@ struct EvictParams {
     int32_t *lists;  // per (row, head): holes [capacity / 2], movers [capacity / 2]
     uint32_t *ws_error;
     int32_t H_kv, max_pages, num_pool_pages, budget, recent;
+    int32_t held_keys, held_table;  // keys and block-table entries a block keeps in shared memory
     int64_t capacity;
 };
 
@@ -97,13 +106,12 @@ union Unit {
     uint8_t v1;
 };
 
-struct EvictShared {
-    uint32_t hist[2][kBins];  // by digit parity: a peer may still read one while the other is counted
-    uint32_t total[kBins];    // the cluster's counts of this digit
+struct __align__(16) EvictShared {
+    uint32_t hist[3][kBins];
+    uint32_t total[kBins];                  // shared selection: the cluster's counts of this digit
     uint32_t gt[kEvictWarps], eq[kEvictWarps];
-    uint32_t block_gt, block_eq;  // read by the peers
-    uint32_t moves;               // likewise, from the block that owns slot A
-    uint32_t digit, above;        // the chosen digit value and how many keys lie above it
+    uint32_t block_gt, block_eq;            // read by the peers
+    uint32_t moves;                         // likewise, written by the block that owns slot A
 };
 
 // The cluster's barrier: of one block, the block's.
@@ -116,15 +124,29 @@ __device__ __forceinline__ void evict_sync()
         cluster_sync_all();
 }
 
-template <int CS>
-__global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_constant__ EvictParams p)
+// Which unit of a token a thread copies, and where.
+struct UnitAddress {
+    uint8_t *base;       // of this (row, head) and unit; NULL: no unit for this thread
+    int64_t page, slot;  // strides
+    int32_t size, dense;
+};
+
+template <int CS, bool LOCAL>
+__global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_constant__ EvictParams p)
 {
+    // [keys][block table][LOCAL: holes, movers as 16-bit slots]
     extern __shared__ uint32_t s_keys[];
     __shared__ EvictShared sh;
+    int32_t *s_table = reinterpret_cast<int32_t *>(s_keys + p.held_keys);
+    uint16_t *s_holes = reinterpret_cast<uint16_t *>(s_table + p.held_table);
+    uint16_t *s_movers = s_holes + p.capacity / 2;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = CS == 1 ? 0 : (int)cluster_ctarank();
     const int pair = blockIdx.x / CS;
-    const int row = pair / p.H_kv, head = pair % p.H_kv;
+    const int row = pair / p.H_kv, head = pair - row * p.H_kv;
+    const int32_t *table = p.block_table + (int64_t)row * p.max_pages;
+    for (int i = tid; i < 3 * kBins; i += kEvictThreads)
+        sh.hist[0][i] = 0;
     grid_dependency_wait();
     grid_launch_dependents();
     const int N = __ldg(p.seq_lens + row);
@@ -145,84 +167,93 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
     const int half = (int)(p.capacity / 2);
     int32_t *holes = p.lists + (int64_t)pair * 2 * half;
     int32_t *movers = holes + half;
+    for (int i = tid; i < min(p.held_table, (N + kPage - 1) / kPage); i += kEvictThreads)
+        s_table[i] = __ldg(table + i);
 
     int moves = 0;
     if (A > 0) {
-        const int share = (M + CS - 1) / CS;
-        const int lo = min(rank * share, M), count = min(lo + share, M) - lo;
-        const int held = min(count, kMaxKeys);
+        const int share = LOCAL ? M : (M + CS - 1) / CS;
+        const int lo = LOCAL ? 0 : min(rank * share, M), count = min(lo + share, M) - lo;
+        const int held = LOCAL ? count : min(count, kMaxKeys);
         for (int i = tid; i < held; i += kEvictThreads)
             s_keys[i] = score_key(scores[lo + i]);
-        auto key_at = [&](int i) { return i < held ? s_keys[i] : score_key(scores[lo + i]); };
+        auto key_at = [&](int i) { return LOCAL || i < held ? s_keys[i] : score_key(scores[lo + i]); };
+        evict_sync<CS>();  // no block moves a score that another has yet to read
 
         // ---- 1. the A-th largest key ----
         uint32_t prefix = 0, need = (uint32_t)A;  // T's digits so far; its rank among the keys that share them
-        for (int shift = 24, d = 0; shift >= 0; shift -= 8, ++d) {
-            uint32_t *hist = sh.hist[d & 1];
-            for (int i = tid; i < kBins; i += kEvictThreads)
-                hist[i] = 0;
-            __syncthreads();
-            const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const int shift = 24 - 8 * d;
+            uint32_t *hist = sh.hist[d % 3];
+            if (d == 2)  // every warp, and every peer, is past its reading of the first counts
+                for (int i = tid; i < kBins; i += kEvictThreads)
+                    sh.hist[0][i] = 0;
             for (int i0 = 0; i0 < count; i0 += kEvictThreads) {
                 const int i = i0 + tid;
                 uint32_t bin = kBins;  // not counted
                 if (i < count) {
                     const uint32_t key = key_at(i);
-                    if ((key & mask) == prefix)
+                    if (d == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
                         bin = (key >> shift) & (kBins - 1);
                 }
-                // equal digits in a whole warp (scores of like size) are one addition
-                int same;
-                __match_all_sync(0xffffffffu, bin, &same);
-                if (same) {
-                    if (lane == 0 && bin < kBins)
-                        atomicAdd(hist + bin, 32u);
+                if (d == 0) {
+                    // scores share their leading bits: one addition per value and warp
+                    const uint32_t same = __match_any_sync(0xffffffffu, bin);
+                    if (bin < kBins && lane == __ffs(same) - 1)
+                        atomicAdd(hist + bin, __popc(same));
                 } else if (bin < kBins) {
                     atomicAdd(hist + bin, 1u);
                 }
             }
-            evict_sync<CS>();
-            if (tid < kBins) {
-                uint32_t sum = 0;
-                if (CS == 1) {
-                    sum = hist[tid];
-                } else {
+            const uint32_t *total = hist;
+            if (LOCAL) {
+                __syncthreads();
+            } else {
+                evict_sync<CS>();
+                if (tid < kBins) {
+                    uint32_t sum = 0;
                     const uint32_t at = smem_addr(hist + tid);
 #pragma unroll
                     for (int c = 0; c < CS; ++c)
-                        sum += ld_cluster_u32(map_shared_rank(at, (uint32_t)c));
+                        sum += CS == 1 ? hist[tid] : ld_cluster_u32(map_shared_rank(at, (uint32_t)c));
+                    sh.total[tid] = sum;
                 }
-                sh.total[tid] = sum;
+                __syncthreads();
+                total = sh.total;
             }
-            __syncthreads();
-            if (warp == 0) {
-                // lane l holds bins 255 - 8 l down to 248 - 8 l: a prefix sum over lanes counts from the top
-                uint32_t sum = 0;
-                for (int j = 0; j < 8; ++j)
-                    sum += sh.total[kBins - 1 - (lane * 8 + j)];
-                uint32_t incl = sum;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o)
-                        incl += v;
-                }
-                uint32_t above = incl - sum;
-                if (above < need && need <= incl) {
-                    for (int j = 0; j < 8; ++j) {
-                        const int bin = kBins - 1 - (lane * 8 + j);
-                        const uint32_t c = sh.total[bin];
-                        if (need <= above + c) {
-                            sh.digit = (uint32_t)bin;
-                            sh.above = above;
-                            break;
-                        }
-                        above += c;
+            // lane l holds bins 255 - 8 l down to 248 - 8 l: a prefix sum over lanes counts from the top
+            uint32_t n[8], sum = 0;
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(total + kBins - 4 - (lane * 8 + j));
+                n[j] = v.w, n[j + 1] = v.z, n[j + 2] = v.y, n[j + 3] = v.x;
+                sum += v.x + v.y + v.z + v.w;
+            }
+            uint32_t incl = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o)
+                    incl += v;
+            }
+            uint32_t above = incl - sum, digit = 0;
+            const bool mine = above < need && need <= incl;
+            if (mine) {
+                bool found = false;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    found = found || need <= above + n[j];
+                    if (!found) {
+                        above += n[j];
+                        digit = j + 1;
                     }
                 }
+                digit = kBins - 1 - (lane * 8 + digit);
             }
-            __syncthreads();
-            prefix |= sh.digit << shift;
-            need -= sh.above;
+            const int owner = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+            prefix |= __shfl_sync(0xffffffffu, digit, owner) << shift;
+            need -= __shfl_sync(0xffffffffu, above, owner);
         }
         const uint32_t T = prefix;  // `need` >= 1 of the keys equal to T stay, the first ones
 
@@ -241,22 +272,33 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
             sh.eq[warp] = eq;
         }
         __syncthreads();
-        if (tid == 0) {
-            uint32_t g = 0, e = 0;
-            for (int w = 0; w < kEvictWarps; ++w) {
-                const uint32_t gw = sh.gt[w], ew = sh.eq[w];
-                sh.gt[w] = g;
-                sh.eq[w] = e;
-                g += gw;
-                e += ew;
+        {
+            // counts of the warps before this one
+            uint32_t g = lane < kEvictWarps ? sh.gt[lane] : 0u, e = lane < kEvictWarps ? sh.eq[lane] : 0u;
+            if (!LOCAL && warp == 0) {
+                uint32_t all_g = g, all_e = e;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    all_g += __shfl_xor_sync(0xffffffffu, all_g, o);
+                    all_e += __shfl_xor_sync(0xffffffffu, all_e, o);
+                }
+                if (lane == 0) {
+                    sh.block_gt = all_g;
+                    sh.block_eq = all_e;
+                }
             }
-            sh.block_gt = g;
-            sh.block_eq = e;
+            g = lane < warp ? g : 0u;
+            e = lane < warp ? e : 0u;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                g += __shfl_xor_sync(0xffffffffu, g, o);
+                e += __shfl_xor_sync(0xffffffffu, e, o);
+            }
+            gt = g;
+            eq = e;
         }
-        evict_sync<CS>();
-        gt = sh.gt[warp];
-        eq = sh.eq[warp];
-        if (CS > 1) {
+        if (!LOCAL) {
+            evict_sync<CS>();
             const uint32_t ag = smem_addr(&sh.block_gt), ae = smem_addr(&sh.block_eq);
 #pragma unroll
             for (int c = 0; c < CS; ++c)
@@ -272,112 +314,183 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const __grid_const
             const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
             const uint32_t below = (1u << lane) - 1u;
             const uint32_t eq_before = eq + __popc(be & below);
-            const uint32_t kept_before = gt + __popc(bg & below) + min(eq_before, need);
+            const int kept_before = (int)(gt + __popc(bg & below) + min(eq_before, need));
             if (i < s1) {
                 const int slot = lo + i;
                 const bool keep = is_gt || (is_eq && eq_before < need);
-                if (slot < A && !keep)
-                    holes[slot - (int)kept_before] = slot;
-                if (slot >= A && keep)
-                    movers[A - 1 - (int)kept_before] = slot;  // the j-th mover from the end
+                if (slot < A && !keep) {
+                    if (LOCAL)
+                        s_holes[slot - kept_before] = (uint16_t)slot;
+                    else
+                        holes[slot - kept_before] = slot;
+                }
+                if (slot >= A && keep) {  // the j-th mover from the end
+                    if (LOCAL)
+                        s_movers[A - 1 - kept_before] = (uint16_t)slot;
+                    else
+                        movers[A - 1 - kept_before] = slot;
+                }
                 if (slot == A) {
                     // kept_before tokens keep their slots below A: the other slots there are holes
-                    for (int c = 0; c < CS; ++c) {
-                        const uint32_t at = CS == 1 ? smem_addr(&sh.moves) : map_shared_rank(smem_addr(&sh.moves), (uint32_t)c);
-                        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"((uint32_t)A - kept_before)
-                                     : "memory");
-                    }
+                    if (LOCAL || CS == 1)
+                        sh.moves = (uint32_t)(A - kept_before);
+                    else
+                        for (int c = 0; c < CS; ++c)
+                            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
+                                             map_shared_rank(smem_addr(&sh.moves), (uint32_t)c)),
+                                         "r"((uint32_t)(A - kept_before))
+                                         : "memory");
                 }
             }
             gt += __popc(bg);
             eq += __popc(be);
         }
-        evict_sync<CS>();
+        if (LOCAL)
+            __syncthreads();
+        else
+            evict_sync<CS>();
         moves = (int)sh.moves;
+    } else {
+        __syncthreads();  // the table
     }
 
-    const int32_t *table = p.block_table + (int64_t)row * p.max_pages;
-    // The bytes of unit u of the token in `slot`; NULL where its page id is out of range.
-    auto unit_at = [&](const EvictPlane &pl, int u, int slot) -> uint8_t * {
-        const int64_t in = (int64_t)(u - pl.first) * pl.unit;
+    // ---- 3. and 4. the copies ----
+    // A token's units lie side by side over the threads; as many tokens at once as fit.
+    const int abreast = max(1, kEvictThreads / p.units);
+    const int first_token = p.units <= kEvictThreads ? tid / p.units : 0;
+    const int first_unit = p.units <= kEvictThreads ? tid - first_token * p.units : tid;
+    const int stride = abreast * CS;                          // tokens per step of the cluster
+    const int first = first_token < abreast ? rank * abreast + first_token : INT_MAX / 2;
+    auto address = [&](int u) {
+        UnitAddress t{nullptr, 0, 0, 0, 0};
+        if (u >= p.units)
+            return t;
+        int which = 0;
+        while (which + 1 < p.n_planes && u >= p.plane[which + 1].first)
+            ++which;
+        const EvictPlane &pl = p.plane[which];
+        t.dense = pl.dense;
+        t.size = pl.unit;
+        t.base = pl.base + (int64_t)(u - pl.first) * pl.unit + (int64_t)head * pl.s1;
         if (pl.dense)
-            return pl.base + (int64_t)row * pl.s0 + (int64_t)head * pl.s1 + (int64_t)slot * pl.s2 + in;
-        const int page = __ldg(table + slot / kPage);
+            t.base += (int64_t)row * pl.s0;
+        t.page = pl.s0;
+        t.slot = pl.s2;
+        return t;
+    };
+    // The unit of the token in `slot`; NULL where its page id is out of range.
+    auto at = [&](const UnitAddress &t, int slot) -> uint8_t * {
+        if (t.dense)
+            return t.base + slot * t.slot;
+        const int index = slot / kPage;
+        const int page = index < p.held_table ? s_table[index] : __ldg(table + index);
         if (page < 0 || page >= p.num_pool_pages) {
             atomicOr(p.ws_error, kErrPageId);
             return nullptr;
         }
-        return pl.base + (int64_t)page * pl.s0 + (int64_t)head * pl.s1 + (int64_t)(slot % kPage) * pl.s2 + in;
+        return t.base + page * t.page + (slot % kPage) * t.slot;
     };
-    // Copies the units of `tokens` moves (token j from source(j) to target(j));
-    // SEPARATE: a cluster barrier keeps a batch's loads before its stores.
-    auto copy = [&](int tokens, auto source, auto target, bool separate) {
-        const int64_t all = (int64_t)tokens * p.units;
-        const int64_t stride = (int64_t)CS * kEvictThreads;
-        for (int64_t b0 = 0; b0 < all; b0 += stride * kBatch) {
-            Unit val[kBatch];
-            uint8_t *dst[kBatch];
-            int size[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int64_t at = b0 + k * stride + rank * kEvictThreads + tid;
-                dst[k] = nullptr;
-                size[k] = 0;
-                if (at < all) {
-                    const int j = (int)(at / p.units), u = (int)(at % p.units);
-                    int which = 0;
-                    while (which + 1 < p.n_planes && u >= p.plane[which + 1].first)
-                        ++which;
-                    const EvictPlane &pl = p.plane[which];
-                    const uint8_t *src = unit_at(pl, u, source(j));
-                    dst[k] = unit_at(pl, u, target(j));
-                    if (!src)
-                        dst[k] = nullptr;
-                    if (dst[k]) {
-                        size[k] = pl.unit;
-                        switch (pl.unit) {
-                        case 16: val[k].v16 = *reinterpret_cast<const uint4 *>(src); break;
-                        case 8: val[k].v8 = *reinterpret_cast<const uint2 *>(src); break;
-                        case 4: val[k].v4 = *reinterpret_cast<const uint32_t *>(src); break;
-                        case 2: val[k].v2 = *reinterpret_cast<const uint16_t *>(src); break;
-                        default: val[k].v1 = *src; break;
-                        }
-                    }
-                }
-            }
-            if (separate)
-                evict_sync<CS>();
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                if (!dst[k])
-                    continue;
-                switch (size[k]) {
-                case 16: *reinterpret_cast<uint4 *>(dst[k]) = val[k].v16; break;
-                case 8: *reinterpret_cast<uint2 *>(dst[k]) = val[k].v8; break;
-                case 4: *reinterpret_cast<uint32_t *>(dst[k]) = val[k].v4; break;
-                case 2: *reinterpret_cast<uint16_t *>(dst[k]) = val[k].v2; break;
-                default: *dst[k] = val[k].v1; break;
-                }
-            }
+    auto load = [&](Unit &v, const uint8_t *src, int size) {
+        switch (size) {
+        case 16: v.v16 = *reinterpret_cast<const uint4 *>(src); break;
+        case 8: v.v8 = *reinterpret_cast<const uint2 *>(src); break;
+        case 4: v.v4 = *reinterpret_cast<const uint32_t *>(src); break;
+        case 2: v.v2 = *reinterpret_cast<const uint16_t *>(src); break;
+        default: v.v1 = *src; break;
         }
     };
-    // ---- 3. holes, then 4. the recent tokens ----
-    copy(moves, [&](int j) { return movers[moves - 1 - j]; }, [&](int j) { return holes[j]; }, false);
-    evict_sync<CS>();  // every mover has been read: the recent tokens may take their slots
-    copy(p.recent, [&](int j) { return M + j; }, [&](int j) { return A + j; }, true);
+    auto store = [&](uint8_t *dst, const Unit &v, int size) {
+        switch (size) {
+        case 16: *reinterpret_cast<uint4 *>(dst) = v.v16; break;
+        case 8: *reinterpret_cast<uint2 *>(dst) = v.v8; break;
+        case 4: *reinterpret_cast<uint32_t *>(dst) = v.v4; break;
+        case 2: *reinterpret_cast<uint16_t *>(dst) = v.v2; break;
+        default: *dst = v.v1; break;
+        }
+    };
+    for (int u = first_unit; u < p.units; u += kEvictThreads) {  // one round unless a token has more units than threads
+        const UnitAddress t = address(u);
+        for (int j0 = first; j0 < moves; j0 += kBatch * stride) {
+            Unit val[kBatch];
+            uint8_t *dst[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int j = j0 + k * stride;
+                dst[k] = nullptr;
+                if (j < moves) {
+                    const uint8_t *src = at(t, LOCAL ? s_movers[moves - 1 - j] : __ldcg(movers + moves - 1 - j));
+                    dst[k] = at(t, LOCAL ? s_holes[j] : __ldcg(holes + j));
+                    if (!src)
+                        dst[k] = nullptr;
+                    if (dst[k])
+                        load(val[k], src, t.size);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (dst[k])
+                    store(dst[k], val[k], t.size);
+        }
+    }
+    // The recent tokens, in batches: all of a batch is loaded before any of it is stored, everywhere in
+    // the cluster; their targets hold movers, which the first barrier has read.  A batch's targets never
+    // hold a later batch's sources.
+    const int rounds = (p.units + kEvictThreads - 1) / kEvictThreads;
+    bool first_batch = true;
+    for (int r = 0; r < rounds; ++r) {
+        const UnitAddress t = address(first_unit + r * kEvictThreads);
+        for (int b0 = 0; b0 < p.recent; b0 += kBatch * stride) {
+            Unit val[kBatch];
+            uint8_t *dst[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int j = b0 + first + k * stride;
+                dst[k] = nullptr;
+                if (t.base && j < p.recent) {
+                    const uint8_t *src = at(t, M + j);
+                    dst[k] = at(t, A + j);
+                    if (!src)
+                        dst[k] = nullptr;
+                    if (dst[k])
+                        load(val[k], src, t.size);
+                }
+            }
+            evict_sync<CS>();
+            first_batch = false;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (dst[k])
+                    store(dst[k], val[k], t.size);
+        }
+    }
+    if (first_batch)
+        evict_sync<CS>();
     // vacated slots start from zero when new tokens take them (all loads lie before a barrier above)
-    for (int t = p.budget + rank * kEvictThreads + tid; t < N; t += CS * kEvictThreads)
-        scores[t] = 0.f;
+    for (int i = p.budget + rank * kEvictThreads + tid; i < N; i += CS * kEvictThreads)
+        scores[i] = 0.f;
 }
 
-template <int CS>
-cudaError_t launch_evict(const EvictParams &p, int64_t pairs, int keys, cudaStream_t st)
+template <int CS, bool LOCAL>
+cudaError_t launch_evict(const EvictParams &p, int64_t pairs, cudaStream_t st)
 {
     static std::atomic<uint64_t> configured{0};
-    const cudaError_t e = allow_smem(evict_kernel<CS>, kMaxKeys * 4, configured);
+    auto kernel = evict_kernel<CS, LOCAL>;
+    const cudaError_t e = allow_smem(kernel, (kMaxKeys + kMaxTable) * 4, configured);
     if (e != cudaSuccess)
         return e;
-    return launch_kernel(evict_kernel<CS>, (unsigned)(pairs * CS), kEvictThreads, (size_t)keys * 4, st, true, p, CS);
+    const size_t smem = (size_t)(p.held_keys + p.held_table) * 4 + (LOCAL ? (size_t)p.capacity * 2 : 0);
+    return launch_kernel(kernel, (unsigned)(pairs * CS), kEvictThreads, smem, st, true, p, CS);
+}
+
+template <bool LOCAL>
+cudaError_t launch_evict_any(int cluster, const EvictParams &p, int64_t pairs, cudaStream_t st)
+{
+    switch (cluster) {
+    case 8: return launch_evict<8, LOCAL>(p, pairs, st);
+    case 4: return launch_evict<4, LOCAL>(p, pairs, st);
+    case 2: return launch_evict<2, LOCAL>(p, pairs, st);
+    default: return launch_evict<1, LOCAL>(p, pairs, st);
+    }
 }
 
 // The largest copy unit that divides a plane's row and all its addresses.
@@ -430,7 +543,7 @@ int pkv_evict_tokens(float *scores, int64_t score_stride_row, int64_t score_stri
         return PKV_ERR_UNSUPPORTED;
     const int64_t capacity = (int64_t)s.max_pages_per_seq * kPage;
     const int64_t pairs = (int64_t)s.B * s.H_kv;
-    if (capacity > INT32_MAX || pairs * kMaxCluster > INT32_MAX)
+    if (capacity > INT32_MAX / 4 || pairs * kMaxCluster > INT32_MAX)
         return PKV_ERR_UNSUPPORTED;
     size_t need = 0;
     pkv_evict_workspace_bytes(shape, &need);
@@ -477,15 +590,15 @@ int pkv_evict_tokens(float *scores, int64_t score_stride_row, int64_t score_stri
     p.capacity = capacity;
 
     int cluster = 1;
-    while (cluster < kMaxCluster && pairs * cluster * 2 <= 296 && capacity / (cluster * 2) >= 512)
+    while (cluster < kMaxCluster && pairs * cluster * 2 <= 296 && capacity / (cluster * 2) >= 256)
         cluster *= 2;
-    const int64_t share = ceil_div(capacity, cluster);
-    const int keys = (int)(share < kMaxKeys ? share : kMaxKeys);
+    const bool local = capacity <= kLocalKeys;
+    p.held_keys = (int32_t)(local ? capacity : std::min<int64_t>(ceil_div(capacity, cluster), kMaxKeys));
+    p.held_keys = (p.held_keys + 3) & ~3;
+    p.held_table = std::min(s.max_pages_per_seq, kMaxTable);
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = cluster == 8   ? launch_evict<8>(p, pairs, keys, st)
-                          : cluster == 4 ? launch_evict<4>(p, pairs, keys, st)
-                          : cluster == 2 ? launch_evict<2>(p, pairs, keys, st)
-                                         : launch_evict<1>(p, pairs, keys, st);
+    const cudaError_t e = local ? launch_evict_any<true>(cluster, p, pairs, st)
+                                : launch_evict_any<false>(cluster, p, pairs, st);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
