@@ -26,12 +26,12 @@
 //      copy unit (16 bytes, or less where a row is shorter) of a token per
 //      step.  A move's source lies at or behind A and its destination before
 //      it, so their order is free.
-//   4. The recent tokens' first batch is loaded beside the moves; after a
+//   4. The recent tokens' first batch is loaded beside the selection; after a
 //      cluster barrier (every mover read, every batch loaded) it is stored.
 //      Longer windows repeat load, barrier, store.
-// Up to kLocalKeys tokens every block of the cluster selects for itself, over
-// all keys: a few thousand keys cost less than the cluster barriers that
-// sharing them takes (64 pairs of 2064 tokens: 24.4 us with shared selection).
+// Up to kLocalKeys tokens the cluster's first block selects alone and the others
+// read its lists through distributed shared memory: a few thousand keys cost
+// less than the cluster barriers that sharing them takes.
 // Above, the blocks own contiguous shares of [0, M), add their counts through
 // distributed shared memory and hand the two lists over through the workspace.
 // Every write has one writer, so results are deterministic.
@@ -45,15 +45,18 @@ namespace pkv {
 
 namespace {
 
-constexpr int kEvictThreads = 512;
+constexpr int kEvictThreads = 256;
+constexpr int kEvictPerSM = 2;       // blocks an SM holds
 constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kLocalKeys = 8192;    // capacity up to which every block selects for itself
+constexpr int kLocalKeys = 8192;    // capacity up to which one block selects for its cluster
 constexpr int kMaxKeys = 16384;     // shared selection: keys a block holds (the rest is read again)
 constexpr int kMaxTable = 2048;     // block-table entries a block holds
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 256;
+constexpr int kBins = 256;          // shared selection: 8-bit digits
+constexpr int kLocalBins = 2048;    // one block's: 11-bit digits
 constexpr int kMaxPlanes = PKV_EVICT_MAX_PLANES;
-constexpr int kBatch = 4;           // units a thread has in flight
+constexpr int kWide = 8;            // 16-byte units a thread has in flight
+constexpr int kNarrow = 2;          // smaller ones
 
 // One array that moves with the tokens.  Paged: row bytes at
 // base + page * s0 + head * s1 + slot_in_page * s2; dense (scores,
@@ -68,7 +71,7 @@ struct EvictPlane {
 
 struct EvictParams {
     EvictPlane plane[kMaxPlanes + 2];
-    int32_t n_planes, units;  // units per token over all planes
+    int32_t n_planes, wide, units;  // units per token: of 16 bytes, and in all (those of 16 bytes first)
     float *scores;
     int64_t score_row, score_head;
     const int32_t *block_table;
@@ -98,20 +101,26 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr)
     return v;
 }
 
-union Unit {
-    uint4 v16;
-    uint2 v8;
-    uint32_t v4;
-    uint16_t v2;
-    uint8_t v1;
-};
+__device__ __forceinline__ int ld_cluster_u16(uint32_t addr)
+{
+    uint16_t v;
+    asm volatile("ld.shared::cluster.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
+}
 
 struct __align__(16) EvictShared {
-    uint32_t hist[3][kBins];
-    uint32_t total[kBins];                  // shared selection: the cluster's counts of this digit
+    union {
+        uint32_t local[kLocalBins];
+        struct {
+            uint32_t hist[3][kBins];
+            uint32_t total[kBins];  // the cluster's counts of this digit
+        };
+    };
+    uint32_t warp_sum[kEvictWarps];
+    uint32_t digit, above;
     uint32_t gt[kEvictWarps], eq[kEvictWarps];
-    uint32_t block_gt, block_eq;            // read by the peers
-    uint32_t moves;                         // likewise, written by the block that owns slot A
+    uint32_t block_gt, block_eq;  // read by the peers
+    uint32_t moves;               // likewise, written by the block that owns slot A
 };
 
 // The cluster's barrier: of one block, the block's.
@@ -124,15 +133,143 @@ __device__ __forceinline__ void evict_sync()
         cluster_sync_all();
 }
 
-// Which unit of a token a thread copies, and where.
+__device__ __forceinline__ uint32_t inclusive_scan(uint32_t v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o)
+            v += up;
+    }
+    return v;
+}
+
+// visit(i, key_at(i)) for this thread's share of [0, count), four keys loaded at a time.
+template <typename K, typename V>
+__device__ __forceinline__ void for_keys(int count, int tid, K key_at, V visit)
+{
+    for (int i0 = 0; i0 < count; i0 += 4 * kEvictThreads) {
+        uint32_t key[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * kEvictThreads + tid;
+            key[k] = i < count ? key_at(i) : 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i0 + k * kEvictThreads + tid < count)
+                visit(key[k]);
+    }
+}
+
+// The need-th largest of `count` keys (1 <= need <= count) in shared memory, by
+// one block: three digits of 11, 11 and 10 bits.  `need` becomes its rank
+// among the keys equal to it.  sh.local is zero before and after.
+__device__ __forceinline__ uint32_t select_local(EvictShared &sh, const uint32_t *keys, int count, uint32_t &need)
+{
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kPer = kLocalBins / kEvictThreads;  // bins per thread, from the top
+    static_assert(kPer == 8, "two 16-byte reads");
+    uint32_t prefix = 0;
+#pragma unroll
+    for (int d = 0; d < 3; ++d) {
+        const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+        const uint32_t mask = d == 2 ? 1023u : 2047u;
+        for_keys(count, tid, [&](int i) { return keys[i]; }, [&](uint32_t key) {
+            if (d == 0 || (key >> (d == 1 ? 21 : 10)) == (prefix >> (d == 1 ? 21 : 10)))
+                atomicAdd(sh.local + ((key >> shift) & mask), 1u);
+        });
+        __syncthreads();
+        uint4 *mine = reinterpret_cast<uint4 *>(sh.local + kLocalBins - kPer - tid * kPer);
+        const uint4 hi = mine[1], lo = mine[0];
+        mine[0] = mine[1] = make_uint4(0, 0, 0, 0);
+        const uint32_t n[kPer] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};  // descending
+        const uint32_t sum = n[0] + n[1] + n[2] + n[3] + n[4] + n[5] + n[6] + n[7];
+        const uint32_t incl = inclusive_scan(sum, lane);
+        if (lane == 31)
+            sh.warp_sum[warp] = incl;
+        __syncthreads();
+        uint32_t above = incl - sum;
+#pragma unroll
+        for (int w = 0; w < kEvictWarps; ++w)
+            above += w < warp ? sh.warp_sum[w] : 0u;
+        if (above < need && need <= above + sum) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                if (above < need && need <= above + n[j]) {
+                    sh.digit = (uint32_t)(kLocalBins - 1 - tid * kPer - j);
+                    sh.above = above;
+                }
+                above += n[j];
+            }
+        }
+        __syncthreads();
+        prefix |= sh.digit << shift;
+        need -= sh.above;
+    }
+    return prefix;
+}
+
+// The same over the keys of all CS blocks (`key_at` gives this block's), in
+// four digits of 8 bits: the blocks' counts are added through distributed
+// shared memory.  sh.hist is zero before.
+template <int CS, typename K>
+__device__ __forceinline__ uint32_t select_shared(EvictShared &sh, K key_at, int count, uint32_t &need)
+{
+    const int tid = threadIdx.x, lane = tid & 31;
+    uint32_t prefix = 0;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const int shift = 24 - 8 * d;
+        uint32_t *hist = sh.hist[d % 3];  // in turn, so that one barrier per digit is enough
+        if (d == 2)  // every warp, and every peer, is past its reading of the first counts
+            for (int i = tid; i < kBins; i += kEvictThreads)
+                sh.hist[0][i] = 0;
+        for_keys(count, tid, key_at, [&](uint32_t key) {
+            if (d == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
+                atomicAdd(hist + ((key >> shift) & (kBins - 1)), 1u);
+        });
+        evict_sync<CS>();
+        if (tid < kBins) {
+            uint32_t sum = 0;
+            const uint32_t at = smem_addr(hist + tid);
+#pragma unroll
+            for (int c = 0; c < CS; ++c)
+                sum += CS == 1 ? hist[tid] : ld_cluster_u32(map_shared_rank(at, (uint32_t)c));
+            sh.total[tid] = sum;
+        }
+        __syncthreads();
+        // lane l of every warp holds bins 255 - 8 l down to 248 - 8 l
+        const uint4 *bins = reinterpret_cast<const uint4 *>(sh.total + kBins - 8 - lane * 8);
+        const uint4 hi = bins[1], lo = bins[0];
+        const uint32_t n[8] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
+        const uint32_t sum = n[0] + n[1] + n[2] + n[3] + n[4] + n[5] + n[6] + n[7];
+        uint32_t above = inclusive_scan(sum, lane) - sum, digit = 0, rest = 0;
+        const bool mine = above < need && need <= above + sum;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (above < need && need <= above + n[j]) {
+                digit = (uint32_t)(kBins - 1 - lane * 8 - j);
+                rest = above;
+            }
+            above += n[j];
+        }
+        const int owner = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+        prefix |= __shfl_sync(0xffffffffu, digit, owner) << shift;
+        need -= __shfl_sync(0xffffffffu, rest, owner);
+    }
+    return prefix;
+}
+
+// A copy unit of one (row, head)'s tokens: where slot s's lies.
 struct UnitAddress {
-    uint8_t *base;       // of this (row, head) and unit; NULL: no unit for this thread
-    int64_t page, slot;  // strides
+    uint8_t *base;  // NULL: no unit
+    int64_t page, slot;
     int32_t size, dense;
 };
 
 template <int CS, bool LOCAL>
-__global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_constant__ EvictParams p)
+__global__ void __launch_bounds__(kEvictThreads, kEvictPerSM) evict_kernel(const __grid_constant__ EvictParams p)
 {
     // [keys][block table][LOCAL: holes, movers as 16-bit slots]
     extern __shared__ uint32_t s_keys[];
@@ -145,8 +282,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
     const int pair = blockIdx.x / CS;
     const int row = pair / p.H_kv, head = pair - row * p.H_kv;
     const int32_t *table = p.block_table + (int64_t)row * p.max_pages;
-    for (int i = tid; i < 3 * kBins; i += kEvictThreads)
-        sh.hist[0][i] = 0;
+    for (int i = tid; i < kLocalBins; i += kEvictThreads)
+        sh.local[i] = 0;
     grid_dependency_wait();
     grid_launch_dependents();
     const int N = __ldg(p.seq_lens + row);
@@ -170,103 +307,32 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
     for (int i = tid; i < min(p.held_table, (N + kPage - 1) / kPage); i += kEvictThreads)
         s_table[i] = __ldg(table + i);
 
-    int moves = 0;
-    if (A > 0) {
+    if (A > 0 && (!LOCAL || rank == 0)) {
         const int share = LOCAL ? M : (M + CS - 1) / CS;
         const int lo = LOCAL ? 0 : min(rank * share, M), count = min(lo + share, M) - lo;
         const int held = LOCAL ? count : min(count, kMaxKeys);
+#pragma unroll 4
         for (int i = tid; i < held; i += kEvictThreads)
             s_keys[i] = score_key(scores[lo + i]);
         auto key_at = [&](int i) { return LOCAL || i < held ? s_keys[i] : score_key(scores[lo + i]); };
-        evict_sync<CS>();  // no block moves a score that another has yet to read
+        __syncthreads();
 
-        // ---- 1. the A-th largest key ----
-        uint32_t prefix = 0, need = (uint32_t)A;  // T's digits so far; its rank among the keys that share them
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const int shift = 24 - 8 * d;
-            uint32_t *hist = sh.hist[d % 3];
-            if (d == 2)  // every warp, and every peer, is past its reading of the first counts
-                for (int i = tid; i < kBins; i += kEvictThreads)
-                    sh.hist[0][i] = 0;
-            for (int i0 = 0; i0 < count; i0 += kEvictThreads) {
-                const int i = i0 + tid;
-                uint32_t bin = kBins;  // not counted
-                if (i < count) {
-                    const uint32_t key = key_at(i);
-                    if (d == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
-                        bin = (key >> shift) & (kBins - 1);
-                }
-                if (d == 0) {
-                    // scores share their leading bits: one addition per value and warp
-                    const uint32_t same = __match_any_sync(0xffffffffu, bin);
-                    if (bin < kBins && lane == __ffs(same) - 1)
-                        atomicAdd(hist + bin, __popc(same));
-                } else if (bin < kBins) {
-                    atomicAdd(hist + bin, 1u);
-                }
-            }
-            const uint32_t *total = hist;
-            if (LOCAL) {
-                __syncthreads();
-            } else {
-                evict_sync<CS>();
-                if (tid < kBins) {
-                    uint32_t sum = 0;
-                    const uint32_t at = smem_addr(hist + tid);
-#pragma unroll
-                    for (int c = 0; c < CS; ++c)
-                        sum += CS == 1 ? hist[tid] : ld_cluster_u32(map_shared_rank(at, (uint32_t)c));
-                    sh.total[tid] = sum;
-                }
-                __syncthreads();
-                total = sh.total;
-            }
-            // lane l holds bins 255 - 8 l down to 248 - 8 l: a prefix sum over lanes counts from the top
-            uint32_t n[8], sum = 0;
-#pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(total + kBins - 4 - (lane * 8 + j));
-                n[j] = v.w, n[j + 1] = v.z, n[j + 2] = v.y, n[j + 3] = v.x;
-                sum += v.x + v.y + v.z + v.w;
-            }
-            uint32_t incl = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o)
-                    incl += v;
-            }
-            uint32_t above = incl - sum, digit = 0;
-            const bool mine = above < need && need <= incl;
-            if (mine) {
-                bool found = false;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    found = found || need <= above + n[j];
-                    if (!found) {
-                        above += n[j];
-                        digit = j + 1;
-                    }
-                }
-                digit = kBins - 1 - (lane * 8 + digit);
-            }
-            const int owner = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-            prefix |= __shfl_sync(0xffffffffu, digit, owner) << shift;
-            need -= __shfl_sync(0xffffffffu, above, owner);
-        }
-        const uint32_t T = prefix;  // `need` >= 1 of the keys equal to T stay, the first ones
+        // ---- 1. the A-th largest key, T: `need` >= 1 of the keys equal to it stay, the first ones ----
+        uint32_t need = (uint32_t)A;
+        const uint32_t T = LOCAL ? select_local(sh, s_keys, count, need) : select_shared<CS>(sh, key_at, count, need);
 
         // ---- 2. ranks, and the lists ----
         const int segment = ((count + kEvictWarps - 1) / kEvictWarps + 31) & ~31;  // per warp
         const int s0 = min(warp * segment, count), s1 = min(s0 + segment, count);
         uint32_t gt = 0, eq = 0;
-        for (int i0 = s0; i0 < s1; i0 += 32) {
-            const int i = i0 + lane;
-            const uint32_t key = i < s1 ? key_at(i) : 0u;
-            gt += __popc(__ballot_sync(0xffffffffu, i < s1 && key > T));
-            eq += __popc(__ballot_sync(0xffffffffu, i < s1 && key == T));
+#pragma unroll 4
+        for (int i = s0 + lane; i < s1; i += 32) {
+            const uint32_t key = key_at(i);
+            gt += key > T;
+            eq += key == T;
         }
+        gt = __reduce_add_sync(0xffffffffu, gt);
+        eq = __reduce_add_sync(0xffffffffu, eq);
         if (lane == 0) {
             sh.gt[warp] = gt;
             sh.eq[warp] = eq;
@@ -274,28 +340,16 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
         __syncthreads();
         {
             // counts of the warps before this one
-            uint32_t g = lane < kEvictWarps ? sh.gt[lane] : 0u, e = lane < kEvictWarps ? sh.eq[lane] : 0u;
+            const uint32_t g = lane < kEvictWarps ? sh.gt[lane] : 0u, e = lane < kEvictWarps ? sh.eq[lane] : 0u;
             if (!LOCAL && warp == 0) {
-                uint32_t all_g = g, all_e = e;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    all_g += __shfl_xor_sync(0xffffffffu, all_g, o);
-                    all_e += __shfl_xor_sync(0xffffffffu, all_e, o);
-                }
+                const uint32_t all_g = __reduce_add_sync(0xffffffffu, g), all_e = __reduce_add_sync(0xffffffffu, e);
                 if (lane == 0) {
                     sh.block_gt = all_g;
                     sh.block_eq = all_e;
                 }
             }
-            g = lane < warp ? g : 0u;
-            e = lane < warp ? e : 0u;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                g += __shfl_xor_sync(0xffffffffu, g, o);
-                e += __shfl_xor_sync(0xffffffffu, e, o);
-            }
-            gt = g;
-            eq = e;
+            gt = __reduce_add_sync(0xffffffffu, lane < warp ? g : 0u);
+            eq = __reduce_add_sync(0xffffffffu, lane < warp ? e : 0u);
         }
         if (!LOCAL) {
             evict_sync<CS>();
@@ -332,7 +386,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
                 }
                 if (slot == A) {
                     // kept_before tokens keep their slots below A: the other slots there are holes
-                    if (LOCAL || CS == 1)
+                    if (CS == 1)
                         sh.moves = (uint32_t)(A - kept_before);
                     else
                         for (int c = 0; c < CS; ++c)
@@ -345,25 +399,31 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
             gt += __popc(bg);
             eq += __popc(be);
         }
-        if (LOCAL)
-            __syncthreads();
-        else
-            evict_sync<CS>();
-        moves = (int)sh.moves;
-    } else {
-        __syncthreads();  // the table
     }
+    __syncthreads();  // the table, for blocks that select nothing
 
     // ---- 3. and 4. the copies ----
-    // A token's units lie side by side over the threads; as many tokens at once as fit.
-    const int abreast = max(1, kEvictThreads / p.units);
-    const int first_token = p.units <= kEvictThreads ? tid / p.units : 0;
-    const int first_unit = p.units <= kEvictThreads ? tid - first_token * p.units : tid;
-    const int stride = abreast * CS;                          // tokens per step of the cluster
-    const int first = first_token < abreast ? rank * abreast + first_token : INT_MAX / 2;
-    auto address = [&](int u) {
+    // A token's units of one width lie side by side over the threads; as many tokens at once as fit.
+    struct Lanes {
+        int unit, first, stride;  // this thread's unit (of those of its width), its first token, tokens per step
+    };
+    auto lanes = [&](int units) {
+        Lanes l{tid, rank, CS};
+        if (units == 0) {
+            l.first = l.stride = INT_MAX / 2;
+        } else if (units <= kEvictThreads) {
+            const int abreast = kEvictThreads / units, mine = tid / units;
+            l.unit = tid - mine * units;
+            l.first = mine < abreast ? rank * abreast + mine : INT_MAX / 2;
+            l.stride = abreast * CS;
+        }
+        return l;
+    };
+    const int narrow_units = p.units - p.wide;
+    const Lanes wide = lanes(p.wide), narrow = lanes(narrow_units);
+    auto address = [&](int u, int end) {
         UnitAddress t{nullptr, 0, 0, 0, 0};
-        if (u >= p.units)
+        if (u >= end)
             return t;
         int which = 0;
         while (which + 1 < p.n_planes && u >= p.plane[which + 1].first)
@@ -378,93 +438,143 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_co
         t.slot = pl.s2;
         return t;
     };
-    // The unit of the token in `slot`; NULL where its page id is out of range.
-    auto at = [&](const UnitAddress &t, int slot) -> uint8_t * {
+    // The unit of the token in `slot`; ok becomes false where its page id is out of range.
+    auto at = [&](const UnitAddress &t, int slot, bool &ok) -> uint8_t * {
         if (t.dense)
             return t.base + slot * t.slot;
         const int index = slot / kPage;
         const int page = index < p.held_table ? s_table[index] : __ldg(table + index);
-        if (page < 0 || page >= p.num_pool_pages) {
+        const bool good = page >= 0 && page < p.num_pool_pages;
+        ok = ok && good;
+        return t.base + (good ? page : 0) * t.page + (slot % kPage) * t.slot;
+    };
+    auto report = [&](bool ok) {
+        if (!ok)
             atomicOr(p.ws_error, kErrPageId);
-            return nullptr;
-        }
-        return t.base + page * t.page + (slot % kPage) * t.slot;
+        return ok;
     };
-    auto load = [&](Unit &v, const uint8_t *src, int size) {
+    auto load_small = [&](const uint8_t *src, int size) -> uint2 {
         switch (size) {
-        case 16: v.v16 = *reinterpret_cast<const uint4 *>(src); break;
-        case 8: v.v8 = *reinterpret_cast<const uint2 *>(src); break;
-        case 4: v.v4 = *reinterpret_cast<const uint32_t *>(src); break;
-        case 2: v.v2 = *reinterpret_cast<const uint16_t *>(src); break;
-        default: v.v1 = *src; break;
+        case 8: return *reinterpret_cast<const uint2 *>(src);
+        case 4: return make_uint2(*reinterpret_cast<const uint32_t *>(src), 0);
+        case 2: return make_uint2(*reinterpret_cast<const uint16_t *>(src), 0);
+        default: return make_uint2(*src, 0);
         }
     };
-    auto store = [&](uint8_t *dst, const Unit &v, int size) {
+    auto store_small = [&](uint8_t *dst, uint2 v, int size) {
         switch (size) {
-        case 16: *reinterpret_cast<uint4 *>(dst) = v.v16; break;
-        case 8: *reinterpret_cast<uint2 *>(dst) = v.v8; break;
-        case 4: *reinterpret_cast<uint32_t *>(dst) = v.v4; break;
-        case 2: *reinterpret_cast<uint16_t *>(dst) = v.v2; break;
-        default: *dst = v.v1; break;
+        case 8: *reinterpret_cast<uint2 *>(dst) = v; break;
+        case 4: *reinterpret_cast<uint32_t *>(dst) = v.x; break;
+        case 2: *reinterpret_cast<uint16_t *>(dst) = (uint16_t)v.x; break;
+        default: *dst = (uint8_t)v.x; break;
         }
     };
-    for (int u = first_unit; u < p.units; u += kEvictThreads) {  // one round unless a token has more units than threads
-        const UnitAddress t = address(u);
-        for (int j0 = first; j0 < moves; j0 += kBatch * stride) {
-            Unit val[kBatch];
-            uint8_t *dst[kBatch];
+    // The recent tokens go in batches: all of a batch is loaded before any of it
+    // is stored, everywhere in the cluster, and a batch's targets never hold a
+    // later batch's sources.  The first is loaded here, beside the selection (no move touches
+    // its sources), and stored once the movers, whose slots it takes, are read.
+    uint4 rw[kWide];
+    uint8_t *rw_dst[kWide];
+    uint2 rn[kNarrow];
+    uint8_t *rn_dst[kNarrow];
+    int rn_size = 0;
+    auto load_recent = [&](int round, int batch) {
+        const UnitAddress tw = address(wide.unit + round * kEvictThreads, p.wide);
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int j = j0 + k * stride;
-                dst[k] = nullptr;
-                if (j < moves) {
-                    const uint8_t *src = at(t, LOCAL ? s_movers[moves - 1 - j] : __ldcg(movers + moves - 1 - j));
-                    dst[k] = at(t, LOCAL ? s_holes[j] : __ldcg(holes + j));
-                    if (!src)
-                        dst[k] = nullptr;
-                    if (dst[k])
-                        load(val[k], src, t.size);
-                }
+        for (int k = 0; k < kWide; ++k) {
+            const int64_t j = (int64_t)(batch * kWide + k) * wide.stride + wide.first;
+            rw_dst[k] = nullptr;
+            if (tw.base && j < p.recent) {
+                bool ok = true;
+                const uint8_t *src = at(tw, M + (int)j, ok);
+                uint8_t *dst = at(tw, A + (int)j, ok);
+                rw[k] = *reinterpret_cast<const uint4 *>(src);
+                rw_dst[k] = report(ok) ? dst : nullptr;
             }
+        }
+        const UnitAddress tn = address(p.wide + narrow.unit + round * kEvictThreads, p.units);
+        rn_size = tn.size;
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (dst[k])
-                    store(dst[k], val[k], t.size);
+        for (int k = 0; k < kNarrow; ++k) {
+            const int64_t j = (int64_t)(batch * kNarrow + k) * narrow.stride + narrow.first;
+            rn_dst[k] = nullptr;
+            if (tn.base && j < p.recent) {
+                bool ok = true;
+                const uint8_t *src = at(tn, M + (int)j, ok);
+                uint8_t *dst = at(tn, A + (int)j, ok);
+                rn[k] = load_small(src, tn.size);
+                rn_dst[k] = report(ok) ? dst : nullptr;
+            }
+        }
+    };
+    load_recent(0, 0);
+    evict_sync<CS>();  // the lists are there
+    int moves = 0;
+    uint32_t hole_at = smem_addr(s_holes), mover_at = smem_addr(s_movers);  // of the block that selected
+    if (A > 0) {
+        moves = (int)sh.moves;
+        if (LOCAL && CS > 1) {
+            hole_at = map_shared_rank(hole_at, 0);
+            mover_at = map_shared_rank(mover_at, 0);
         }
     }
-    // The recent tokens, in batches: all of a batch is loaded before any of it is stored, everywhere in
-    // the cluster; their targets hold movers, which the first barrier has read.  A batch's targets never
-    // hold a later batch's sources.
-    const int rounds = (p.units + kEvictThreads - 1) / kEvictThreads;
-    bool first_batch = true;
+    auto mover = [&](int j) { return LOCAL ? ld_cluster_u16(mover_at + 2 * (moves - 1 - j)) : __ldcg(movers + moves - 1 - j); };
+    auto hole = [&](int j) { return LOCAL ? ld_cluster_u16(hole_at + 2 * j) : __ldcg(holes + j); };
+    for (int u = wide.unit; u < p.wide; u += kEvictThreads) {  // once unless a token has more units than the block threads
+        const UnitAddress t = address(u, p.wide);
+        for (int j0 = wide.first; j0 < moves; j0 += 4 * wide.stride) {
+            int from[4], to[4];
+            uint4 val[4];
+            uint8_t *dst[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = min(j0 + k * wide.stride, moves - 1);
+                from[k] = mover(j);
+                to[k] = hole(j);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                bool ok = true;
+                const uint8_t *src = at(t, from[k], ok);
+                dst[k] = at(t, to[k], ok);
+                val[k] = *reinterpret_cast<const uint4 *>(src);
+                if (!report(ok) || j0 + k * wide.stride >= moves)
+                    dst[k] = nullptr;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (dst[k])
+                    *reinterpret_cast<uint4 *>(dst[k]) = val[k];
+        }
+    }
+    for (int u = narrow.unit; u < narrow_units; u += kEvictThreads) {
+        const UnitAddress t = address(p.wide + u, p.units);
+        for (int j = narrow.first; j < moves; j += narrow.stride) {
+            bool ok = true;
+            const uint8_t *src = at(t, mover(j), ok);
+            uint8_t *dst = at(t, hole(j), ok);
+            const uint2 v = load_small(src, t.size);
+            if (report(ok))
+                store_small(dst, v, t.size);
+        }
+    }
+    const int rounds = (max(p.wide, narrow_units) + kEvictThreads - 1) / kEvictThreads;
     for (int r = 0; r < rounds; ++r) {
-        const UnitAddress t = address(first_unit + r * kEvictThreads);
-        for (int b0 = 0; b0 < p.recent; b0 += kBatch * stride) {
-            Unit val[kBatch];
-            uint8_t *dst[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int j = b0 + first + k * stride;
-                dst[k] = nullptr;
-                if (t.base && j < p.recent) {
-                    const uint8_t *src = at(t, M + j);
-                    dst[k] = at(t, A + j);
-                    if (!src)
-                        dst[k] = nullptr;
-                    if (dst[k])
-                        load(val[k], src, t.size);
-                }
-            }
+        for (int b = 0; b == 0 || (int64_t)b * kWide * wide.stride < p.recent || (int64_t)b * kNarrow * narrow.stride < p.recent;
+             ++b) {
+            if (r > 0 || b > 0)
+                load_recent(r, b);
             evict_sync<CS>();
-            first_batch = false;
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (dst[k])
-                    store(dst[k], val[k], t.size);
+            for (int k = 0; k < kWide; ++k)
+                if (rw_dst[k])
+                    *reinterpret_cast<uint4 *>(rw_dst[k]) = rw[k];
+#pragma unroll
+            for (int k = 0; k < kNarrow; ++k)
+                if (rn_dst[k])
+                    store_small(rn_dst[k], rn[k], rn_size);
         }
     }
-    if (first_batch)
-        evict_sync<CS>();
     // vacated slots start from zero when new tokens take them (all loads lie before a barrier above)
     for (int i = p.budget + rank * kEvictThreads + tid; i < N; i += CS * kEvictThreads)
         scores[i] = 0.f;
@@ -569,7 +679,15 @@ int pkv_evict_tokens(float *scores, int64_t score_stride_row, int64_t score_stri
             return PKV_ERR_INVALID;
         if (pl.row_bytes > PKV_EVICT_MAX_ROW_BYTES)
             return PKV_ERR_UNSUPPORTED;
-        add(pl.base, pl.stride_page, pl.stride_head, pl.stride_token, unit_bytes(pl), pl.row_bytes, 0);
+    }
+    for (int wide = 1; wide >= 0; --wide) {  // planes of 16-byte units first
+        for (int i = 0; i < n_planes; ++i) {
+            const pkv_plane &pl = planes[i];
+            if ((unit_bytes(pl) == 16) == (wide == 1))
+                add(pl.base, pl.stride_page, pl.stride_head, pl.stride_token, unit_bytes(pl), pl.row_bytes, 0);
+        }
+        if (wide)
+            p.wide = p.units;
     }
     add(scores, score_stride_row * 4, score_stride_head * 4, 4, 4, 4, 1);
     if (positions)
@@ -590,7 +708,7 @@ int pkv_evict_tokens(float *scores, int64_t score_stride_row, int64_t score_stri
     p.capacity = capacity;
 
     int cluster = 1;
-    while (cluster < kMaxCluster && pairs * cluster * 2 <= 296 && capacity / (cluster * 2) >= 256)
+    while (cluster < kMaxCluster && pairs * cluster * 2 <= 148 * kEvictPerSM && capacity / (cluster * 2) >= 256)
         cluster *= 2;
     const bool local = capacity <= kLocalKeys;
     p.held_keys = (int32_t)(local ? capacity : std::min<int64_t>(ceil_div(capacity, cluster), kMaxKeys));
