@@ -48,14 +48,14 @@ namespace {
 constexpr int kEvictThreads = 256;
 constexpr int kEvictPerSM = 2;       // blocks an SM holds
 constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kLocalKeys = 8192;    // capacity up to which one block selects for its cluster
+constexpr int kLocalKeys = 16384;   // capacity up to which one block selects for its cluster
 constexpr int kMaxKeys = 16384;     // shared selection: keys a block holds (the rest is read again)
 constexpr int kMaxTable = 2048;     // block-table entries a block holds
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 256;          // shared selection: 8-bit digits
-constexpr int kLocalBins = 2048;    // one block's: 11-bit digits
+constexpr int kBins = 2048;
 constexpr int kMaxPlanes = PKV_EVICT_MAX_PLANES;
-constexpr int kWide = 8;            // 16-byte units a thread has in flight
+constexpr int kWide = 4;            // 16-byte units of recent tokens a thread has in flight
+constexpr int kDeep = 8;            // ... and of moves
 constexpr int kNarrow = 2;          // smaller ones
 
 // One array that moves with the tokens.  Paged: row bytes at
@@ -101,6 +101,11 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 __device__ __forceinline__ int ld_cluster_u16(uint32_t addr)
 {
     uint16_t v;
@@ -109,14 +114,9 @@ __device__ __forceinline__ int ld_cluster_u16(uint32_t addr)
 }
 
 struct __align__(16) EvictShared {
-    union {
-        uint32_t local[kLocalBins];
-        struct {
-            uint32_t hist[3][kBins];
-            uint32_t total[kBins];  // the cluster's counts of this digit
-        };
-    };
-    uint32_t warp_sum[kEvictWarps];
+    uint32_t hist[2][kBins];
+    uint32_t total[kBins / 2];  // shared selection: the cluster's counts of this block's slice of the values
+    uint32_t warp_sum[kEvictWarps], scan[kEvictWarps], slice_sum[kMaxCluster];
     uint32_t digit, above;
     uint32_t gt[kEvictWarps], eq[kEvictWarps];
     uint32_t block_gt, block_eq;  // read by the peers
@@ -144,119 +144,149 @@ __device__ __forceinline__ uint32_t inclusive_scan(uint32_t v, int lane)
     return v;
 }
 
-// visit(i, key_at(i)) for this thread's share of [0, count), four keys loaded at a time.
+// Adds the block's keys to hist by digit_of(key) (kBins: not counted), four
+// keys loaded at a time.  One value may dominate (tokens that no query has met yet all score
+// zero), and additions to one address run one by one: the lanes of a warp
+// that agree with its first make one addition.
 template <typename K, typename V>
-__device__ __forceinline__ void for_keys(int count, int tid, K key_at, V visit)
+__device__ __forceinline__ void count_keys(uint32_t *hist, int count, int tid, K key_at, V digit_of)
 {
+    const int lane = tid & 31;
     for (int i0 = 0; i0 < count; i0 += 4 * kEvictThreads) {
-        uint32_t key[4];
+        uint32_t digit[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int i = i0 + k * kEvictThreads + tid;
-            key[k] = i < count ? key_at(i) : 0u;
+            digit[k] = i < count ? digit_of(key_at(i)) : (uint32_t)kBins;
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (i0 + k * kEvictThreads + tid < count)
-                visit(key[k]);
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t first = __shfl_sync(0xffffffffu, digit[k], 0);
+            const uint32_t same = __ballot_sync(0xffffffffu, digit[k] == first);
+            if (digit[k] < kBins && (lane == 0 || digit[k] != first))
+                atomicAdd(hist + digit[k], lane == 0 ? __popc(same) : 1u);
+        }
     }
 }
 
-// The need-th largest of `count` keys (1 <= need <= count) in shared memory, by
-// one block: three digits of 11, 11 and 10 bits.  `need` becomes its rank
-// among the keys equal to it.  sh.local is zero before and after.
-__device__ __forceinline__ uint32_t select_local(EvictShared &sh, const uint32_t *keys, int count, uint32_t &need)
+// n: this thread's counts of the digit values from top_value down, threads in
+// order from the top, `above` keys above all of them: found(digit, keys above
+// it) in the thread that holds the digit of the need-th key.
+template <int N, typename F>
+__device__ __forceinline__ void find_digit(EvictShared &sh, const uint32_t (&n)[N], int top_value, uint32_t above, uint32_t need,
+                                           F found)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t sum = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        sum += n[j];
+    const uint32_t incl = inclusive_scan(sum, lane);
+    if (lane == 31)
+        sh.scan[warp] = incl;
+    __syncthreads();
+    above += incl - sum;
+#pragma unroll
+    for (int w = 0; w < kEvictWarps; ++w)
+        above += w < warp ? sh.scan[w] : 0u;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        if (above < need && need <= above + n[j])
+            found((uint32_t)(top_value - j), above);
+        above += n[j];
+    }
+}
+
+// The need-th largest (1 <= need <= all) of the keys of CS blocks (`key_at`
+// gives this block's `count`), in three digits of 11, 11 and 10 bits: with
+// that many values the first digit splits scores of like size well enough that
+// the counting is not serialised on a few addresses.  The blocks' counts are
+// added through distributed shared memory.  `need` becomes T's rank among the keys
+// equal to it.  sh.hist is zero before.
+template <int CS, typename K>
+__device__ __forceinline__ uint32_t select_key(EvictShared &sh, K key_at, int count, uint32_t &need)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kPer = kLocalBins / kEvictThreads;  // bins per thread, from the top
+    constexpr int kPer = kBins / kEvictThreads;  // bins per thread, from the top
     static_assert(kPer == 8, "two 16-byte reads");
     uint32_t prefix = 0;
 #pragma unroll
     for (int d = 0; d < 3; ++d) {
         const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
         const uint32_t mask = d == 2 ? 1023u : 2047u;
-        for_keys(count, tid, [&](int i) { return keys[i]; }, [&](uint32_t key) {
-            if (d == 0 || (key >> (d == 1 ? 21 : 10)) == (prefix >> (d == 1 ? 21 : 10)))
-                atomicAdd(sh.local + ((key >> shift) & mask), 1u);
+        uint32_t *hist = sh.hist[d & 1];
+        count_keys(hist, count, tid, key_at, [&](uint32_t key) {
+            const bool in = d == 0 || (key >> (d == 1 ? 21 : 10)) == (prefix >> (d == 1 ? 21 : 10));
+            return in ? (key >> shift) & mask : (uint32_t)kBins;
         });
-        __syncthreads();
-        uint4 *mine = reinterpret_cast<uint4 *>(sh.local + kLocalBins - kPer - tid * kPer);
-        const uint4 hi = mine[1], lo = mine[0];
-        mine[0] = mine[1] = make_uint4(0, 0, 0, 0);
-        const uint32_t n[kPer] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};  // descending
-        const uint32_t sum = n[0] + n[1] + n[2] + n[3] + n[4] + n[5] + n[6] + n[7];
-        const uint32_t incl = inclusive_scan(sum, lane);
-        if (lane == 31)
-            sh.warp_sum[warp] = incl;
-        __syncthreads();
-        uint32_t above = incl - sum;
+        evict_sync<CS>();
+        if (CS == 1) {
+            const int at = kBins - kPer - tid * kPer;
+            const uint4 hi = *reinterpret_cast<const uint4 *>(hist + at + 4);
+            const uint4 lo = *reinterpret_cast<const uint4 *>(hist + at);
+            const uint32_t n[kPer] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};  // descending
+            find_digit(sh, n, kBins - 1 - tid * kPer, 0u, need, [&](uint32_t digit, uint32_t above) {
+                sh.digit = digit;
+                sh.above = above;
+            });
+        } else {
+            // Block c adds up the cluster's counts of its slice of the values, slices from the top; the
+            // slices' sums tell every block where T's digit lies, and that slice's block finds it.
+            constexpr int kSlice = kBins / CS, kMine = kSlice / kEvictThreads;  // per thread: 1, 2 or 4
+            const int rank = (int)cluster_ctarank();
+            const uint32_t *slice = hist + kBins - (rank + 1) * kSlice;
+            uint32_t sum = 0;
 #pragma unroll
-        for (int w = 0; w < kEvictWarps; ++w)
-            above += w < warp ? sh.warp_sum[w] : 0u;
-        if (above < need && need <= above + sum) {
+            for (int h = 0; h < kMine; ++h) {
+                const uint32_t mine = smem_addr(slice + tid + h * kEvictThreads);
+                uint32_t v[CS], all = 0;
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                if (above < need && need <= above + n[j]) {
-                    sh.digit = (uint32_t)(kLocalBins - 1 - tid * kPer - j);
-                    sh.above = above;
-                }
-                above += n[j];
+                for (int c = 0; c < CS; ++c)
+                    v[c] = ld_cluster_u32(map_shared_rank(mine, (uint32_t)c));
+#pragma unroll
+                for (int c = 0; c < CS; ++c)
+                    all += v[c];
+                sh.total[tid + h * kEvictThreads] = all;
+                sum += all;
             }
+            sum = __reduce_add_sync(0xffffffffu, sum);
+            if (lane == 0)
+                sh.warp_sum[warp] = sum;
+            __syncthreads();
+            if (tid < CS) {
+                uint32_t all = 0;
+#pragma unroll
+                for (int w = 0; w < kEvictWarps; ++w)
+                    all += sh.warp_sum[w];
+                st_cluster_u32(map_shared_rank(smem_addr(sh.slice_sum + rank), (uint32_t)tid), all);
+            }
+            evict_sync<CS>();
+            uint32_t above = 0, mine = 0;
+#pragma unroll
+            for (int c = 0; c < CS; ++c) {
+                above += c < rank ? sh.slice_sum[c] : 0u;
+                mine = c == rank ? sh.slice_sum[c] : mine;
+            }
+            if (above < need && need <= above + mine) {  // the same for the whole block
+                uint32_t n[kMine];
+#pragma unroll
+                for (int j = 0; j < kMine; ++j)
+                    n[j] = sh.total[kSlice - 1 - tid * kMine - j];
+                find_digit(sh, n, kBins - rank * kSlice - 1 - tid * kMine, above, need, [&](uint32_t digit, uint32_t rest) {
+                    for (int c = 0; c < CS; ++c) {
+                        st_cluster_u32(map_shared_rank(smem_addr(&sh.digit), (uint32_t)c), digit);
+                        st_cluster_u32(map_shared_rank(smem_addr(&sh.above), (uint32_t)c), rest);
+                    }
+                });
+            }
+            evict_sync<CS>();
         }
+        if (d == 1)  // the third digit counts where the first did: every block is past its reading of those
+            for (int i = tid; i < kBins; i += kEvictThreads)
+                sh.hist[0][i] = 0;
         __syncthreads();
         prefix |= sh.digit << shift;
         need -= sh.above;
-    }
-    return prefix;
-}
-
-// The same over the keys of all CS blocks (`key_at` gives this block's), in
-// four digits of 8 bits: the blocks' counts are added through distributed
-// shared memory.  sh.hist is zero before.
-template <int CS, typename K>
-__device__ __forceinline__ uint32_t select_shared(EvictShared &sh, K key_at, int count, uint32_t &need)
-{
-    const int tid = threadIdx.x, lane = tid & 31;
-    uint32_t prefix = 0;
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        const int shift = 24 - 8 * d;
-        uint32_t *hist = sh.hist[d % 3];  // in turn, so that one barrier per digit is enough
-        if (d == 2)  // every warp, and every peer, is past its reading of the first counts
-            for (int i = tid; i < kBins; i += kEvictThreads)
-                sh.hist[0][i] = 0;
-        for_keys(count, tid, key_at, [&](uint32_t key) {
-            if (d == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8)))
-                atomicAdd(hist + ((key >> shift) & (kBins - 1)), 1u);
-        });
-        evict_sync<CS>();
-        if (tid < kBins) {
-            uint32_t sum = 0;
-            const uint32_t at = smem_addr(hist + tid);
-#pragma unroll
-            for (int c = 0; c < CS; ++c)
-                sum += CS == 1 ? hist[tid] : ld_cluster_u32(map_shared_rank(at, (uint32_t)c));
-            sh.total[tid] = sum;
-        }
-        __syncthreads();
-        // lane l of every warp holds bins 255 - 8 l down to 248 - 8 l
-        const uint4 *bins = reinterpret_cast<const uint4 *>(sh.total + kBins - 8 - lane * 8);
-        const uint4 hi = bins[1], lo = bins[0];
-        const uint32_t n[8] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
-        const uint32_t sum = n[0] + n[1] + n[2] + n[3] + n[4] + n[5] + n[6] + n[7];
-        uint32_t above = inclusive_scan(sum, lane) - sum, digit = 0, rest = 0;
-        const bool mine = above < need && need <= above + sum;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (above < need && need <= above + n[j]) {
-                digit = (uint32_t)(kBins - 1 - lane * 8 - j);
-                rest = above;
-            }
-            above += n[j];
-        }
-        const int owner = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-        prefix |= __shfl_sync(0xffffffffu, digit, owner) << shift;
-        need -= __shfl_sync(0xffffffffu, rest, owner);
     }
     return prefix;
 }
@@ -282,8 +312,8 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictPerSM) evict_kernel(const
     const int pair = blockIdx.x / CS;
     const int row = pair / p.H_kv, head = pair - row * p.H_kv;
     const int32_t *table = p.block_table + (int64_t)row * p.max_pages;
-    for (int i = tid; i < kLocalBins; i += kEvictThreads)
-        sh.local[i] = 0;
+    for (int i = tid; i < 2 * kBins; i += kEvictThreads)
+        sh.hist[0][i] = 0;
     grid_dependency_wait();
     grid_launch_dependents();
     const int N = __ldg(p.seq_lens + row);
@@ -319,7 +349,7 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictPerSM) evict_kernel(const
 
         // ---- 1. the A-th largest key, T: `need` >= 1 of the keys equal to it stay, the first ones ----
         uint32_t need = (uint32_t)A;
-        const uint32_t T = LOCAL ? select_local(sh, s_keys, count, need) : select_shared<CS>(sh, key_at, count, need);
+        const uint32_t T = select_key<(LOCAL ? 1 : CS)>(sh, key_at, count, need);
 
         // ---- 2. ranks, and the lists ----
         const int segment = ((count + kEvictWarps - 1) / kEvictWarps + 31) & ~31;  // per warp
@@ -390,10 +420,8 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictPerSM) evict_kernel(const
                         sh.moves = (uint32_t)(A - kept_before);
                     else
                         for (int c = 0; c < CS; ++c)
-                            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(
-                                             map_shared_rank(smem_addr(&sh.moves), (uint32_t)c)),
-                                         "r"((uint32_t)(A - kept_before))
-                                         : "memory");
+                            st_cluster_u32(map_shared_rank(smem_addr(&sh.moves), (uint32_t)c),
+                                           (uint32_t)(A - kept_before));
                 }
             }
             gt += __popc(bg);
@@ -522,40 +550,64 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictPerSM) evict_kernel(const
     auto hole = [&](int j) { return LOCAL ? ld_cluster_u16(hole_at + 2 * j) : __ldcg(holes + j); };
     for (int u = wide.unit; u < p.wide; u += kEvictThreads) {  // once unless a token has more units than the block threads
         const UnitAddress t = address(u, p.wide);
-        for (int j0 = wide.first; j0 < moves; j0 += 4 * wide.stride) {
-            int from[4], to[4];
-            uint4 val[4];
-            uint8_t *dst[4];
+        // a step's rows are loaded while the next step's places are looked up
+        int from[kDeep], to[kDeep];
+        auto places = [&](int j0) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kDeep; ++k) {
                 const int j = min(j0 + k * wide.stride, moves - 1);
                 from[k] = mover(j);
                 to[k] = hole(j);
             }
+        };
+        if (wide.first < moves)
+            places(wide.first);
+        for (int j0 = wide.first; j0 < moves; j0 += kDeep * wide.stride) {
+            uint4 val[kDeep];
+            uint8_t *dst[kDeep];
+            bool all = true;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kDeep; ++k) {
                 bool ok = true;
-                const uint8_t *src = at(t, from[k], ok);
+                val[k] = *reinterpret_cast<const uint4 *>(at(t, from[k], ok));
                 dst[k] = at(t, to[k], ok);
-                val[k] = *reinterpret_cast<const uint4 *>(src);
-                if (!report(ok) || j0 + k * wide.stride >= moves)
+                all = all && ok;
+                if (!ok || j0 + k * wide.stride >= moves)
                     dst[k] = nullptr;
             }
+            report(all);
+            if (moves - j0 > kDeep * wide.stride)
+                places(j0 + kDeep * wide.stride);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < kDeep; ++k)
                 if (dst[k])
                     *reinterpret_cast<uint4 *>(dst[k]) = val[k];
         }
     }
     for (int u = narrow.unit; u < narrow_units; u += kEvictThreads) {
         const UnitAddress t = address(p.wide + u, p.units);
-        for (int j = narrow.first; j < moves; j += narrow.stride) {
-            bool ok = true;
-            const uint8_t *src = at(t, mover(j), ok);
-            uint8_t *dst = at(t, hole(j), ok);
-            const uint2 v = load_small(src, t.size);
-            if (report(ok))
-                store_small(dst, v, t.size);
+        for (int j0 = narrow.first; j0 < moves; j0 += 4 * narrow.stride) {
+            int from[4], to[4];
+            uint2 val[4];
+            uint8_t *dst[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = min(j0 + k * narrow.stride, moves - 1);
+                from[k] = mover(j);
+                to[k] = hole(j);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                bool ok = true;
+                val[k] = load_small(at(t, from[k], ok), t.size);
+                dst[k] = at(t, to[k], ok);
+                if (!report(ok) || j0 + k * narrow.stride >= moves)
+                    dst[k] = nullptr;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (dst[k])
+                    store_small(dst[k], val[k], t.size);
         }
     }
     const int rounds = (max(p.wide, narrow_units) + kEvictThreads - 1) / kEvictThreads;
@@ -585,7 +637,7 @@ cudaError_t launch_evict(const EvictParams &p, int64_t pairs, cudaStream_t st)
 {
     static std::atomic<uint64_t> configured{0};
     auto kernel = evict_kernel<CS, LOCAL>;
-    const cudaError_t e = allow_smem(kernel, (kMaxKeys + kMaxTable) * 4, configured);
+    const cudaError_t e = allow_smem(kernel, (kMaxKeys + kMaxTable) * 4 + kLocalKeys * 2, configured);
     if (e != cudaSuccess)
         return e;
     const size_t smem = (size_t)(p.held_keys + p.held_table) * 4 + (LOCAL ? (size_t)p.capacity * 2 : 0);
