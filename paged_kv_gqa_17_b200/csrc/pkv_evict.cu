@@ -337,100 +337,9 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictPerSM) evict_kernel(const
     for (int i = tid; i < min(p.held_table, (N + kPage - 1) / kPage); i += kEvictThreads)
         s_table[i] = __ldg(table + i);
 
-    if (A > 0 && (!LOCAL || rank == 0)) {
-        const int share = LOCAL ? M : (M + CS - 1) / CS;
-        const int lo = LOCAL ? 0 : min(rank * share, M), count = min(lo + share, M) - lo;
-        const int held = LOCAL ? count : min(count, kMaxKeys);
-#pragma unroll 4
-        for (int i = tid; i < held; i += kEvictThreads)
-            s_keys[i] = score_key(scores[lo + i]);
-        auto key_at = [&](int i) { return LOCAL || i < held ? s_keys[i] : score_key(scores[lo + i]); };
-        __syncthreads();
+    __syncthreads();
 
-        // ---- 1. the A-th largest key, T: `need` >= 1 of the keys equal to it stay, the first ones ----
-        uint32_t need = (uint32_t)A;
-        const uint32_t T = select_key<(LOCAL ? 1 : CS)>(sh, key_at, count, need);
-
-        // ---- 2. ranks, and the lists ----
-        const int segment = ((count + kEvictWarps - 1) / kEvictWarps + 31) & ~31;  // per warp
-        const int s0 = min(warp * segment, count), s1 = min(s0 + segment, count);
-        uint32_t gt = 0, eq = 0;
-#pragma unroll 4
-        for (int i = s0 + lane; i < s1; i += 32) {
-            const uint32_t key = key_at(i);
-            gt += key > T;
-            eq += key == T;
-        }
-        gt = __reduce_add_sync(0xffffffffu, gt);
-        eq = __reduce_add_sync(0xffffffffu, eq);
-        if (lane == 0) {
-            sh.gt[warp] = gt;
-            sh.eq[warp] = eq;
-        }
-        __syncthreads();
-        {
-            // counts of the warps before this one
-            const uint32_t g = lane < kEvictWarps ? sh.gt[lane] : 0u, e = lane < kEvictWarps ? sh.eq[lane] : 0u;
-            if (!LOCAL && warp == 0) {
-                const uint32_t all_g = __reduce_add_sync(0xffffffffu, g), all_e = __reduce_add_sync(0xffffffffu, e);
-                if (lane == 0) {
-                    sh.block_gt = all_g;
-                    sh.block_eq = all_e;
-                }
-            }
-            gt = __reduce_add_sync(0xffffffffu, lane < warp ? g : 0u);
-            eq = __reduce_add_sync(0xffffffffu, lane < warp ? e : 0u);
-        }
-        if (!LOCAL) {
-            evict_sync<CS>();
-            const uint32_t ag = smem_addr(&sh.block_gt), ae = smem_addr(&sh.block_eq);
-#pragma unroll
-            for (int c = 0; c < CS; ++c)
-                if (c < rank) {
-                    gt += ld_cluster_u32(map_shared_rank(ag, (uint32_t)c));
-                    eq += ld_cluster_u32(map_shared_rank(ae, (uint32_t)c));
-                }
-        }
-        for (int i0 = s0; i0 < s1; i0 += 32) {
-            const int i = i0 + lane;
-            const uint32_t key = i < s1 ? key_at(i) : 0u;
-            const bool is_gt = i < s1 && key > T, is_eq = i < s1 && key == T;
-            const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
-            const uint32_t below = (1u << lane) - 1u;
-            const uint32_t eq_before = eq + __popc(be & below);
-            const int kept_before = (int)(gt + __popc(bg & below) + min(eq_before, need));
-            if (i < s1) {
-                const int slot = lo + i;
-                const bool keep = is_gt || (is_eq && eq_before < need);
-                if (slot < A && !keep) {
-                    if (LOCAL)
-                        s_holes[slot - kept_before] = (uint16_t)slot;
-                    else
-                        holes[slot - kept_before] = slot;
-                }
-                if (slot >= A && keep) {  // the j-th mover from the end
-                    if (LOCAL)
-                        s_movers[A - 1 - kept_before] = (uint16_t)slot;
-                    else
-                        movers[A - 1 - kept_before] = slot;
-                }
-                if (slot == A) {
-                    // kept_before tokens keep their slots below A: the other slots there are holes
-                    if (CS == 1)
-                        sh.moves = (uint32_t)(A - kept_before);
-                    else
-                        for (int c = 0; c < CS; ++c)
-                            st_cluster_u32(map_shared_rank(smem_addr(&sh.moves), (uint32_t)c),
-                                           (uint32_t)(A - kept_before));
-                }
-            }
-            gt += __popc(bg);
-            eq += __popc(be);
-        }
-    }
-    __syncthreads();  // the table, for blocks that select nothing
-
-    // ---- 3. and 4. the copies ----
+    // ---- the copies' lanes and addresses; the first recent tokens ----
     // A token's units of one width lie side by side over the threads; as many tokens at once as fit.
     struct Lanes {
         int unit, first, stride;  // this thread's unit (of those of its width), its first token, tokens per step
@@ -536,6 +445,100 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictPerSM) evict_kernel(const
         }
     };
     load_recent(0, 0);
+
+    if (A > 0 && (!LOCAL || rank == 0)) {
+        const int share = LOCAL ? M : (M + CS - 1) / CS;
+        const int lo = LOCAL ? 0 : min(rank * share, M), count = min(lo + share, M) - lo;
+        const int held = LOCAL ? count : min(count, kMaxKeys);
+#pragma unroll 4
+        for (int i = tid; i < held; i += kEvictThreads)
+            s_keys[i] = score_key(scores[lo + i]);
+        auto key_at = [&](int i) { return LOCAL || i < held ? s_keys[i] : score_key(scores[lo + i]); };
+        __syncthreads();
+
+        // ---- 1. the A-th largest key, T: `need` >= 1 of the keys equal to it stay, the first ones ----
+        uint32_t need = (uint32_t)A;
+        const uint32_t T = select_key<(LOCAL ? 1 : CS)>(sh, key_at, count, need);
+
+        // ---- 2. ranks, and the lists ----
+        const int segment = ((count + kEvictWarps - 1) / kEvictWarps + 31) & ~31;  // per warp
+        const int s0 = min(warp * segment, count), s1 = min(s0 + segment, count);
+        uint32_t gt = 0, eq = 0;
+#pragma unroll 4
+        for (int i = s0 + lane; i < s1; i += 32) {
+            const uint32_t key = key_at(i);
+            gt += key > T;
+            eq += key == T;
+        }
+        gt = __reduce_add_sync(0xffffffffu, gt);
+        eq = __reduce_add_sync(0xffffffffu, eq);
+        if (lane == 0) {
+            sh.gt[warp] = gt;
+            sh.eq[warp] = eq;
+        }
+        __syncthreads();
+        {
+            // counts of the warps before this one
+            const uint32_t g = lane < kEvictWarps ? sh.gt[lane] : 0u, e = lane < kEvictWarps ? sh.eq[lane] : 0u;
+            if (!LOCAL && warp == 0) {
+                const uint32_t all_g = __reduce_add_sync(0xffffffffu, g), all_e = __reduce_add_sync(0xffffffffu, e);
+                if (lane == 0) {
+                    sh.block_gt = all_g;
+                    sh.block_eq = all_e;
+                }
+            }
+            gt = __reduce_add_sync(0xffffffffu, lane < warp ? g : 0u);
+            eq = __reduce_add_sync(0xffffffffu, lane < warp ? e : 0u);
+        }
+        if (!LOCAL) {
+            evict_sync<CS>();
+            const uint32_t ag = smem_addr(&sh.block_gt), ae = smem_addr(&sh.block_eq);
+#pragma unroll
+            for (int c = 0; c < CS; ++c)
+                if (c < rank) {
+                    gt += ld_cluster_u32(map_shared_rank(ag, (uint32_t)c));
+                    eq += ld_cluster_u32(map_shared_rank(ae, (uint32_t)c));
+                }
+        }
+        for (int i0 = s0; i0 < s1; i0 += 32) {
+            const int i = i0 + lane;
+            const uint32_t key = i < s1 ? key_at(i) : 0u;
+            const bool is_gt = i < s1 && key > T, is_eq = i < s1 && key == T;
+            const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
+            const uint32_t below = (1u << lane) - 1u;
+            const uint32_t eq_before = eq + __popc(be & below);
+            const int kept_before = (int)(gt + __popc(bg & below) + min(eq_before, need));
+            if (i < s1) {
+                const int slot = lo + i;
+                const bool keep = is_gt || (is_eq && eq_before < need);
+                if (slot < A && !keep) {
+                    if (LOCAL)
+                        s_holes[slot - kept_before] = (uint16_t)slot;
+                    else
+                        holes[slot - kept_before] = slot;
+                }
+                if (slot >= A && keep) {  // the j-th mover from the end
+                    if (LOCAL)
+                        s_movers[A - 1 - kept_before] = (uint16_t)slot;
+                    else
+                        movers[A - 1 - kept_before] = slot;
+                }
+                if (slot == A) {
+                    // kept_before tokens keep their slots below A: the other slots there are holes
+                    if (CS == 1)
+                        sh.moves = (uint32_t)(A - kept_before);
+                    else
+                        for (int c = 0; c < CS; ++c)
+                            st_cluster_u32(map_shared_rank(smem_addr(&sh.moves), (uint32_t)c),
+                                           (uint32_t)(A - kept_before));
+                }
+            }
+            gt += __popc(bg);
+            eq += __popc(be);
+        }
+    }
+
+    // ---- 3. the moves ----
     evict_sync<CS>();  // the lists are there
     int moves = 0;
     uint32_t hole_at = smem_addr(s_holes), mover_at = smem_addr(s_movers);  // of the block that selected
@@ -610,6 +613,7 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictPerSM) evict_kernel(const
                     store_small(dst[k], val[k], t.size);
         }
     }
+    // ---- 4. the recent tokens ----
     const int rounds = (max(p.wide, narrow_units) + kEvictThreads - 1) / kEvictThreads;
     for (int r = 0; r < rounds; ++r) {
         for (int b = 0; b == 0 || (int64_t)b * kWide * wide.stride < p.recent || (int64_t)b * kNarrow * narrow.stride < p.recent;
