@@ -390,7 +390,8 @@ struct DCfg {
     static constexpr int kPairOff = kBarOff + kWarps * kStages * 8;  // pair of each of the 2 kWarps states, and
     static constexpr int kScanOff = kPairOff + 4 * kWarps * 4;       // where the n-th of those present lies
     static constexpr int kWeightOff = kScanOff + 64;                // the block's merge: weights, maxima and sums
-    static constexpr int kPrefixOff = kWeightOff + 3 * 16 * 32 * 4;  // int32 [B + 1]
+    static constexpr int kGroupOff = (kWeightOff + 3 * 16 * 32 * 4 + 15) / 16 * 16;  // its pairs
+    static constexpr int kPrefixOff = kGroupOff + 32 * 16;                          // int32 [B + 1]
     static_assert(kWarpRing % 16 == 0 && kBarOff % 8 == 0, "alignment of the copies and their barriers");
     static_assert(kPrefixOff + (kMaxRows + 1) * 4 <= 227 * 1024, "shared memory of a block");
 };
@@ -806,9 +807,8 @@ __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)
 
     // ---- softmax against the reference max ----
     if (st.vlow == ~0u) {
-        // the pair's first pages set the reference, and each block's window of V's scales
-        move_reference(s, nv, lane, st);
-        // from its first token's scales (any token's would do: what lies outside takes the wide path)
+        // the pair's first pages set each block's window of V's scales, from its first token's
+        // (any token's would do: what lies outside takes the wide path)
         uint32_t v[4];
         load_value_scales<D>(rec + (nv[0] > 0 ? 0 : R::kBytes), lane, v);
         const uint32_t first = __shfl_sync(0xffffffffu, v[0], 0);
@@ -817,7 +817,8 @@ __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)
         for (int b = 0; b < kBlocks; ++b)
             st.vlow |= (uint32_t)min(max((int)((first >> (8 * b)) & 255u) - 4, 0), 247) << (8 * b);
     }
-    auto exponents = [&]() {
+#pragma unroll 1
+    for (;;) {  // twice where the reference has to move (from infinity on the pair's first pages), else once
         float top = -INFINITY;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -831,11 +832,9 @@ __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)
                         t[h][nt][i] = -INFINITY;
                     top = fmaxf(top, t[h][nt][i]);
                 }
-        return top;
-    };
-    if (__any_sync(0xffffffffu, exponents() > kPTop)) {
+        if (!__any_sync(0xffffffffu, top > kPTop))
+            break;
         move_reference(s, nv, lane, st);
-        exponents();
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -1174,69 +1173,72 @@ __global__ void __launch_bounds__(DCfg<D, NT>::kThreads, 1) mx4_decode_kernel(co
         const uint32_t later = starts & ~((2u << first) - 1u);
         return __popc(later ? there & ((later & (0u - later)) - 1u) : there);
     };
-    for (int g = warp; g < G; g += kWarps) {
+    const int groups = __popc(starts), group = __popc(starts & below);  // pairs among the states; this lane's, at its start
+    // Per pair: {pair, its first state's number, one past its last, state slot}
+    int4 *group_at = reinterpret_cast<int4 *>(smem + C::kGroupOff);
+    if (warp == 0 && (starts >> lane) & 1u) {
+        const int row = my_pair / p.H_kv;
+        const uint32_t pages = prefix[row + 1] - prefix[row];
+        const uint32_t P0 = (uint32_t)prefix[row] * p.H_kv + (uint32_t)(my_pair - row * p.H_kv) * pages;
+        const bool whole = P0 >= u0 && P0 + pages <= u1;
+        const int slot = whole ? 2 * p.blocks + my_pair : 2 * (int)blockIdx.x + (P0 > u0 ? 1 : 0);
+        group_at[group] = make_int4(my_pair, nth, end_of(lane), slot);
+        if (P0 >= u0 && P0 + pages > u1) {
+            // the pair begins here and reaches beyond this block
+            const SlotRange span{slot, (int)(blocks.owner(P0 + pages - 1) - blockIdx.x) + 1, 2 * (int)blockIdx.x, 2};
+            p.spans[blockIdx.x] = span;
+            p.span_pair[blockIdx.x] = my_pair;
+            if (SCORED)
+                p.ranges[my_pair] = span;
+        }
+        if (SCORED && whole)
+            p.ranges[my_pair] = SlotRange{slot, 1, 0, 0};
+    }
+    if (warp == kWarps - 1 && my_pair >= 0)
+        state_pair[2 * kWarps + nth] = (int)(state_at(lane) - reinterpret_cast<float *>(smem));  // where the n-th lies
+    // weights: a warp per (head, pair)
+    for (int w = warp; w < G * groups; w += kWarps) {
+        const int g = w % G, which = w / G;
+        const int first = __ffs(__ballot_sync(0xffffffffu, ((starts >> lane) & 1u) != 0 && group == which)) - 1;
+        const bool mine = my_pair >= 0 && lane >= first && nth < end_of(first);
         const float *sk = state_at(lane) + C::kHeads * (D + 4) + g;
-        const float m = my_pair >= 0 ? sk[0] : -INFINITY, l = my_pair >= 0 ? sk[C::kHeads] : 0.f;
-        for (uint32_t left = starts; left; left &= left - 1u) {
-            const int first = __ffs(left) - 1;
-            const bool mine = my_pair >= 0 && lane >= first && nth < end_of(first);
-            float M = mine ? m : -INFINITY;
+        const float m = mine ? sk[0] : -INFINITY, l = mine ? sk[C::kHeads] : 0.f;
+        float M = m;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            const float w = exp2_approx(m - (M == -INFINITY ? 0.f : M));
-            float L = mine ? l * w : 0.f;
+        for (int o = 16; o > 0; o >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float wt = exp2_approx(m - (M == -INFINITY ? 0.f : M));
+        float L = mine ? l * wt : 0.f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                L += __shfl_xor_sync(0xffffffffu, L, o);
-            if (mine)
-                weight[g * 32 + nth] = w;
-            if (lane == first) {
-                pair_m[g * 32 + nth] = M;
-                pair_l[g * 32 + nth] = L;
-            }
+        for (int o = 16; o > 0; o >>= 1)
+            L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (mine)
+            weight[g * 32 + nth] = wt;
+        if (lane == first) {
+            pair_m[g * 32 + nth] = M;
+            pair_l[g * 32 + nth] = L;
         }
     }
-    if (warp == 0 && my_pair >= 0)
-        state_pair[2 * kWarps + nth] = (int)(state_at(lane) - reinterpret_cast<float *>(smem));  // where the n-th lies
     __syncthreads();
-    for (uint32_t left = starts; left; left &= left - 1u) {
-        const int first = __ffs(left) - 1;
-        const int n0 = __popc(there & ((1u << first) - 1u)), n1 = end_of(first);
-        const int which = state_pair[first];
-        const int row = which / p.H_kv;
-        const uint32_t pages = prefix[row + 1] - prefix[row];
-        const uint32_t P0 = (uint32_t)prefix[row] * p.H_kv + (uint32_t)(which - row * p.H_kv) * pages;
-        const bool whole = P0 >= u0 && P0 + pages <= u1;
-        const int slot = whole ? 2 * p.blocks + which : 2 * (int)blockIdx.x + (P0 > u0 ? 1 : 0);
-        if (tid == 0 && P0 >= u0 && P0 + pages > u1) {
-            // the pair begins here and reaches beyond this block
-            const int count = (int)(blocks.owner(P0 + pages - 1) - blockIdx.x) + 1;
-            const SlotRange span{slot, count, 2 * (int)blockIdx.x, 2};
-            p.spans[blockIdx.x] = span;
-            p.span_pair[blockIdx.x] = which;
-            if (SCORED)
-                p.ranges[which] = span;
-        }
-        if (SCORED && tid == 0 && whole)
-            p.ranges[which] = SlotRange{slot, 1, 0, 0};
-        for (int e = tid; e < G * D4; e += kThreads) {
-            const int g = e / D4, d4 = (e % D4) * 4;
-            const float *col = reinterpret_cast<float *>(smem) + g * (D + 4) + d4;
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int e = tid; e < groups * G * D4; e += kThreads) {
+        const int column = e / D4, d4 = (e % D4) * 4;
+        const int which = column / G, g = column - which * G;
+        const int4 at = group_at[which];
+        const float *col = reinterpret_cast<float *>(smem) + g * (D + 4) + d4;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-            for (int k = n0; k < n1; ++k)
-                O = fma4(*reinterpret_cast<const float4 *>(col + state_pair[2 * kWarps + k]), weight[g * 32 + k], O);
-            const float L = pair_l[g * 32 + n0];
-            const int64_t at = (int64_t)slot * G + g;
-            if (whole)
-                store_bf16x4(p.out + ((int64_t)which * G + g) * D + d4, scale4(O, L == 0.f ? 0.f : 1.f / L));
-            else
-                *reinterpret_cast<float4 *>(p.ws_acc + at * D + d4) = O;
-            if (d4 == 0 && (SCORED || !whole)) {
-                p.ws_m[at] = pair_m[g * 32 + n0];
-                p.ws_l[at] = L;
-            }
+        for (int k = at.y; k < at.z; ++k)
+            O = fma4(*reinterpret_cast<const float4 *>(col + state_pair[2 * kWarps + k]), weight[g * 32 + k], O);
+        const float L = pair_l[g * 32 + at.y];
+        const bool whole = at.w >= 2 * p.blocks;
+        const int64_t to = (int64_t)at.w * G + g;
+        if (whole)
+            store_bf16x4(p.out + ((int64_t)at.x * G + g) * D + d4, scale4(O, L == 0.f ? 0.f : 1.f / L));
+        else
+            *reinterpret_cast<float4 *>(p.ws_acc + to * D + d4) = O;
+        if (d4 == 0 && (SCORED || !whole)) {
+            p.ws_m[to] = pair_m[g * 32 + at.y];
+            p.ws_l[to] = L;
         }
     }
 }
