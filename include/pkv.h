@@ -489,8 +489,9 @@ PKV_API int pkv_evict_tokens(float *scores, int64_t score_stride_row, int64_t sc
  * clamped to >= 1; 0 for a block of zeros; 255 where a value is infinite or
  * NaN), codes are rounded to nearest even and saturate at 6.
  * A position past the row's pages, or a page id out of range, is reported in
- * the workspace's error word and its token skipped.  `workspace` is a decode
- * plan's workspace, or any 256 zeroed bytes. */
+ * the workspace's error word and its token skipped.  A page that takes new
+ * tokens must belong to one row: two tokens of a call with one place would mix.
+ * `workspace` is a decode plan's workspace, or any 256 zeroed bytes. */
 PKV_API int pkv_mx4_append(const void *k, const void *v, int64_t k_stride_token,
                            int64_t k_stride_head, int64_t v_stride_token, int64_t v_stride_head,
                            void *pool, const int32_t *block_table, const int32_t *seq_lens,

@@ -703,6 +703,11 @@ def _cuda_index(name: str, t: torch.Tensor) -> int:
     return index
 
 
+def _check_plan(plan, index: int):
+    if plan.workspace.get_device() != index:
+        raise ValueError(f"the plan was made on {plan.workspace.device}, the tensors are on cuda:{index}")
+
+
 def _check_tensor(name: str, t: torch.Tensor, dtype, index: int, contiguous: bool = True):
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -756,6 +761,7 @@ def paged_decode_scored(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
     shape = plan.shape
     if not plan.plan.flags & FLAG_SCORES:
         raise ValueError("the plan was not made for scores: plan_decode(..., scores=True)")
+    _check_plan(plan, index)
     if out is None:
         out = _empty(q.shape, torch.bfloat16, index, stream)
     _check_decode_tensors(q, k_pool, v_pool, block_table, seq_lens, out, shape)
@@ -824,6 +830,7 @@ def evict_tokens(scores: torch.Tensor, planes: Sequence[torch.Tensor], block_tab
     shape = plan.shape
     if shape.B != B or shape.H_kv != H_kv or shape.max_pages_per_seq != max_pages:
         raise ValueError("the plan was made for another batch (B, H_kv or max_pages)")
+    _check_plan(plan, index)
     pos_ptr, pos_st = None, (0, 0)
     if positions is not None:
         pos_st = _check_scores("positions", positions, torch.int32, B, H_kv, max_pages, index)
@@ -929,6 +936,13 @@ def plan_mx4(shape: Shape, device, scores: bool = False, blocks: Optional[int] =
     return Mx4Plan(shape, plan, torch.zeros(n.value, dtype=torch.uint8, device=device))
 
 
+def _own_mx4_plan(pool, block_table, q_heads, scores: bool, stream) -> Mx4Plan:
+    """The plan of a call that was given none; its workspace belongs to the call's stream."""
+    index = _cuda_index("pool", pool)
+    with _on(index, stream):
+        return plan_mx4(mx4_shape(pool, block_table, q_heads), index, scores)
+
+
 def _check_mx4(pool, block_table, seq_lens, shape: Shape) -> int:
     """The pool, table and lengths of a call against its plan's shape; one combined test passes every well-formed
     call, the itemised ones name what is wrong with another.  Returns the device index."""
@@ -988,9 +1002,10 @@ def mx4_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, block_table
     (workspace_status(plan))."""
     L = lib()
     if plan is None:
-        plan = plan_mx4(mx4_shape(pool, block_table), _cuda_index("pool", pool))
+        plan = _own_mx4_plan(pool, block_table, None, False, stream)
     shape = plan.shape
     index = _check_mx4(pool, block_table, seq_lens, shape)
+    _check_plan(plan, index)
     n = k.shape[0]
     k_token, k_head = _check_token_rows("k", k, n, shape, index)
     v_token, v_head = _check_token_rows("v", v, n, shape, index)
@@ -1007,9 +1022,10 @@ def mx4_read(pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tens
     indptr wrote.  Exact.  `out` = (k, v) is written in place; tokens that the append skips get zeros."""
     L = lib()
     if plan is None:
-        plan = plan_mx4(mx4_shape(pool, block_table), _cuda_index("pool", pool))
+        plan = _own_mx4_plan(pool, block_table, None, False, stream)
     shape = plan.shape
     index = _check_mx4(pool, block_table, seq_lens, shape)
+    _check_plan(plan, index)
     n = int(n_tokens)
     if n < 0:
         raise ValueError(f"n_tokens must be >= 0, got {n}")
@@ -1037,9 +1053,10 @@ def mx4_decode(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, s
     a captured call can be replayed after seq_lens changed on the device."""
     L = lib()
     if plan is None:
-        plan = plan_mx4(mx4_shape(pool, block_table, int(q.shape[1])), _cuda_index("pool", pool), scores is not None)
+        plan = _own_mx4_plan(pool, block_table, int(q.shape[1]), scores is not None, stream)
     shape = plan.shape
     index = _check_mx4(pool, block_table, seq_lens, shape)
+    _check_plan(plan, index)
     _check_tensor("q", q, torch.bfloat16, index)
     if q.shape != (shape.B, shape.H_q, shape.head_dim):
         raise ValueError(f"q must be [{shape.B}][{shape.H_q}][{shape.head_dim}], got {list(q.shape)}")
