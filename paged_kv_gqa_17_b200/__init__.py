@@ -5,7 +5,9 @@ table, where G = H_q / H_kv query heads share each KV head: a split-S kernel
 whose chunks produce partial softmax states, an exact merge, a compact work
 queue (with a chunk that can fill one wave of the GPU, and a balanced cut for
 a persistent grid, both also buildable on the device) and a calibrated policy
-that picks the plan per batch.  Every step runs in the C-ABI library
+that picks the plan per batch.  Beside it stand operators that shrink the
+cache: decode that accumulates attention weights, eviction by them, and a
+microscaled 4-bit cache with its own decode.  Every step runs in the C-ABI library
 `libpkv.so` (CUDA for sm_100a plus host C++); this package only marshals
 arguments to it.
 
