@@ -696,6 +696,14 @@ def _empty(shape, dtype, index: int, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=index)
 
 
+def _empty_like(t: torch.Tensor, index: int, stream) -> torch.Tensor:
+    """The same by a (CUDA, contiguous) tensor's example, which is cheaper."""
+    if stream is None:
+        return torch.empty_like(t)
+    with _on(index, stream):
+        return torch.empty_like(t)
+
+
 def _cuda_index(name: str, t: torch.Tensor) -> int:
     index = t.get_device()
     if index < 0:
@@ -763,7 +771,7 @@ def paged_decode_scored(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
         raise ValueError("the plan was not made for scores: plan_decode(..., scores=True)")
     _check_plan(plan, index)
     if out is None:
-        out = _empty(q.shape, torch.bfloat16, index, stream)
+        out = _empty_like(q, index, stream)
     _check_decode_tensors(q, k_pool, v_pool, block_table, seq_lens, out, shape)
     st = _check_scores("scores", scores, torch.float32, shape.B, shape.H_kv, shape.max_pages_per_seq, index)
     ws = plan.workspace
@@ -835,10 +843,12 @@ def evict_tokens(scores: torch.Tensor, planes: Sequence[torch.Tensor], block_tab
     if positions is not None:
         pos_st = _check_scores("positions", positions, torch.int32, B, H_kv, max_pages, index)
         pos_ptr = positions.data_ptr()
+    _check_tensor("block_table", block_table, torch.int32, index)
+    _check_tensor("seq_lens", seq_lens, torch.int32, index)
     if out is None:
-        out = _empty(B, torch.int32, index, stream)
-    for name, t in (("block_table", block_table), ("seq_lens", seq_lens), ("out", out)):
-        _check_tensor(name, t, torch.int32, index)
+        out = _empty_like(seq_lens, index, stream) if seq_lens.shape == (B,) else _empty(B, torch.int32, index, stream)
+    else:
+        _check_tensor("out", out, torch.int32, index)
     lens_ptr, out_ptr = seq_lens.data_ptr(), out.data_ptr()
     if seq_lens.numel() < B or out.numel() < B:
         raise ValueError(f"seq_lens and out must hold {B} lengths")
@@ -1032,7 +1042,8 @@ def mx4_read(pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tens
     ptr = _check_indptr(indptr, n, shape, index)
     dims = (n, shape.H_kv, shape.head_dim)
     if out is None:
-        k, v = _empty(dims, torch.bfloat16, index, stream), _empty(dims, torch.bfloat16, index, stream)
+        k = _empty(dims, torch.bfloat16, index, stream)
+        v = _empty_like(k, index, stream)
     else:
         k, v = out
         for name, t in (("k", k), ("v", v)):
@@ -1067,7 +1078,7 @@ def mx4_decode(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, s
         st = _check_scores("scores", scores, torch.float32, shape.B, shape.H_kv, shape.max_pages_per_seq, index)
         score_ptr = scores.data_ptr()
     if out is None:
-        out = _empty(q.shape, torch.bfloat16, index, stream)
+        out = _empty_like(q, index, stream)
     else:
         _check_tensor("out", out, torch.bfloat16, index)
         if out.shape != q.shape:
