@@ -353,10 +353,12 @@ __global__ void __launch_bounds__(kTokenThreads) mx4_read_kernel(const __grid_co
 
 constexpr int kMaxRows = 4096;       // rows whose page offsets a block keeps in shared memory
 constexpr int kMaxBlocks = 1024;
-// P is held times 2^kPShift relative to the reference max and may grow to
-// 2^kPTop, the top of f16's range, before the reference has to move.
+// A pair's P are 2^(logit - m), with the reference m set kPShift below the
+// largest logit; they may grow to 2^kPTop, the top of f16's range, before it
+// has to move.  Sums of values between warps and blocks are kept times kPUnit,
+// 2^-kPShift, so that they reach no further than the values themselves do.
 constexpr float kPShift = 8.f, kPTop = 15.f;
-constexpr float kPUnit = 0x1p-8f;    // 2^-kPShift
+constexpr float kPUnit = 0x1p-8f;
 
 struct DecodeParams {
     const __nv_bfloat16 *q;
@@ -437,12 +439,12 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
 }
 
 // A warp's running state for one pair: heads 8 nt + 2 c + {0, 1}.  o is in units of
-// 2^(vref(b) - 127 - kPShift) for its block b of 32 dims, l in units of 2^-kPShift.
+// 2^(vref(b) - 127) for its block b of 32 dims.
 template <int D, int NT>
 struct State {
     uint32_t qf[D / 16][NT][2];  // q as the MMA's B operand
     float sl[NT][2];             // logit = product * sl (log2 domain)
-    float nb[NT][2];             // kPShift - m, with m the reference max (log2 domain): P is 2^(logit + nb)
+    float nb[NT][2];             // -m, minus the reference (log2 domain): P is 2^(logit + nb)
     float l[NT][2];
     float o[D / 16][NT][4];
     uint32_t vlow;               // per block the lower end of its window of V's scales, 0 .. 247; ~0: none yet
@@ -737,10 +739,14 @@ __device__ __forceinline__ void add_values_wide(const uint8_t *rec, int nvalid, 
     }
 }
 
-// Moves the reference max to the largest logit so far (s: products, nv[h]
-// valid tokens per page), rescaling the state.  Out of line of the common
-// path: a pair's first pages come here, later ones only when a logit
-// outgrows the reference by 2^(kPTop - kPShift).
+// A product's logit (log2 domain).  An infinite product comes of a NaN scale
+// (255): + 0 * s makes it NaN.
+__device__ __forceinline__ float logit(float s, float sl) { return fmaf(s, 0.f, s * sl); }
+
+// Moves the references that the largest of these logits outgrew (s: products,
+// nv[h] valid tokens per page), rescaling the state.  Out of line of the common
+// path: a pair's first pages come here, later ones only when a logit grows by
+// 2^(kPTop - kPShift).
 template <int NT, int D>
 __device__ __forceinline__ void move_reference(const float (&s)[2][NT][4], const int (&nv)[2], int lane, State<D, NT> &st)
 {
@@ -749,22 +755,27 @@ __device__ __forceinline__ void move_reference(const float (&s)[2][NT][4], const
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const float old = kPShift - st.nb[nt][j];
-            float mx = old;
+            float mx = -INFINITY;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float v = s[h][nt][2 * k + j];
+                for (int k = 0; k < 2; ++k)
                     if (r + 8 * k < nv[h])
-                        mx = fmaxf(mx, fmaf(v, 0.f, v * st.sl[nt][j]));
-                }
+                        mx = fmaxf(mx, logit(s[h][nt][2 * k + j], st.sl[nt][j]));
 #pragma unroll
             for (int sh = 4; sh < 32; sh <<= 1)
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+            const float old = -st.nb[nt][j];
+            float m = old;
+            if (mx - old > kPTop) {
+                m = mx - kPShift;
+                // where floats are further apart than kPShift (logits of 2^27 and more) that may have rounded too far down
+                if (mx - m > kPTop)
+                    m = mx;
+            }
             // a head with nothing but NaN so far: -inf - -inf, NaN as its sums are
-            const float al = exp2_approx(old - mx);
-            st.nb[nt][j] = kPShift - mx;
+            const float al = exp2_approx(old - m);
+            st.nb[nt][j] = -m;
             st.l[nt][j] *= al;
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt) {
@@ -801,7 +812,7 @@ __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)
                     float x[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        x[i] = fmaf(s[h][nt][i], 0.f, s[h][nt][i] * st.sl[nt][i & 1]);
+                        x[i] = logit(s[h][nt][i], st.sl[nt][i & 1]);
                     float *dst = logits + (h * kPage + r) * logit_heads + g;
                     if (r < nv[h])
                         *reinterpret_cast<float2 *>(dst) = make_float2(x[0], x[1]);
@@ -824,7 +835,7 @@ __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)
             st.vlow |= (uint32_t)min(max((int)((first >> (8 * b)) & 255u) - 4, 0), 247) << (8 * b);
     }
 #pragma unroll 1
-    for (;;) {  // twice where the reference has to move (from infinity on the pair's first pages), else once
+    for (int turn = 0;; ++turn) {  // twice where a reference has to move (from -infinity on the pair's first pages)
         float top = -INFINITY;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -832,13 +843,12 @@ __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    // an infinite product comes of a NaN scale (255): + 0 * s makes it NaN
-                    t[h][nt][i] = fmaf(s[h][nt][i], 0.f, fmaf(s[h][nt][i], st.sl[nt][i & 1], st.nb[nt][i & 1]));
+                    t[h][nt][i] = logit(s[h][nt][i], st.sl[nt][i & 1]) + st.nb[nt][i & 1];
                     if (!full && r + (i < 2 ? 0 : 8) >= nv[h])
                         t[h][nt][i] = -INFINITY;
                     top = fmaxf(top, t[h][nt][i]);
                 }
-        if (!__any_sync(0xffffffffu, top > kPTop))
+        if (turn == 1 || !__any_sync(0xffffffffu, top > kPTop))
             break;
         move_reference(s, nv, lane, st);
     }
@@ -908,20 +918,23 @@ __device__ __forceinline__ bool attend_whole_pages(const uint8_t *rec, int lane,
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if constexpr (SCORED) {
+                // the weights are worked out from the rounded logits, so P is too
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    t[h][nt][i] = logit(t[h][nt][i], st.sl[nt][i & 1]);
                 const int g = 8 * nt + 2 * c;
                 if (g < logit_heads) {
-                    float x[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[i] = fmaf(t[h][nt][i], 0.f, t[h][nt][i] * st.sl[nt][i & 1]);
                     float *dst = logits + (h * kPage + r) * logit_heads + g;
-                    *reinterpret_cast<float2 *>(dst) = make_float2(x[0], x[1]);
-                    *reinterpret_cast<float2 *>(dst + 8 * logit_heads) = make_float2(x[2], x[3]);
+                    *reinterpret_cast<float2 *>(dst) = make_float2(t[h][nt][0], t[h][nt][1]);
+                    *reinterpret_cast<float2 *>(dst + 8 * logit_heads) = make_float2(t[h][nt][2], t[h][nt][3]);
                 }
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                t[h][nt][i] = fmaf(t[h][nt][i], 0.f, fmaf(t[h][nt][i], st.sl[nt][i & 1], st.nb[nt][i & 1]));
+                if constexpr (SCORED)
+                    t[h][nt][i] += st.nb[nt][i & 1];
+                else
+                    t[h][nt][i] = fmaf(t[h][nt][i], 0.f, fmaf(t[h][nt][i], st.sl[nt][i & 1], st.nb[nt][i & 1]));
                 top = fmaxf(top, t[h][nt][i]);
             }
         }
@@ -951,7 +964,7 @@ __device__ __forceinline__ bool attend_whole_pages(const uint8_t *rec, int lane,
     return true;
 }
 
-// A warp's finished state to shared memory, in true units: o [head][D + 4], m, l per head.
+// A warp's finished state to shared memory: o [head][D + 4] times kPUnit, m, l per head.
 template <int D, int NT>
 __device__ __forceinline__ void put_state(float *dst, int lane, const State<D, NT> &st)
 {
@@ -968,12 +981,12 @@ __device__ __forceinline__ void put_state(float *dst, int lane, const State<D, N
             for (int sh = 4; sh < 32; sh <<= 1)
                 l += __shfl_xor_sync(0xffffffffu, l, sh);
             if (r == 0) {
-                dm[g] = kPShift - st.nb[nt][j];
-                dl[g] = l * kPUnit;
+                dm[g] = -st.nb[nt][j];
+                dl[g] = l;
             }
 #pragma unroll
             for (int b = 0; b < D / 32; ++b) {
-                // 2^(vref - 127 - kPShift) in two steps, the exponent byte itself the second
+                // kPUnit 2^(vref - 127) in two steps, the exponent byte itself the second
                 const float f = __uint_as_float((uint32_t)st.vref(b) << 23);
                 *reinterpret_cast<float4 *>(dst + g * (D + 4) + 32 * b + 4 * r) =
                     make_float4(st.o[2 * b][nt][j] * kPUnit * f, st.o[2 * b][nt][2 + j] * kPUnit * f,
@@ -998,8 +1011,7 @@ __device__ __forceinline__ void write_pair(const DecodeParams &p, int pair, int 
                 l += __shfl_xor_sync(0xffffffffu, l, sh);
             if (g >= p.G)
                 continue;
-            l *= kPUnit;
-            const float inv = (l == 0.f ? 0.f : 1.f / l) * kPUnit;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             __nv_bfloat16 *dst = p.out + ((int64_t)pair * p.G + g) * D;
 #pragma unroll
             for (int b = 0; b < D / 32; ++b) {
@@ -1010,7 +1022,7 @@ __device__ __forceinline__ void write_pair(const DecodeParams &p, int pair, int 
             }
             if (SCORED && r == 0) {
                 const int64_t at = (int64_t)(2 * p.blocks + pair) * p.G + g;
-                p.ws_m[at] = kPShift - st.nb[nt][j];
+                p.ws_m[at] = -st.nb[nt][j];
                 p.ws_l[at] = l;
                 if (g == 0)
                     p.ranges[pair] = SlotRange{2 * p.blocks + pair, 1, 0, 0};
@@ -1303,7 +1315,7 @@ __global__ void __launch_bounds__(DCfg<D, NT>::kThreads, 1) mx4_decode_kernel(co
         const bool whole = at.w >= 2 * p.blocks;
         const int64_t to = (int64_t)at.w * G + g;
         if (whole)
-            store_bf16x4(p.out + ((int64_t)at.x * G + g) * D + d4, scale4(O, L == 0.f ? 0.f : 1.f / L));
+            store_bf16x4(p.out + ((int64_t)at.x * G + g) * D + d4, scale4(O, L == 0.f ? 0.f : 1.f / kPUnit / L));
         else
             *reinterpret_cast<float4 *>(p.ws_acc + to * D + d4) = O;
         if (d4 == 0 && (SCORED || !whole)) {
@@ -1397,7 +1409,7 @@ __global__ void __launch_bounds__(kFinishThreads) mx4_finish_kernel(const __grid
 #pragma unroll
     for (int k = 1; k < kParts; ++k)
         O = fma4(s_o[k][col], 1.f, O);
-    store_bf16x4(p.out + ((int64_t)pair * G + g) * D + col * 4, scale4(O, L == 0.f ? 0.f : 1.f / L));
+    store_bf16x4(p.out + ((int64_t)pair * G + g) * D + col * 4, scale4(O, L == 0.f ? 0.f : 1.f / kPUnit / L));
 }
 
 // ---------------------------------------------------------------------------

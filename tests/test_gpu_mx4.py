@@ -251,6 +251,33 @@ def test_peaked_softmax_over_a_long_row():
     Case([4000], 1, 8, 128, q_scale=30.0).run(True)
 
 
+@pytest.mark.parametrize("exponent", [18, 19, 21, 60, -100])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("scores", [False, True])
+def test_logits_whose_floats_are_far_apart(exponent, D, scores):
+    """Queries of 1 and -1 on unit scales: products are multiples of 1/2, exact in fp32, so equal ones give equal
+    logits and the others lie 2^(exponent - 1) apart, which leaves them no weight.  Logits of 2^27 and more cannot be
+    shifted by small amounts."""
+    c = Case([1, 40, 700, 3, 16], 2, 4, D, seed=exponent + 200)
+    c.pool[:, :, 16 * D:16 * D + D // 2] = np.where(c.pool[:, :, 16 * D:16 * D + D // 2] == 255, 255, 127)
+    c.q = c.q.sign()
+    c.scale = 2.0 ** exponent
+    q, pool, table, lens = c.device()
+    for blocks in (None, 3):
+        plan = bd.plan_mx4(bd.mx4_shape(pool, table, q.shape[1]), "cuda", scores=scores, blocks=blocks)
+        s = torch.from_numpy(c.before).cuda() if scores else None
+        out = bd.mx4_decode(q, pool, table, lens, 16, c.scale, plan=plan, scores=s).double().cpu().numpy()
+        assert bd.workspace_status(plan) == 0
+        for i, n in enumerate(c.lens):
+            k, v = U.mx4_rows(c.pool, c.table, c.lens, i)
+            want, w, reach, size = C.attend(c.q[i].double().numpy(), k, v, c.scale, c.G)
+            exact = np.zeros_like(size)  # no error in the logits that count
+            U.check_out(out[i], want, reach, exact, D, c.scale, U.F16_HALF, (blocks, i))
+            if scores:
+                got = s[i].double().cpu().numpy()
+                U.check_scores(got[:, :n], c.before[i, :, :n].astype(float), w, exact, D, c.scale, (blocks, i))
+
+
 def test_infinities_and_nan_stay_in_their_rows():
     c = Case([40, 40, 40], 1, 4, 128)
     D = c.D
