@@ -455,8 +455,9 @@ PKV_API int pkv_evict_workspace_bytes(const pkv_shape *shape, size_t *bytes);
  *   workspace  >= pkv_evict_workspace_bytes(), zeroed once
  * A page that two of the rows (or two places of one row) share is moved for
  * each of them: give shared pages to one row, or copy them, before evicting.
- * A page id out of range is reported (pkv_workspace_status) and its tokens
- * are not moved; so is a length out of range, whose row is left alone
+ * A page id out of range is reported (pkv_workspace_status) and moves to or
+ * from it leave the planes alone (scores and positions move all the same);
+ * so is a length out of range, whose row is left alone
  * (new_lens gets it clamped).  One kernel, asynchronous on `stream`,
  * capturable, deterministic. */
 PKV_API int pkv_evict_tokens(float *scores, int64_t score_stride_row, int64_t score_stride_head,
