@@ -88,8 +88,8 @@ struct TokenMap {
 
 // The record of token j (of head 0) and its slot, or NULL: no row's token, or
 // out of its row's pages or the pool (reported).
-__device__ __forceinline__ uint8_t *token_record(const TokenMap &m, uint8_t *pool, int64_t stride_page, int j,
-                                                 bool report, int &slot)
+__device__ __forceinline__ const uint8_t *token_record(const TokenMap &m, const uint8_t *pool, int64_t stride_page, int j,
+                                                       bool report, int &slot)
 {
     int row = j;
     int64_t at;
@@ -144,118 +144,152 @@ struct ReadParams {
 
 constexpr int kTokenThreads = 256;
 
-// Both token kernels: D/8 lanes take one row (K or V of a token's head), eight
-// dims each; a warp takes 32 / (D/4) heads at a time, K and V side by side,
-// ROUNDS times over before it uses the first, so that the many small rows
-// keep the memory busy.  Meanwhile one lane per (token, head) finds its record.
+// Both token kernels: D/16 lanes take one row (K or V of a token's head), eight
+// dims of two neighbouring scale blocks each; a warp takes 256 / D (token, head)
+// items at a time, K and V side by side, ROUNDS times over before it uses the
+// first, so that the many small rows keep the memory busy.  Meanwhile one lane per
+// item finds its record.
 template <int D, int ROUNDS>
 struct TokenTile {
-    static constexpr int kLanes = D / 8;               // per row
-    static constexpr int kHeads = 32 / (2 * kLanes);   // (token, head) items per round: 1 or 2
+    static constexpr int kLanes = D / 16;              // per row
+    static constexpr int kHeads = 32 / (2 * kLanes);   // items per round: 2 or 4
     static constexpr int kItems = kHeads * ROUNDS;     // per warp and pass
-    static_assert(kItems <= 32, "a lane per item");
+    static_assert(kItems <= 16, "a lane per item and side");
 };
 
-// The item of one lane: its token, head, record and slot (record NULL as token_record).
+// Lane l and l + 16 look after item base + l: its token and head.
 struct TokenItem {
     uint32_t j, head;
-    uint8_t *rec;
-    int slot;
+    bool mine;
 };
 
-// Lane l < kItems looks up item base + l.
 template <int D, int ROUNDS>
-__device__ __forceinline__ void locate_item(TokenItem &t, const TokenMap &m, uint8_t *pool, int64_t stride_page,
-                                            int64_t stride_head, uint32_t base, uint32_t items, int lane)
+__device__ __forceinline__ TokenItem item_of_lane(uint32_t base, uint32_t items, uint32_t H_kv, int lane)
 {
-    t.rec = nullptr;
-    t.slot = 0;
-    if (lane >= TokenTile<D, ROUNDS>::kItems || base + lane >= items)
-        return;
-    t.rec = token_record(m, pool, stride_page, (int)t.j, t.head == 0, t.slot);
-    if (t.rec)
-        t.rec += (int64_t)t.head * stride_head;
+    const uint32_t item = base + (lane & 15);
+    TokenItem t;
+    t.j = item / H_kv;
+    t.head = item - t.j * H_kv;
+    t.mine = (lane & 15) < TokenTile<D, ROUNDS>::kItems && item < items;
+    return t;
 }
 
-__device__ __forceinline__ uint8_t *shfl_pointer(uint8_t *x, int src)
+// The item's record with its slot in the low four bits (records are 16-byte
+// aligned), 0 as token_record's NULL; in lanes below 16.
+__device__ __forceinline__ uint64_t locate_item(const TokenItem &t, const TokenMap &m, const uint8_t *pool,
+                                                int64_t stride_page, int64_t stride_head, int lane)
 {
-    return reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, (unsigned long long)x, src));
+    if (!t.mine || lane >= 16)
+        return 0;
+    int slot = 0;
+    const uint8_t *rec = token_record(m, pool, stride_page, (int)t.j, t.head == 0, slot);
+    return rec ? (uint64_t)(rec + (int64_t)t.head * stride_head) + (uint32_t)slot : 0;
 }
 
-// V's two bytes per (block, r) of lane (b, c): rows r = 2c and 2c + 1 of block
-// b; with the neighbour block's lane (b ^ 1) they become four bytes of one r.
-// The exchange is its own inverse.
-__device__ __forceinline__ uint32_t pair_blocks(uint32_t codes, int b)
+// A lane's place in its row's records.  Its two blocks' codes are two words: of
+// K, a block each; of V, a row r = 2c and 2c + 1 each, with two bytes per block.
+template <int D>
+struct TokenLane {
+    int is_v, part, dim;     // K or V, item of the round, first dim (the second block's: + 32)
+    int code, gap, scale;    // bytes: codes' first word, to the second; the blocks' two scales
+    bool has_scale;
+    __device__ __forceinline__ explicit TokenLane(int lane)
+    {
+        using R = Rec<D>;
+        constexpr int kLanes = D / 16;
+        const int sub = lane % kLanes, two = sub >> 2, c = sub & 3;
+        is_v = (lane / kLanes) & 1;
+        part = lane / (2 * kLanes);
+        dim = 64 * two + 8 * c;
+        code = is_v ? R::kV + 2 * c * (D / 16) + 4 * two : c * (D / 8) + 8 * two;
+        gap = is_v ? D / 16 : 4;
+        scale = (is_v ? R::kVs : R::kKs) + 2 * two;
+        has_scale = c == 0;
+    }
+    // blocks' codes to words, and words to blocks' codes
+    __device__ __forceinline__ void exchange(uint32_t (&w)[2]) const
+    {
+        const uint32_t low = __byte_perm(w[0], w[1], is_v ? 0x5410 : 0x3210);
+        w[1] = __byte_perm(w[0], w[1], is_v ? 0x7632 : 0x7654);
+        w[0] = low;
+    }
+};
+
+// Eight bf16 values to codes and their block's scale byte.  The four lanes of a
+// block find its largest magnitude by two shuffles; the scale comes from that
+// magnitude's exponent field (its largest value lands in [4, 8) and saturates at 6),
+// and the products are by a power of two, exact where the code is not zero.
+__device__ __forceinline__ uint32_t quantise(const uint4 &raw, uint32_t &scale)
 {
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, codes, 4);
-    return b & 1 ? __byte_perm(codes, other, 0x3276) : __byte_perm(codes, other, 0x5410);
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    // bf16 magnitudes order like their bits, infinities and NaN above every number
+    uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                            __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    top = max(top & 0xffffu, top >> 16);  // bf16 bits of the block's largest magnitude
+    const bool bad = top >= 0x7f80u;      // the block reads back as NaN
+    const int s = max((int)(top >> 7) - 2, 1);
+    const float mul = __uint_as_float((uint32_t)(254 - s) << 23);  // 2^(127 - s)
+    scale = bad ? 255u : top == 0 ? 0u : (uint32_t)s;
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        x[2 * k] = __uint_as_float(w[k] << 16) * mul;
+        x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * mul;
+    }
+    return bad ? 0u : floats_to_codes(x);
 }
 
-// Quantises K and V of the new tokens into their slots.  Per row: the largest
-// magnitude of each block by two shuffles among its four lanes, the scale from
-// that magnitude's exponent field (its largest value lands in [4, 8) and
-// saturates at 6), and the products by a power of two, which are exact.
-// 4 D bytes in, 17 D / 16 out per token and head.  Bound by instruction issue
-// (68 % of its slots, the logic pipe at 62 %) before memory: 22983 tokens of 8
-// heads, D = 128, quantised and read back in 53.5 us, 32 us of it here (3.7 TB/s).
+// Quantises K and V of the new tokens into their slots: 4 D bytes in, 17 D / 8
+// out per token and head.  Two blocks to a lane: with one, the lookups, shuffles
+// and addresses took as many instructions as the values (29.0 us against 25.4 for 22983
+// tokens of 8 heads, D = 128: now 5.7 TB/s, 88 % of the copy rate).
 template <int D, int ROUNDS>
 __global__ void __launch_bounds__(kTokenThreads) mx4_write_kernel(const __grid_constant__ WriteParams p)
 {
     using R = Rec<D>;
     using T = TokenTile<D, ROUNDS>;
     const int lane = threadIdx.x & 31;
-    const int sub = lane % T::kLanes, is_v = (lane / T::kLanes) & 1, part = lane / (2 * T::kLanes);
-    const int b = sub >> 2, c = sub & 3;
+    const TokenLane<D> l(lane);
     const uint32_t items = (uint32_t)p.n_tokens * p.H_kv;  // below 2^31 (checked on the host)
-    const __nv_bfloat16 *in = (is_v ? p.v : p.k) + sub * 8;
-    const int64_t in_token = is_v ? p.v_token : p.k_token, in_head = is_v ? p.v_head : p.k_head;
-    const int at = is_v ? R::kV + (2 * c + (b & 1)) * (D / 16) + 4 * (b >> 1) : c * (D / 8) + 4 * b;
-    const int scale_at = (is_v ? R::kVs : R::kKs) + b;
+    const __nv_bfloat16 *in = (l.is_v ? p.v : p.k) + l.dim;
+    // lanes 16 to 31 work out where the items' values lie, the others where their keys do
+    const int64_t in_token = lane < 16 ? p.k_token : p.v_token, in_head = lane < 16 ? p.k_head : p.v_head;
     grid_dependency_wait();
     grid_launch_dependents();
     const uint32_t step = gridDim.x * (kTokenThreads / 32) * T::kItems;
     for (uint32_t base = (blockIdx.x * (kTokenThreads / 32) + threadIdx.x / 32) * T::kItems; base < items; base += step) {
-        TokenItem mine;
-        mine.j = (base + lane) / p.H_kv;
-        mine.head = base + lane - mine.j * p.H_kv;
-        uint4 raw[ROUNDS];
+        const TokenItem mine = item_of_lane<D, ROUNDS>(base, items, p.H_kv, lane);
+        const long long offset = mine.j * in_token + mine.head * in_head;
+        uint4 raw[ROUNDS][2];
 #pragma unroll
         for (int i = 0; i < ROUNDS; ++i) {
-            const uint32_t j = __shfl_sync(0xffffffffu, mine.j, i * T::kHeads + part);
-            const uint32_t head = __shfl_sync(0xffffffffu, mine.head, i * T::kHeads + part);
-            raw[i] = make_uint4(0, 0, 0, 0);
-            if (base + i * T::kHeads + part < items)
-                raw[i] = __ldg(reinterpret_cast<const uint4 *>(in + j * in_token + head * in_head));
-        }
-        locate_item<D, ROUNDS>(mine, p.map, p.pool, p.stride_page, p.stride_head, base, items, lane);
-#pragma unroll
-        for (int i = 0; i < ROUNDS; ++i) {
-            uint8_t *rec = shfl_pointer(mine.rec, i * T::kHeads + part);
-            const int slot = __shfl_sync(0xffffffffu, mine.slot, i * T::kHeads + part);
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-            // bf16 magnitudes order like their bits, infinities and NaN above every number
-            uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                                    __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            top = max(top & 0xffffu, top >> 16);  // bf16 bits of the block's largest magnitude
-            const bool bad = top >= 0x7f80u;      // the block reads back as NaN
-            int scale = max((int)(top >> 7) - 2, 1);
-            const float mul = __uint_as_float((uint32_t)(254 - scale) << 23);  // 2^(127 - scale)
-            scale = bad ? 255 : top == 0 ? 0 : scale;
-            float x[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                x[2 * k] = __uint_as_float(w[k] << 16) * mul;
-                x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * mul;
+            const int at = i * T::kHeads + l.part;
+            const __nv_bfloat16 *src = in + __shfl_sync(0xffffffffu, offset, 16 * l.is_v + at);
+            raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
+            if (base + at < items) {
+                raw[i][0] = __ldg(reinterpret_cast<const uint4 *>(src));
+                raw[i][1] = __ldg(reinterpret_cast<const uint4 *>(src + 32));
             }
-            const uint32_t codes = bad ? 0u : floats_to_codes(x);
-            const uint32_t paired = pair_blocks(codes, b);
-            if (!rec)
+        }
+        const unsigned long long found = locate_item(mine, p.map, p.pool, p.stride_page, p.stride_head, lane);
+#pragma unroll
+        for (int i = 0; i < ROUNDS; ++i) {
+            const unsigned long long to = __shfl_sync(0xffffffffu, found, i * T::kHeads + l.part);
+            uint32_t w[2], scale[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                w[k] = quantise(raw[i][k], scale[k]);
+            l.exchange(w);
+            if (to == 0)
                 continue;
-            *reinterpret_cast<uint32_t *>(rec + slot * R::kRow + at) = is_v ? paired : codes;
-            if (c == 0)
-                rec[scale_at + slot * R::kScaleRow] = (uint8_t)scale;
+            uint8_t *rec = reinterpret_cast<uint8_t *>(to & ~15ull);
+            const uint32_t slot = (uint32_t)to & 15u;
+            *reinterpret_cast<uint32_t *>(rec + slot * R::kRow + l.code) = w[0];
+            *reinterpret_cast<uint32_t *>(rec + slot * R::kRow + l.code + l.gap) = w[1];
+            if (l.has_scale)
+                *reinterpret_cast<uint16_t *>(rec + slot * R::kScaleRow + l.scale) = (uint16_t)(scale[0] | scale[1] << 8);
         }
     }
 }
@@ -266,55 +300,55 @@ __device__ __forceinline__ float scale_value(uint32_t s)
     return __uint_as_float(s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23);
 }
 
-// The stored values as bf16, exactly (e2m1 has two significant bits).  Bound by
-// memory: 29 us for 22983 tokens of 8 heads, D = 128, 4.1 TB/s.
+// The stored values as bf16, exactly (e2m1 has two significant bits): 25.7 us for
+// 22983 tokens of 8 heads, D = 128, 5.6 TB/s.
 template <int D, int ROUNDS>
 __global__ void __launch_bounds__(kTokenThreads) mx4_read_kernel(const __grid_constant__ ReadParams p)
 {
     using R = Rec<D>;
     using T = TokenTile<D, ROUNDS>;
     const int lane = threadIdx.x & 31;
-    const int sub = lane % T::kLanes, is_v = (lane / T::kLanes) & 1, part = lane / (2 * T::kLanes);
-    const int b = sub >> 2, c = sub & 3;
+    const TokenLane<D> l(lane);
     const uint32_t items = (uint32_t)p.n_tokens * p.H_kv;  // below 2^31 (checked on the host)
-    __nv_bfloat16 *out = (is_v ? p.v : p.k) + sub * 8;
-    const int at = is_v ? R::kV + (2 * c + (b & 1)) * (D / 16) + 4 * (b >> 1) : c * (D / 8) + 4 * b;
-    const int scale_at = (is_v ? R::kVs : R::kKs) + b;
+    __nv_bfloat16 *out = (l.is_v ? p.v : p.k) + l.dim;
     grid_dependency_wait();
     grid_launch_dependents();
     const uint32_t step = gridDim.x * (kTokenThreads / 32) * T::kItems;
     for (uint32_t base = (blockIdx.x * (kTokenThreads / 32) + threadIdx.x / 32) * T::kItems; base < items; base += step) {
-        TokenItem mine;
-        mine.j = (base + lane) / p.H_kv;
-        mine.head = base + lane - mine.j * p.H_kv;
-        locate_item<D, ROUNDS>(mine, p.map, const_cast<uint8_t *>(p.pool), p.stride_page, p.stride_head, base, items,
-                               lane);
-        uint32_t codes[ROUNDS], scale[ROUNDS];
+        const TokenItem mine = item_of_lane<D, ROUNDS>(base, items, p.H_kv, lane);
+        const unsigned long long found = locate_item(mine, p.map, p.pool, p.stride_page, p.stride_head, lane);
+        uint32_t codes[ROUNDS][2], scales[ROUNDS];
 #pragma unroll
         for (int i = 0; i < ROUNDS; ++i) {
-            const uint8_t *rec = shfl_pointer(mine.rec, i * T::kHeads + part);
-            const int slot = __shfl_sync(0xffffffffu, mine.slot, i * T::kHeads + part);
-            codes[i] = 0;  // a skipped token reads as zeros
-            scale[i] = 127;
-            if (rec) {
-                codes[i] = *reinterpret_cast<const uint32_t *>(rec + slot * R::kRow + at);
-                scale[i] = rec[scale_at + slot * R::kScaleRow];
+            const unsigned long long from = __shfl_sync(0xffffffffu, found, i * T::kHeads + l.part);
+            codes[i][0] = codes[i][1] = 0;  // a skipped token reads as zeros
+            scales[i] = 127 | 127 << 8;
+            if (from) {
+                const uint8_t *rec = reinterpret_cast<const uint8_t *>(from & ~15ull);
+                const uint32_t slot = (uint32_t)from & 15u;
+                codes[i][0] = *reinterpret_cast<const uint32_t *>(rec + slot * R::kRow + l.code);
+                codes[i][1] = *reinterpret_cast<const uint32_t *>(rec + slot * R::kRow + l.code + l.gap);
+                scales[i] = *reinterpret_cast<const uint16_t *>(rec + slot * R::kScaleRow + l.scale);
             }
         }
 #pragma unroll
         for (int i = 0; i < ROUNDS; ++i) {
-            const uint32_t paired = pair_blocks(codes[i], b);
-            const float s = scale_value(scale[i]);
-            uint32_t h[4], o[4];
-            codes_to_half2(is_v ? paired : codes[i], h);
+            const uint32_t item = base + i * T::kHeads + l.part;
+            if (item >= items)
+                continue;
+            l.exchange(codes[i]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
-                o[k] = pack_bf16(f.x * s, f.y * s);
+            for (int k = 0; k < 2; ++k) {
+                const float s = scale_value((scales[i] >> (8 * k)) & 255u);
+                uint32_t h[4], o[4];
+                codes_to_half2(codes[i][k], h);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
+                    o[j] = pack_bf16(f.x * s, f.y * s);
+                }
+                __stcs(reinterpret_cast<uint4 *>(out + (int64_t)item * D + 32 * k), make_uint4(o[0], o[1], o[2], o[3]));
             }
-            const uint32_t item = base + i * T::kHeads + part;
-            if (item < items)
-                __stcs(reinterpret_cast<uint4 *>(out + (int64_t)item * D), make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
 }
@@ -1505,19 +1539,20 @@ cudaError_t launch_finish(const FinishParams &p, bool scores, int64_t grid, cuda
 // Pages below which a decode of this tile is one block's: nothing to merge.
 int min_pages(int G) { return G <= 8 ? DCfg<128, 1>::kMinPages : DCfg<128, 2>::kMinPages; }
 
-// Rounds of a token kernel: eight where every warp of a full GPU then has a
-// pass (enough rows in flight to stream), else one, for the shortest way
-// through a few tokens.
-constexpr int kManyRounds = 8;
+// Rounds of a token kernel: four (enough rows in flight to stream) where one
+// would fill three quarters of a full GPU's warps, else one, for the shortest way
+// through a few tokens.  Quantising tokens of 8 heads, D = 128, one round against
+// four: 1024 tokens 3.1 and 3.4 us, 2048 tokens 4.4 and 4.1, 22983 tokens 30.9 and 25.4.
+constexpr int kManyRounds = 4;
 constexpr int kTokenBlocks = 148 * 8;  // of 256 threads: a full GPU
 
-bool many_rounds(int64_t items) { return items >= (int64_t)kTokenBlocks * (kTokenThreads / 32) * kManyRounds / 2; }
+bool many_rounds(int64_t rounds) { return rounds >= (int64_t)kTokenBlocks * (kTokenThreads / 32) * 3 / 4; }
 
 template <typename P>
 cudaError_t launch_tokens(void (*many)(P), void (*few)(P), int heads, const P &p, cudaStream_t st)
 {
     const int64_t items = (int64_t)p.n_tokens * p.H_kv;
-    const bool m = many_rounds(items);
+    const bool m = many_rounds(ceil_div(items, (int64_t)heads));
     const int64_t blocks = ceil_div(items, (int64_t)heads * (m ? kManyRounds : 1) * (kTokenThreads / 32));
     return launch_kernel(m ? many : few, (unsigned)std::min<int64_t>(blocks, kTokenBlocks), kTokenThreads, 0, st, true, p);
 }
@@ -1579,8 +1614,8 @@ int pkv_mx4_append(const void *k, const void *v, int64_t k_stride_token, int64_t
     p.H_kv = s.H_kv;
     const cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e = s.head_dim == 128
-                              ? launch_tokens(mx4_write_kernel<128, kManyRounds>, mx4_write_kernel<128, 1>, 1, p, st)
-                              : launch_tokens(mx4_write_kernel<64, kManyRounds>, mx4_write_kernel<64, 1>, 2, p, st);
+                              ? launch_tokens(mx4_write_kernel<128, kManyRounds>, mx4_write_kernel<128, 1>, 2, p, st)
+                              : launch_tokens(mx4_write_kernel<64, kManyRounds>, mx4_write_kernel<64, 1>, 4, p, st);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -1606,8 +1641,8 @@ int pkv_mx4_read(const void *pool, const int32_t *block_table, const int32_t *se
     p.H_kv = s.H_kv;
     const cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e = s.head_dim == 128
-                              ? launch_tokens(mx4_read_kernel<128, kManyRounds>, mx4_read_kernel<128, 1>, 1, p, st)
-                              : launch_tokens(mx4_read_kernel<64, kManyRounds>, mx4_read_kernel<64, 1>, 2, p, st);
+                              ? launch_tokens(mx4_read_kernel<128, kManyRounds>, mx4_read_kernel<128, 1>, 2, p, st)
+                              : launch_tokens(mx4_read_kernel<64, kManyRounds>, mx4_read_kernel<64, 1>, 4, p, st);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

@@ -87,6 +87,30 @@ def test_append_and_read(D, H, starts, counts):
         assert np.array_equal(got.double().cpu().numpy(), want, equal_nan=True)
 
 
+@pytest.mark.parametrize("D,H,counts", [(128, 7, [1501, 0, 700]), (64, 15, [33, 1931])])
+def test_prompts_long_enough_for_several_rounds(D, H, counts):
+    """More rows than a full GPU takes at one each, the last pass of a warp cut off."""
+    rng = np.random.default_rng(D)
+    starts = [3, 5, 20][:len(counts)]
+    lens = [s + c for s, c in zip(starts, counts)]
+    table, pages = U.scattered_table(rng, lens, max(-(-n // 16) for n in lens))
+    indptr = np.concatenate([[0], np.cumsum(counts)])
+    n = int(indptr[-1])
+    assert n * H * D // 256 > 148 * 64 * 3 // 4 and n * H % (1024 // D) != 0
+    k, v = tokens(rng, n, H, D), tokens(rng, n, H, D)
+    before = rng.integers(0, 256, (pages, H, 17 * D)).astype(np.uint8)
+    pool, td = torch.from_numpy(before).cuda(), torch.from_numpy(table).cuda()
+    start, ind = (torch.from_numpy(np.asarray(x, np.int32)).cuda() for x in (starts, indptr))
+    plan = bd.plan_mx4(bd.mx4_shape(pool, td), "cuda")
+    bd.mx4_append(k.cuda(), v.cuda(), pool, td, start, plan=plan, indptr=ind)
+    gk, gv = bd.mx4_read(pool, td, start, n, plan=plan, indptr=ind)
+    assert bd.workspace_status(plan) == 0
+    want, (wk, wv) = stored(before, k, v, table, starts, indptr)
+    assert (pool.cpu().numpy() == want).all()
+    for got, w in ((gk, wk), (gv, wv)):
+        assert np.array_equal(got.double().cpu().numpy(), w, equal_nan=True)
+
+
 def test_append_strided_inputs_and_pool():
     rng = np.random.default_rng(1)
     H, D, n = 2, 128, 21
