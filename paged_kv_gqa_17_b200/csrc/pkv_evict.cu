@@ -33,13 +33,13 @@
 // Up to kLocalKeys tokens the cluster's first block selects alone and the others
 // read its lists through distributed shared memory: a few thousand keys cost
 // less than the cluster barriers that sharing them takes (64 rows and heads of
-// 2064 tokens: 13.2 us against 24.4 us shared; at 9008 tokens the two meet, 24.8
+// 2064 tokens: 12.7 us against 24.4 us shared; at 9008 tokens the two meet, 24.4
 // and 23.5 us).  Above, the blocks own contiguous shares of [0, M), add their
 // counts through distributed shared memory, each block the values of its
 // slice, and hand the two lists over through the workspace.
 // Every write has one writer, so results are deterministic.
 //
-// What bounds it: one page over the budget, latency (13.2 us for 10 MB that could
+// What bounds it: one page over the budget, latency (12.7 us for 10 MB that could
 // pass in 1.6 us: a dependent chain of loads of scores, three digits, lists,
 // page ids and rows); whole prompts, memory (32 rows and heads of 16384 to 32768
 // fresh tokens to 8192, with nothing in L2: 82 us, 4.2 TB/s while the rows move).
@@ -63,8 +63,8 @@ constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;
 constexpr int kMaxPlanes = PKV_EVICT_MAX_PLANES;
 constexpr int kWide = 4;            // 16-byte units of recent tokens a thread has in flight
-constexpr int kDeep = 8;            // ... and of moves
-constexpr int kNarrow = 2;          // smaller ones
+constexpr int kDeep = 6;            // ... and of moves
+constexpr int kNarrow = 2;          // smaller ones; with 8 moves or 4 smaller units registers spill (12.7 -> 13.3 us one page over)
 
 // One array that moves with the tokens.  Paged: row bytes at
 // base + page * s0 + head * s1 + slot_in_page * s2; dense (scores,
