@@ -12,7 +12,7 @@ import json
 import os
 import weakref
 from dataclasses import dataclass
-from typing import List, Optional, Sequence
+from typing import List, Optional, Sequence, Union
 
 import torch
 
@@ -1057,12 +1057,17 @@ def mx4_read(pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tens
 
 def mx4_decode(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
                page_size: int, scale: float, *, plan: Optional[Mx4Plan] = None,
-               scores: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               scores: Union[torch.Tensor, bool, None] = None, out: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
     """paged_decode over a 4-bit pool; with `scores` (as in paged_decode_scored, and a plan with scores=True) the
-    attention weights are added to them.  q bf16 [B][H_q][D], 1 <= H_q / H_kv <= 16.  The plan serves any lengths, so
-    a captured call can be replayed after seq_lens changed on the device."""
+    attention weights are added to them; None and False, as plan_mx4 takes it, both say no scores.  q bf16
+    [B][H_q][D], 1 <= H_q / H_kv <= 16.  The plan serves any lengths, so a captured call can be replayed after
+    seq_lens changed on the device."""
     L = lib()
+    if scores is False:
+        scores = None
+    elif scores is not None and not isinstance(scores, torch.Tensor):
+        raise TypeError(f"scores must be a tensor, None or False, got {type(scores).__name__}")
     if plan is None:
         plan = _own_mx4_plan(pool, block_table, int(q.shape[1]), scores is not None, stream)
     shape = plan.shape
