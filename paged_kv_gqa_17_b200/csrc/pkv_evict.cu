@@ -128,7 +128,7 @@ struct __align__(16) EvictShared {
     uint32_t digit, above;
     uint32_t gt[kEvictWarps], eq[kEvictWarps];
     uint32_t block_gt, block_eq;  // read by the peers
-    uint32_t moves;               // likewise, written by the block that owns slot A
+    uint32_t moves;               // written by the block that owns slot A: to all (shared selection), or read by the peers
 };
 
 // The cluster's barrier: of one block, the block's.
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictPerSM) evict_kernel(const
                 }
                 if (slot == A) {
                     // kept_before tokens keep their slots below A: the other slots there are holes
-                    if (CS == 1)
+                    if (CS == 1 || LOCAL)
                         sh.moves = (uint32_t)(A - kept_before);
                     else
                         for (int c = 0; c < CS; ++c)
@@ -551,10 +551,14 @@ __global__ void __launch_bounds__(kEvictThreads, kEvictPerSM) evict_kernel(const
     int moves = 0;
     uint32_t hole_at = smem_addr(s_holes), mover_at = smem_addr(s_movers);  // of the block that selected
     if (A > 0) {
-        moves = (int)sh.moves;
         if (LOCAL && CS > 1) {
+            // The selecting block wrote these in its own shared memory alone: a block's may be touched by others only
+            // once it is known to run, and for a local selection the barrier above is the first to say so.
             hole_at = map_shared_rank(hole_at, 0);
             mover_at = map_shared_rank(mover_at, 0);
+            moves = (int)ld_cluster_u32(map_shared_rank(smem_addr(&sh.moves), 0));
+        } else {
+            moves = (int)sh.moves;
         }
     }
     auto mover = [&](int j) { return LOCAL ? ld_cluster_u16(mover_at + 2 * (moves - 1 - j)) : __ldcg(movers + moves - 1 - j); };
