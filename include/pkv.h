@@ -404,7 +404,11 @@ PKV_API int pkv_paged_decode(const void *q, const void *k_pool, const void *v_po
  * `plan` carries PKV_FLAG_SCORES (NO_SPLIT, SPLIT_S or WORK_QUEUE, device-filled queues
  * included); the workspace is sized by pkv_workspace_bytes for that plan and holds the logits
  * between the decode kernel and the weights kernel that follows it on `stream`.  A token whose
- * row attends to nothing (every logit -inf) gets no weight.  Deterministic.  Other arguments,
+ * row attends to nothing (every logit -inf) gets no weight.  Tokens that the call did not attend
+ * to keep their scores: those of a (row, KV head) one of whose work items was refused, and those
+ * past the end of a plan that was made for a shorter row, which is reported as a malformed work
+ * item in every mode (SPLIT_S reports it without scores too).  Nothing is added on a workspace
+ * that has recorded a timeout (pkv_workspace_init clears it).  Deterministic.  Other arguments,
  * layouts, errors and return codes as pkv_paged_decode. */
 PKV_API int pkv_paged_decode_scored(const void *q, const void *k_pool, const void *v_pool,
                                     const int32_t *block_table, const int32_t *seq_lens,

@@ -95,10 +95,11 @@ struct __align__(64) Params {
     int32_t n_units;          // prefix-sharing queue: units (the grid); their offsets follow the pair offsets
     int32_t device_fill;      // WORK_QUEUE: every block derives its own item from the device lengths
     int32_t fill_blocks;      // ... of the queue whose chunk fills one wave of this many blocks
-    // scored decode (PKV_FLAG_SCORES): the logits in the log2 domain, [pair][max_pages * P][logit_heads], and each
-    // pair's state slots, both for the weights kernel that follows
+    // scored decode (PKV_FLAG_SCORES): the logits in the log2 domain, [pair][max_pages * P][logit_heads], each pair's
+    // state slots and each slot's record, all for the weights kernel that follows
     float *logits;
     SlotRange *slot_range;
+    SlotRecord *records;
     int32_t logit_heads;
 #ifdef PKV_TRACE
     int32_t trace_epoch;
@@ -1175,6 +1176,15 @@ __global__ void __launch_bounds__((NW + 1) * 32, (NST >= 12 ? 2 : 3)) split_kern
             mbar_wait(bar_full + 8 * lane, 0, p.ws_error, kWaitLimitNs, p.host_err);
     };
 
+    // ... and tells the weights kernel that its slot holds nothing of this call
+    auto leave = [&]() {
+        drain();
+        if (SCORED && tid == 0) {
+            grid_dependency_wait();  // the kernel before may still read the records
+            p.records[blockIdx.x].pair = -1;
+        }
+    };
+
     // ---- which (row, KV head, token range) this block owns ----
     // The producer warp fetches the first 32 block-table entries of the
     // range as soon as the range's first page is known, which for the
@@ -1196,7 +1206,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, (NST >= 12 ? 2 : 3)) split_kern
         const FillItem f = fill_queue_item<C::kThreads>(p, fill_scratch, fill_res, false);
         PKV_TRACE_POINT(14);
         if (!f.valid) {
-            drain();
+            leave();
             return;
         }
         hit = guess.x == f.row && guess.y == f.h && guess.z == f.tb && guess.w == f.te;
@@ -1211,7 +1221,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, (NST >= 12 ? 2 : 3)) split_kern
         if (slot0 + nslots > p.n_items) {
             if (tid == 0)
                 raise_error(p, kErrItem);
-            drain();
+            leave();
             return;
         }
         if (warp == NW) {
@@ -1237,7 +1247,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, (NST >= 12 ? 2 : 3)) split_kern
                 g_entry = __ldg(p.block_table + (int64_t)guess.x * p.max_pages + idx);
         }
         if ((int)blockIdx.x >= n_real) {
-            drain();
+            leave();
             return;
         }
         hit = guess.x >= 0 && guess.x == it.x && guess.y == it.y && guess.z == it.z && guess.w == it.w;
@@ -1259,7 +1269,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, (NST >= 12 ? 2 : 3)) split_kern
         if (!ok) {
             if (tid == 0)
                 raise_error(p, kErrItem);
-            drain();
+            leave();
             return;
         }
         if (warp == NW) {
@@ -1394,6 +1404,13 @@ __global__ void __launch_bounds__((NW + 1) * 32, (NST >= 12 ? 2 : 3)) split_kern
         // Q as the MMA's B operand (k = head_dim, n = query head), loaded once.
         if (p.pdl_early)
             grid_dependency_wait();  // q may come from the previous kernel
+        if constexpr (SCORED) {
+            if (tid == 0) {
+                p.records[my_slot] = SlotRecord{pair, slot0, nslots, tb, te, {}};
+                if (my_slot == slot0)
+                    p.slot_range[pair] = SlotRange{slot0, nslots, slot0, 1};
+            }
+        }
         uint32_t qf[D / 16][NT][2];
         const __nv_bfloat16 *qb = p.q + ((int64_t)row * p.H_q + (int64_t)h * p.G) * D;
 #pragma unroll
@@ -1553,10 +1570,6 @@ __global__ void __launch_bounds__((NW + 1) * 32, (NST >= 12 ? 2 : 3)) split_kern
         }
     }
 
-    if constexpr (SCORED) {
-        if (tid == 0 && my_slot == slot0)
-            p.slot_range[pair] = SlotRange{slot0, nslots, slot0, 1};
-    }
     PKV_TRACE_POINT(4);
     if (CL) {
         // ---- cluster merge: the S blocks of this (row, KV head) form one
@@ -3089,6 +3102,7 @@ int paged_decode_impl(const void *q, const void *k_pool, const void *v_pool, con
     if (scores) {
         prm.logits = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + ws.logits_off);
         prm.slot_range = reinterpret_cast<SlotRange *>(static_cast<uint8_t *>(workspace) + ws.range_off);
+        prm.records = reinterpret_cast<SlotRecord *>(static_cast<uint8_t *>(workspace) + ws.record_off);
         prm.logit_heads = logit_heads(prm.G);
     }
 #ifdef PKV_TRACE
@@ -3136,6 +3150,8 @@ int paged_decode_impl(const void *q, const void *k_pool, const void *v_pool, con
         w.m = prm.ws_m;
         w.l = prm.ws_l;
         w.ranges = prm.slot_range;
+        w.records = prm.records;
+        w.ws_error = prm.ws_error;
         w.seq_lens = seq_lens;
         w.scores = scores->scores;
         w.stride_row = scores->stride_row;

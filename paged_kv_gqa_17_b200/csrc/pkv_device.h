@@ -371,17 +371,26 @@ struct ScoreArgs {
 };
 
 // The state slots of one (row, KV head): slot(0) = first, slot(i) = base + step * i.
-// `count` 0: none (no tokens, or a work item that was refused).
+// `count` 0: none.
 struct __align__(16) SlotRange {
     int32_t first, count, base, step;
     __device__ int64_t slot(int i) const { return i == 0 ? first : base + (int64_t)step * i; }
+};
+
+// What the block of a slot did in THIS call: every block of a scored bf16 decode writes its own slot's, also one that
+// refuses its work item or has none (pair -1).  The pairs' ranges and the states lie in a workspace that earlier calls
+// filled; only where a pair's records all agree were its states and logits of tokens [tb, te) written by this call.
+struct __align__(16) SlotRecord {
+    int32_t pair, first, count, tb, te, unused[3];
 };
 
 // Arguments of the weights kernel (pkv_scores.cu).
 struct WeightParams {
     const float *logits;       // [pair][capacity][logit_heads(G)], log2 domain
     const float *m, *l;        // [slot][G] states: running max (log2 domain) and denominator
-    const SlotRange *ranges;   // per pair
+    const SlotRange *ranges;   // per pair; the bf16 decode's are of this call only where the records say so
+    const SlotRecord *records; // bf16 decode: per slot
+    uint32_t *ws_error;
     const int32_t *seq_lens;
     float *scores;
     int64_t stride_row, stride_head;
@@ -395,18 +404,46 @@ constexpr int kWeightThreads = 256;
 constexpr int kWeightTokens = 1024;
 inline int64_t weight_blocks(int64_t pairs, int64_t capacity) { return pairs * ceil_div(capacity, kWeightTokens); }
 
+// The tokens of a pair, from 0, whose logits this call's bf16 decode wrote, for the whole
+// warp: the row's, or fewer where the plan covers fewer, or -1 where some item was refused.
+__device__ __forceinline__ int attended_end(const WeightParams &p, int pair, const SlotRange &range, int lane)
+{
+    bool ok = true;
+    int end = 0;
+    for (int k0 = 0; k0 < range.count; k0 += 32) {
+        const int k = k0 + lane;
+        int4 r = make_int4(pair, range.first, range.count, 0);
+        int te = 0;
+        if (k < range.count) {
+            const int4 *record = reinterpret_cast<const int4 *>(p.records + range.first + k);
+            r = __ldcg(record);
+            te = __ldcg(&record[1].x);
+        }
+        const int above = __shfl_up_sync(0xffffffffu, te, 1);
+        ok = ok && r.x == pair && r.y == range.first && r.z == range.count &&
+             (k >= range.count || r.w == (lane == 0 ? end : above));  // the tokens follow one another without a gap
+        end = __shfl_sync(0xffffffffu, te, min(31, range.count - 1 - k0));
+    }
+    return __all_sync(0xffffffffu, ok) ? end : -1;
+}
+
 // One block's part of the weights kernel, after the kernel before it has
 // completed: adds the weights of tokens [chunk * kWeightTokens, + kWeightTokens)
 // of a pair to its scores.  LH = logit_heads(G).  The token's logits and
 // scores are loaded before the pair's maximum and sum are known, all at once.
-template <int LH>
-__device__ __forceinline__ void add_weights(const WeightParams &p, int pair, int chunk, float *s_m, float *s_inv)
+// Tokens that the call's decode did not attend to (a refused work item's pair,
+// a row that is longer than its plan) keep their scores; so do all on a workspace
+// in which a wait ran out.  RECORDS: the bf16 decode's.
+template <int LH, bool RECORDS>
+__device__ __forceinline__ void add_weights(const WeightParams &p, int pair, int chunk, float *s_m, float *s_inv,
+                                            int *s_end)
 {
     constexpr int kTokens = kWeightTokens / kWeightThreads;
     const int row = pair / p.H_kv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t0 = (int64_t)chunk * kWeightTokens + threadIdx.x;
     const SlotRange range = p.ranges[pair];
+    const uint32_t error = __ldcg(p.ws_error);
     int64_t n = __ldg(p.seq_lens + row);
     n = n < 0 ? 0 : (n > p.capacity ? p.capacity : n);
     if ((int64_t)chunk * kWeightTokens >= n)
@@ -432,9 +469,18 @@ __device__ __forceinline__ void add_weights(const WeightParams &p, int pair, int
             }
         }
     }
-    // a decode block that refused a malformed work item leaves no usable range
     if (range.first < 0 || range.count < 1 || range.first >= p.n_slots || range.slot(range.count - 1) >= p.n_slots)
-        return;
+        return;  // none, or an earlier call's
+    if (error & kErrTimeout)
+        return;  // some page never came: states and logits may be missing
+    if (RECORDS && warp == kWeightThreads / 32 - 1) {
+        const int end = attended_end(p, pair, range, lane);
+        if (lane == 0) {
+            *s_end = end < 0 ? 0 : end;
+            if (chunk == 0 && end >= 0 && end < n)
+                atomicOr(p.ws_error, kErrItem);  // the plan does not cover this row
+        }
+    }
     for (int g = warp; g < LH; g += kWeightThreads / 32) {
         float m = -INFINITY, l = 0.f;
         if (g < p.G) {
@@ -473,10 +519,11 @@ __device__ __forceinline__ void add_weights(const WeightParams &p, int pair, int
         for (int k = 0; k < kTokens; ++k)
             w[k] = fmaf(exp2_approx(v[k][g] - m), inv, w[k]);
     }
+    const int64_t end = RECORDS ? min(n, (int64_t)*s_end) : n;
 #pragma unroll
     for (int k = 0; k < kTokens; ++k) {
         const int64_t t = t0 + k * kWeightThreads;
-        if (t < n)
+        if (t < end)
             out[t] = old[k] + w[k];
     }
 }

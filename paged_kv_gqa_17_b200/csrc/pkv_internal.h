@@ -31,6 +31,7 @@ struct WsLayout {
     size_t l_off = 0;        // float l[slot][G]
     size_t acc_off = 0;      // float acc[slot][G][D]
     size_t range_off = 0;    // PKV_FLAG_SCORES: the pair's slots, as int4 (SlotRange)
+    size_t record_off = 0;   // PKV_FLAG_SCORES: what each slot's block did, 32 bytes (SlotRecord)
     size_t logits_off = 0;   // PKV_FLAG_SCORES: float logits[pair][max_pages * P][logit_heads(G)]
     size_t total = 0;
     int64_t n_slots = 0;
@@ -64,6 +65,8 @@ inline WsLayout ws_layout(const pkv_shape &s, const pkv_plan &p, int32_t n_items
     if (scores) {
         w.range_off = off;
         off += round_up((size_t)pairs * 16, kWsAlign);
+        w.record_off = off;
+        off += round_up((size_t)w.n_slots * 32, kWsAlign);
         w.logits_off = off;
         off += round_up((size_t)pairs * s.max_pages_per_seq * s.page_size * logit_heads(G) * 4, kWsAlign);
     }

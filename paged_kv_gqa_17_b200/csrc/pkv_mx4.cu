@@ -1393,7 +1393,7 @@ __global__ void __launch_bounds__(kFinishThreads) mx4_finish_kernel(const __grid
     grid_launch_dependents();
     if (LH > 0 && (int)blockIdx.x >= p.blocks * G) {
         const int i = blockIdx.x - p.blocks * G;
-        add_weights<(LH > 0 ? LH : 2)>(p.w, i / p.chunks, i % p.chunks, s_m, s_inv);
+        add_weights<(LH > 0 ? LH : 2), false>(p.w, i / p.chunks, i % p.chunks, s_m, s_inv, nullptr);
         return;
     }
     const int b = blockIdx.x / G, g = blockIdx.x % G;
@@ -1740,6 +1740,7 @@ int pkv_mx4_decode(const void *q, const void *pool, const int32_t *block_table, 
     if (scores) {
         f.w.logits = p.logits;
         f.w.ranges = p.ranges;
+        f.w.ws_error = p.ws_error;
         f.w.seq_lens = seq_lens;
         f.w.scores = scores;
         f.w.stride_row = score_stride_row;

@@ -10,6 +10,10 @@
 // The weights need the final M and L, which no block of the decode has while
 // it streams K, so the logits make one trip through L2 (8 to 64 bytes per
 // token against 512 bytes of K and V at D = 128) instead of K being read again.
+// Scores outlive the call and decide what an eviction drops, so nothing of an
+// earlier call may enter them: the workspace is zeroed once, and a pair's range,
+// states and logits count only where every one of its slots' blocks left a
+// record of this call.  The check runs beside the loads of the states.
 // Sums run over the heads in ascending order and every score has one writer,
 // so results are deterministic.
 //
@@ -27,10 +31,11 @@ template <int LH>
 __global__ void __launch_bounds__(kWeightThreads) add_weights_kernel(const __grid_constant__ WeightParams p)
 {
     __shared__ float s_m[LH], s_inv[LH];
+    __shared__ int s_end;
     const int chunks = (int)((p.capacity + kWeightTokens - 1) / kWeightTokens);
     grid_dependency_wait();
     grid_launch_dependents();
-    add_weights<LH>(p, blockIdx.x / chunks, blockIdx.x % chunks, s_m, s_inv);
+    add_weights<LH, true>(p, blockIdx.x / chunks, blockIdx.x % chunks, s_m, s_inv, &s_end);
 }
 
 }  // namespace
