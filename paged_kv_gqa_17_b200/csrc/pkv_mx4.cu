@@ -17,6 +17,7 @@
 #include "pkv_device.h"
 
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cstring>
 
@@ -481,7 +482,7 @@ template <int D, int NT>
 struct State {
     uint32_t qf[D / 16][NT][2];  // q as the MMA's B operand
     float sl[NT][2];             // logit = product * sl (log2 domain)
-    float nb[NT][2];             // -m, minus the reference (log2 domain): P is 2^(logit + nb)
+    float nb[NT][2];             // -m, minus the reference (log2 domain): P is 2^(logit + nb); FLT_MAX: none yet
     float l[NT][2];
     float o[D / 16][NT][4];
     uint32_t vlow;               // per block the lower end of its window of V's scales, 0 .. 247; ~0: none yet
@@ -534,7 +535,8 @@ __device__ __forceinline__ void load_q(const DecodeParams &p, int pair, int lane
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        st.nb[nt][0] = st.nb[nt][1] = INFINITY;
+        // Any logit but -inf, which has no weight (P = 0, where infinity would make NaN of it), outgrows this reference
+        st.nb[nt][0] = st.nb[nt][1] = FLT_MAX;
         st.l[nt][0] = st.l[nt][1] = 0.f;
 #pragma unroll
         for (int mt = 0; mt < D / 16; ++mt)
@@ -810,7 +812,6 @@ __device__ __forceinline__ void move_reference(const float (&s)[2][NT][4], const
                 if (mx - m > kPTop)
                     m = mx;
             }
-            // a head with nothing but NaN so far: -inf - -inf, NaN as its sums are
             const float al = exp2_approx(old - m);
             st.nb[nt][j] = -m;
             st.l[nt][j] *= al;
@@ -872,7 +873,7 @@ __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)
             st.vlow |= (uint32_t)min(max((int)((first >> (8 * b)) & 255u) - 4, 0), 247) << (8 * b);
     }
 #pragma unroll 1
-    for (int turn = 0;; ++turn) {  // twice where a reference has to move (from -infinity on the pair's first pages)
+    for (int turn = 0;; ++turn) {  // twice where a reference has to move (from none on the pair's first pages)
         float top = -INFINITY;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
