@@ -482,6 +482,7 @@ template <int D, int NT>
 struct State {
     uint32_t qf[D / 16][NT][2];  // q as the MMA's B operand
     float sl[NT][2];             // logit = product * sl (log2 domain)
+    uint32_t q_exp;              // byte 2 nt + j: the exponent byte of what undoes a head's scaling of q to f16
     float nb[NT][2];             // -m, minus the reference (log2 domain): P is 2^(logit + nb); FLT_MAX: none yet
     float l[NT][2];
     float o[D / 16][NT][4];
@@ -513,9 +514,11 @@ __device__ __forceinline__ void load_q(const DecodeParams &p, int pair, int lane
         }
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // the largest element to [2^13, 2^14): 2^up and its inverse stay normal floats for |up| <= 126
+        // The largest element to [2^13, 2^14): 2^up and its inverse stay normal floats for |up| <= 126.  Elements keep
+        // bf16's eight bits down to 2^-30 of it; smaller ones are rounded to multiples of 2^-38 of it, so a logit is
+        // off by at most scale 2^-38 max|q| sum |k|.
         const int e = (int)(amax >> 23);
-        const int up = e == 0 || e == 255 ? 0 : min(126, 13 + 127 - e);
+        const int up = e == 255 ? 0 : min(126, 13 + 127 - e);
         const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
 #pragma unroll
         for (int b = 0; b < D / 32; ++b) {
@@ -532,6 +535,9 @@ __device__ __forceinline__ void load_q(const DecodeParams &p, int pair, int lane
         const float inv = p.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
         st.sl[nt][0] = __shfl_sync(0xffffffffu, inv, 8 * c);
         st.sl[nt][1] = __shfl_sync(0xffffffffu, inv, 8 * c + 4);
+        const uint32_t both = (uint32_t)__shfl_sync(0xffffffffu, 127 - up, 8 * c) |
+                              (uint32_t)__shfl_sync(0xffffffffu, 127 - up, 8 * c + 4) << 8;
+        st.q_exp = nt == 0 ? both : st.q_exp | both << 16;
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -589,8 +595,14 @@ __device__ __forceinline__ int top_scale(const uint32_t (&vs)[4], int lane, int 
 
 // S^T = K q^T of one page, each block of 32 dims under its tokens' scales:
 // rows are tokens r and r + 8, columns heads 8 nt + 2c and 2c + 1.
-template <int D, int NT>
-__device__ __forceinline__ void page_products(const uint8_t *rec, int lane, const State<D, NT> &st, float (&s)[NT][4])
+// Products carry q's scaling to f16, 2^up, which takes them out of fp32 where
+// large keys meet small queries although the logits are ordinary.  WIDE undoes
+// an up above 0 before the keys' scales, so that only what K q^T itself cannot
+// hold overflows (under an up below 0 the product is the smaller one anyway), and takes a
+// scale of 255 for the NaN it is; s are logits then.
+template <int D, int NT, bool WIDE>
+__device__ __forceinline__ void page_products(const uint8_t *rec, int lane, const State<D, NT> &st, float (&s)[NT][4],
+                                              float scale_log2 = 0.f)
 {
     using R = Rec<D>;
     constexpr int kBlocks = D / 32;
@@ -616,16 +628,32 @@ __device__ __forceinline__ void page_products(const uint8_t *rec, int lane, cons
         uint32_t fa[4], fb[4];
         codes_to_half2(ka[b], fa);
         codes_to_half2(kb[b], fb);
-        const float sa = exponent_float(ksa, b), sb = exponent_float(ksb, b);
+        float sa = exponent_float(ksa, b), sb = exponent_float(ksb, b);
+        if (WIDE) {
+            sa = fmaf(sa, 0.f, sa);
+            sb = fmaf(sb, 0.f, sb);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float part[4];
             mma_f16_new(part, fa[0], fb[0], fa[1], fb[1], st.qf[2 * b][nt][0], st.qf[2 * b][nt][1]);
             mma_f16(part, fa[2], fb[2], fa[3], fb[3], st.qf[2 * b + 1][nt][0], st.qf[2 * b + 1][nt][1]);
+            if (WIDE) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    part[i] *= fminf(1.f, exponent_float(st.q_exp, 2 * nt + (i & 1)));
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 s[nt][i] = b == 0 ? part[i] * (i < 2 ? sa : sb) : fmaf(part[i], i < 2 ? sa : sb, s[nt][i]);
         }
+    }
+    if (WIDE) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // rounded before the reference comes off, as the weights kernel has them
+                s[nt][i] = __fmul_rn(s[nt][i] * scale_log2, fmaxf(1.f, exponent_float(st.q_exp, 2 * nt + (i & 1))));
     }
 }
 
@@ -779,15 +807,24 @@ __device__ __forceinline__ void add_values_wide(const uint8_t *rec, int nvalid, 
 }
 
 // A product's logit (log2 domain).  An infinite product comes of a NaN scale
-// (255): + 0 * s makes it NaN.
+// (255), or of factors that page_products<WIDE> keeps in range: + 0 * s makes it
+// NaN, which sends its page there.
 __device__ __forceinline__ float logit(float s, float sl) { return fmaf(s, 0.f, s * sl); }
 
-// Moves the references that the largest of these logits outgrew (s: products,
+// The larger of two numbers, NaN if either is.
+__device__ __forceinline__ float max_or_nan(float a, float b)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// Moves the references that the largest of these logits outgrew (x: logits,
 // nv[h] valid tokens per page), rescaling the state.  Out of line of the common
 // path: a pair's first pages come here, later ones only when a logit grows by
 // 2^(kPTop - kPShift).
 template <int NT, int D>
-__device__ __forceinline__ void move_reference(const float (&s)[2][NT][4], const int (&nv)[2], int lane, State<D, NT> &st)
+__device__ __forceinline__ void move_reference(const float (&x)[2][NT][4], const int (&nv)[2], int lane, State<D, NT> &st)
 {
     const int r = lane >> 2;
 #pragma unroll
@@ -800,7 +837,7 @@ __device__ __forceinline__ void move_reference(const float (&s)[2][NT][4], const
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
                     if (r + 8 * k < nv[h])
-                        mx = fmaxf(mx, logit(s[h][nt][2 * k + j], st.sl[nt][j]));
+                        mx = fmaxf(mx, x[h][nt][2 * k + j]);
 #pragma unroll
             for (int sh = 4; sh < 32; sh <<= 1)
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
@@ -830,16 +867,16 @@ __device__ __forceinline__ void move_reference(const float (&s)[2][NT][4], const
 // scales outside their windows are branches that whole pages rarely take.
 template <int D, int NT, bool SCORED>
 __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)[2], int lane, State<D, NT> &st,
-                                             float *logits, int logit_heads)
+                                             float scale_log2, float *logits, int logit_heads)
 {
     using R = Rec<D>;
     constexpr int kBlocks = D / 32;
     const int r = lane >> 2, c = lane & 3;
     const bool full = nv[0] == kPage && nv[1] == kPage;
-    float s[2][NT][4], t[2][NT][4];
+    float x[2][NT][4], t[2][NT][4];  // logits, and above the reference
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-        page_products<D, NT>(rec + h * R::kBytes, lane, st, s[h]);
+        page_products<D, NT, true>(rec + h * R::kBytes, lane, st, x[h], scale_log2);
     if constexpr (SCORED) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -847,15 +884,11 @@ __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)
             for (int nt = 0; nt < NT; ++nt) {
                 const int g = 8 * nt + 2 * c;
                 if (g < logit_heads) {
-                    float x[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[i] = logit(s[h][nt][i], st.sl[nt][i & 1]);
                     float *dst = logits + (h * kPage + r) * logit_heads + g;
                     if (r < nv[h])
-                        *reinterpret_cast<float2 *>(dst) = make_float2(x[0], x[1]);
+                        *reinterpret_cast<float2 *>(dst) = make_float2(x[h][nt][0], x[h][nt][1]);
                     if (r + 8 < nv[h])
-                        *reinterpret_cast<float2 *>(dst + 8 * logit_heads) = make_float2(x[2], x[3]);
+                        *reinterpret_cast<float2 *>(dst + 8 * logit_heads) = make_float2(x[h][nt][2], x[h][nt][3]);
                 }
             }
     }
@@ -881,14 +914,14 @@ __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    t[h][nt][i] = logit(s[h][nt][i], st.sl[nt][i & 1]) + st.nb[nt][i & 1];
+                    t[h][nt][i] = x[h][nt][i] + st.nb[nt][i & 1];
                     if (!full && r + (i < 2 ? 0 : 8) >= nv[h])
                         t[h][nt][i] = -INFINITY;
                     top = fmaxf(top, t[h][nt][i]);
                 }
         if (turn == 1 || !__any_sync(0xffffffffu, top > kPTop))
             break;
-        move_reference(s, nv, lane, st);
+        move_reference(x, nv, lane, st);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -938,7 +971,7 @@ __device__ __forceinline__ void attend_pages(const uint8_t *rec, const int (&nv)
 }
 
 // The same for two whole pages whose logits stay in reach of the reference
-// max and whose V scales lie in their windows, as nearly all do: no masks, no
+// max and whose products and V scales lie in theirs, as nearly all do: no masks, no
 // rescaling.  False, with the state unchanged, where they do not.  A path of
 // its own saves the predicated masks and lets the loads run further ahead:
 // 65.4 us against 70.4 us without it at 262144 tokens (one row, 32/8 heads, D = 128).
@@ -952,7 +985,7 @@ __device__ __forceinline__ bool attend_whole_pages(const uint8_t *rec, int lane,
     uint32_t out_of = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        page_products<D, NT>(rec + h * R::kBytes, lane, st, t[h]);
+        page_products<D, NT, false>(rec + h * R::kBytes, lane, st, t[h]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if constexpr (SCORED) {
@@ -973,14 +1006,14 @@ __device__ __forceinline__ bool attend_whole_pages(const uint8_t *rec, int lane,
                     t[h][nt][i] += st.nb[nt][i & 1];
                 else
                     t[h][nt][i] = fmaf(t[h][nt][i], 0.f, fmaf(t[h][nt][i], st.sl[nt][i & 1], st.nb[nt][i & 1]));
-                top = fmaxf(top, t[h][nt][i]);
+                top = max_or_nan(top, t[h][nt][i]);
             }
         }
         uint32_t vs[4];
         load_value_scales<D>(rec + h * R::kBytes, lane, vs);
         out_of |= (vs[0] - st.vlow) | (vs[1] - st.vlow) | (vs[2] - st.vlow) | (vs[3] - st.vlow);
     }
-    if (__any_sync(0xffffffffu, top > kPTop || (out_of & 0xf8f8f8f8u) != 0))
+    if (__any_sync(0xffffffffu, !(top <= kPTop) || (out_of & 0xf8f8f8f8u) != 0))
         return false;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -1239,7 +1272,7 @@ __global__ void __launch_bounds__(DCfg<D, NT>::kThreads, 1) mx4_decode_kernel(co
             const uint8_t *rec = ring + stage * C::kStageBytes;
             if (nv[0] < kPage || nv[1] < kPage || st.vlow == ~0u ||
                 !attend_whole_pages<D, NT, SCORED>(rec, lane, st, logits, heads))
-                attend_pages<D, NT, SCORED>(rec, nv, lane, st, logits, heads);
+                attend_pages<D, NT, SCORED>(rec, nv, lane, st, p.scale_log2, logits, heads);
             index += take;
             j += take;
             if ((j & 1) && j < n)
