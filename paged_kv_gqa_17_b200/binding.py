@@ -7,6 +7,7 @@ the library is missing or cannot be loaded, every call raises PkvError.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import json
 import os
@@ -603,6 +604,14 @@ def plan_decode(seq_lens_host, shape: Shape, device, rules=None, plan: Optional[
     return DecodePlan(shape, plan, items, indptr, n_items, ws, plan_counters(seq_lens_host, shape, plan))
 
 
+def _own_decode_plan(q, seq_lens, seq_lens_host, shape: Shape, rules, scores: bool, stream) -> DecodePlan:
+    """The plan of a decode that was given none.  All of it belongs to the call's stream: the lengths are read behind
+    what is queued there, and the workspace's memory is not reused before the call's kernels are done."""
+    with _on(q.get_device(), stream):
+        host = seq_lens_host if seq_lens_host is not None else seq_lens.detach().cpu()
+        return plan_decode(host, shape, q.device, rules, scores=scores)
+
+
 def paged_decode(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, block_table: torch.Tensor,
                  seq_lens: torch.Tensor, page_size: int, scale: float, *, plan: Optional[DecodePlan] = None,
                  seq_lens_host=None, layout: str = "HND", rules=None, out: Optional[torch.Tensor] = None,
@@ -613,14 +622,13 @@ def paged_decode(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, bl
     [pages][P][H_kv][D], any strides with a contiguous head_dim axis, see
     shape_of); block_table int32 [B][max_pages]; seq_lens int32 [B], all on one
     CUDA device.  Without `plan`, the policy and queue are built from
-    `seq_lens_host` (or a host copy of seq_lens).  Tensors of another dtype,
+    `seq_lens_host` (or a host copy of seq_lens, made in the order of the call's stream).  Tensors of another dtype,
     device or layout raise TypeError / ValueError before anything is launched.
     """
     L = lib()
     if plan is None:
         shape = shape_of(q, k_pool, block_table, layout, v_pool)
-        host = seq_lens_host if seq_lens_host is not None else seq_lens.detach().cpu()
-        plan = plan_decode(host, shape, q.device, rules)
+        plan = _own_decode_plan(q, seq_lens, seq_lens_host, shape, rules, False, stream)
     shape = plan.shape
     if out is None:
         out = torch.empty_like(q)
@@ -669,7 +677,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _on(index: int, stream):
     """Context in which a call's kernels and allocations belong to `stream` (default: the current stream of CUDA
-    device `index`), whatever device is current."""
+    device `index`), whatever device is current.  No device (index -1, a tensor that the checks refuse): none."""
+    if index < 0:
+        return contextlib.nullcontext()
     if stream is None:
         return torch.cuda.device(index)
     if stream.device.index != index:
@@ -763,9 +773,7 @@ def paged_decode_scored(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
     index = _cuda_index("q", q)
     if plan is None:
         shape = shape_of(q, k_pool, block_table, layout, v_pool)
-        host = seq_lens_host if seq_lens_host is not None else seq_lens.detach().cpu()
-        with _on(index, stream):
-            plan = plan_decode(host, shape, q.device, rules, scores=True)
+        plan = _own_decode_plan(q, seq_lens, seq_lens_host, shape, rules, True, stream)
     shape = plan.shape
     if not plan.plan.flags & FLAG_SCORES:
         raise ValueError("the plan was not made for scores: plan_decode(..., scores=True)")
