@@ -366,6 +366,15 @@ PKV_API int pkv_selftest_wait_timeout(void *workspace, size_t workspace_bytes, u
  * of range, 4 page id out of range, 8 malformed work item). */
 PKV_API int pkv_workspace_status(const void *workspace, void *stream, int32_t *device_error);
 
+/* For calls whose workspace nobody keeps (the binding's calls without a plan):
+ * pkv_collect_errors, queued on `stream` behind such a call, adds the
+ * workspace's device error word to one that the library holds per device;
+ * pkv_unplanned_status takes that one (it is zero afterwards) once the calls
+ * queued on `stream` before have run, and reports it as pkv_workspace_status
+ * does.  Collecting is asynchronous and capturable; neither call allocates. */
+PKV_API int pkv_collect_errors(const void *workspace, void *stream);
+PKV_API int pkv_unplanned_status(void *stream, int32_t *device_error);
+
 /* One decode step on the GPU.  All pointers but `shape`, `plan` are device
  * pointers:
  *   q            bf16 [B][H_q][D], contiguous

@@ -23,7 +23,7 @@ _LAZY = {
     "NO_SPLIT", "SPLIT_S", "WORK_QUEUE", "BALANCED", "FLAG_SEPARATE_MERGE", "FLAG_NO_PDL", "FLAG_DEEP_RING",
     "build_balanced_queue", "paged_decode_noalloc", "shape_of", "HostDecoder", "FLAG_CLUSTER_MERGE",
     "FLAG_PDL_EARLY", "FLAG_DEVICE_FILL", "FLAG_SHARED_PREFIX", "build_prefix_queue", "HostTiming", "HostCall", "host_replays",
-    "noalloc_status", "balanced_queue_capacity",
+    "noalloc_status", "unplanned_status", "balanced_queue_capacity",
     "paged_decode_scored", "plan_evict", "EvictPlan", "evict_tokens", "FLAG_SCORES",
     "mx4_pool", "mx4_planes", "mx4_shape", "plan_mx4", "Mx4Plan", "mx4_append", "mx4_read", "mx4_decode",
     "build_balanced_queue_device", "fill_queue_capacity", "build_fill_queue_device",

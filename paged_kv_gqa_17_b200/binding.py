@@ -122,6 +122,8 @@ SIGNATURES = [
     ("pkv_workspace_bytes", ctypes.c_int, [c_p, c_p, c_i32, c_p]),
     ("pkv_workspace_init", ctypes.c_int, [c_p, c_sz, c_p]),
     ("pkv_workspace_status", ctypes.c_int, [c_p, c_p, c_p]),
+    ("pkv_collect_errors", ctypes.c_int, [c_p, c_p]),
+    ("pkv_unplanned_status", ctypes.c_int, [c_p, c_p]),
     ("pkv_selftest_wait_timeout", ctypes.c_int, [c_p, c_sz, ctypes.c_uint32, c_p]),
     ("pkv_paged_decode", ctypes.c_int,
      [c_p, c_p, c_p, c_p, c_p, c_i32, ctypes.c_float, c_p, c_p, c_p, c_p, c_p, c_i32, c_p, c_sz, c_p]),
@@ -624,9 +626,12 @@ def paged_decode(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, bl
     CUDA device.  Without `plan`, the policy and queue are built from
     `seq_lens_host` (or a host copy of seq_lens, made in the order of the call's stream).  Tensors of another dtype,
     device or layout raise TypeError / ValueError before anything is launched.
+    Errors that the kernels meet on device data: workspace_status(plan), or
+    without a plan unplanned_status().
     """
     L = lib()
-    if plan is None:
+    own = plan is None
+    if own:
         shape = shape_of(q, k_pool, block_table, layout, v_pool)
         plan = _own_decode_plan(q, seq_lens, seq_lens_host, shape, rules, False, stream)
     shape = plan.shape
@@ -646,6 +651,8 @@ def paged_decode(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, bl
                             plan.indptr.data_ptr() if plan.indptr is not None else None, plan.n_items,
                             plan.workspace.data_ptr(), plan.workspace.numel(), _stream_ptr(stream))
     _check(rc, "pkv_paged_decode")
+    if own:
+        _collect(plan, q.get_device(), stream)
     return out
 
 
@@ -696,6 +703,11 @@ def _launch(fn, what: str, index: int, stream, *args):
             rc = fn(*args, _raw_stream(index))
     if rc != 0:
         raise PkvError(rc, what)
+
+
+def _collect(plan, index: int, stream):
+    """The device errors of a call that made its own plan, for unplanned_status()."""
+    _launch(lib().pkv_collect_errors, "pkv_collect_errors", index, stream, plan.workspace.data_ptr())
 
 
 def _empty(shape, dtype, index: int, stream) -> torch.Tensor:
@@ -771,7 +783,8 @@ def paged_decode_scored(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
     are left alone.  Everything else as paged_decode."""
     L = lib()
     index = _cuda_index("q", q)
-    if plan is None:
+    own = plan is None
+    if own:
         shape = shape_of(q, k_pool, block_table, layout, v_pool)
         plan = _own_decode_plan(q, seq_lens, seq_lens_host, shape, rules, True, stream)
     shape = plan.shape
@@ -793,6 +806,8 @@ def paged_decode_scored(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
             v_pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), page_size, scale, out.data_ptr(),
             scores.data_ptr(), st[0], st[1], ctypes.byref(shape), ctypes.byref(plan.plan), items, indptr, plan.n_items,
             ws.data_ptr(), ws.numel())
+    if own:
+        _collect(plan, index, stream)
     return out
 
 
@@ -840,7 +855,8 @@ def evict_tokens(scores: torch.Tensor, planes: Sequence[torch.Tensor], block_tab
     if not 0 <= recent <= budget or budget > INT32_MAX:
         raise ValueError(f"0 <= recent <= budget, got recent {recent}, budget {budget}")
     score_st = _check_scores("scores", scores, torch.float32, B, H_kv, max_pages, index)
-    if plan is None:
+    own = plan is None
+    if own:
         with _on(index, stream):
             plan = plan_evict(B, H_kv, max_pages, index)
     shape = plan.shape
@@ -886,6 +902,8 @@ def evict_tokens(scores: torch.Tensor, planes: Sequence[torch.Tensor], block_tab
     _launch(L.pkv_evict_tokens, "pkv_evict_tokens", index, stream, scores.data_ptr(), score_st[0], score_st[1], pos_ptr,
             pos_st[0], pos_st[1], arr, len(planes), block_table.data_ptr(), lens_ptr, budget, recent, out_ptr,
             ctypes.byref(shape), plan.workspace.data_ptr(), plan.workspace.numel())
+    if own:
+        _collect(plan, index, stream)
     return out
 
 
@@ -1016,10 +1034,11 @@ def mx4_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, block_table
 
     Token j belongs to the row i with indptr[i] <= j < indptr[i + 1] (int32 [B + 1] on the device; without it there
     is one token per row) and goes to position seq_lens[i] + j - indptr[i]; seq_lens are the lengths before the call
-    and stay unchanged.  Positions past a row's pages and bad page ids are skipped and reported
-    (workspace_status(plan))."""
+    and stay unchanged.  Positions past a row's pages and bad page ids are skipped and reported: by
+    workspace_status(plan), or without a plan by unplanned_status()."""
     L = lib()
-    if plan is None:
+    own = plan is None
+    if own:
         plan = _own_mx4_plan(pool, block_table, None, False, stream)
     shape = plan.shape
     index = _check_mx4(pool, block_table, seq_lens, shape)
@@ -1031,6 +1050,8 @@ def mx4_append(k: torch.Tensor, v: torch.Tensor, pool: torch.Tensor, block_table
     _launch(L.pkv_mx4_append, "pkv_mx4_append", index, stream, k.data_ptr(), v.data_ptr(), k_token, k_head, v_token,
             v_head, pool.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), ptr, n, ctypes.byref(shape),
             plan.workspace.data_ptr())
+    if own:
+        _collect(plan, index, stream)
 
 
 def mx4_read(pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, n_tokens: int, *,
@@ -1039,7 +1060,8 @@ def mx4_read(pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tens
     """The stored values, bf16 (k, v) [n_tokens][H_kv][D], of the tokens that mx4_append with the same seq_lens and
     indptr wrote.  Exact.  `out` = (k, v) is written in place; tokens that the append skips get zeros."""
     L = lib()
-    if plan is None:
+    own = plan is None
+    if own:
         plan = _own_mx4_plan(pool, block_table, None, False, stream)
     shape = plan.shape
     index = _check_mx4(pool, block_table, seq_lens, shape)
@@ -1060,6 +1082,8 @@ def mx4_read(pool: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tens
                 raise ValueError(f"out's {name} must be {list(dims)}, got {list(t.shape)}")
     _launch(L.pkv_mx4_read, "pkv_mx4_read", index, stream, pool.data_ptr(), block_table.data_ptr(),
             seq_lens.data_ptr(), ptr, n, k.data_ptr(), v.data_ptr(), ctypes.byref(shape), plan.workspace.data_ptr())
+    if own:
+        _collect(plan, index, stream)
     return k, v
 
 
@@ -1076,7 +1100,8 @@ def mx4_decode(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, s
         scores = None
     elif scores is not None and not isinstance(scores, torch.Tensor):
         raise TypeError(f"scores must be a tensor, None or False, got {type(scores).__name__}")
-    if plan is None:
+    own = plan is None
+    if own:
         plan = _own_mx4_plan(pool, block_table, int(q.shape[1]), scores is not None, stream)
     shape = plan.shape
     index = _check_mx4(pool, block_table, seq_lens, shape)
@@ -1100,7 +1125,22 @@ def mx4_decode(q: torch.Tensor, pool: torch.Tensor, block_table: torch.Tensor, s
     _launch(L.pkv_mx4_decode, "pkv_mx4_decode", index, stream, q.data_ptr(), pool.data_ptr(), block_table.data_ptr(),
             seq_lens.data_ptr(), page_size, scale, out.data_ptr(), score_ptr, st[0], st[1], ctypes.byref(shape),
             ctypes.byref(plan.plan), ws.data_ptr(), ws.numel())
+    if own:
+        _collect(plan, index, stream)
     return out
+
+
+def unplanned_status(stream=None) -> int:
+    """Synchronize and return the raw device error mask (0 = clean) of the calls without a plan on `stream`'s device
+    (default: the current stream), of which only those queued on that stream are sure to be in; it is zero afterwards.
+    Calls with a plan have theirs: workspace_status(plan)."""
+    err = c_i32(0)
+    index = torch.cuda.current_device() if stream is None else stream.device.index
+    with _on(index, stream):
+        rc = lib().pkv_unplanned_status(_raw_stream(index), ctypes.byref(err))
+    if rc not in (0, -5, -6):
+        _check(rc, "pkv_unplanned_status")
+    return int(err.value)
 
 
 def noalloc_status(stream=None) -> int:

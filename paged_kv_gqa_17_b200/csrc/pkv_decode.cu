@@ -3310,6 +3310,40 @@ int pkv_workspace_status(const void *workspace, void *stream, int32_t *device_er
     return status_from_error_word(w);
 }
 
+// What calls whose workspaces nobody reads have met (pkv_collect_errors), until pkv_unplanned_status takes it.
+static __device__ uint32_t g_unplanned_error, g_unplanned_taken;
+
+static __global__ void collect_errors_kernel(const uint32_t *word)
+{
+    if (const uint32_t e = *word)
+        atomicOr(&g_unplanned_error, e);
+}
+
+static __global__ void take_errors_kernel() { g_unplanned_taken = atomicExch(&g_unplanned_error, 0u); }
+
+int pkv_collect_errors(const void *workspace, void *stream)
+{
+    if (!workspace || !aligned(workspace, 4))
+        return workspace ? PKV_ERR_UNSUPPORTED : PKV_ERR_INVALID;
+    collect_errors_kernel<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<const uint32_t *>(workspace));
+    return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+int pkv_unplanned_status(void *stream, int32_t *device_error)
+{
+    static std::mutex mu;  // g_unplanned_taken serves one caller at a time
+    std::lock_guard<std::mutex> lock(mu);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint32_t w = 0;
+    take_errors_kernel<<<1, 1, 0, st>>>();
+    if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess ||
+        cudaMemcpyFromSymbol(&w, g_unplanned_taken, sizeof w) != cudaSuccess)
+        return PKV_ERR_CUDA;
+    if (device_error)
+        *device_error = (int32_t)w;
+    return status_from_error_word(w);
+}
+
 namespace {
 
 // ---------------------------------------------------------------------------
