@@ -30,13 +30,19 @@
 //   4. The recent tokens' first batch is loaded beside the selection; after a
 //      cluster barrier (every mover read, every batch loaded) it is stored.
 //      Longer windows repeat load, barrier, store.
-// Up to kLocalKeys tokens the cluster's first block selects alone and the others
-// read its lists through distributed shared memory: a few thousand keys cost
-// less than the cluster barriers that sharing them takes (64 rows and heads of
-// 2064 tokens: 12.7 us against 24.4 us shared; at 9008 tokens the two meet, 24.4
-// and 23.5 us).  Above, the blocks own contiguous shares of [0, M), add their
-// counts through distributed shared memory, each block the values of its
-// slice, and hand the two lists over through the workspace.
+// Where the block table has room for few tokens (kLocalKeys; the lengths are on
+// the device) the cluster's first block selects alone and the others read its
+// lists through distributed shared memory: a few thousand keys cost less than
+// the cluster barriers that sharing them takes.  Above, the blocks own contiguous
+// shares of [0, M), add their counts through distributed shared memory, each
+// block the values of its slice, and hand the two lists over through the
+// workspace.  Alone against shared, us on fresh scores with a cold L2, one page
+// over the budget: 64 pairs (clusters of four) 22.5 / 26.6 at 2064 tokens, 28.6 /
+// 28.7 at 5120, 34.8 / 30.7 at 8192, 84 / 35 at 16384; 8 pairs (of eight) 20.5 /
+// 26.6, 24.6 / 26.6, 30.7 / 26.6, 45 / 31.  A block without peers has no barrier to
+// save, only lists that are nearer (kAloneKeys): 152 pairs 28.7 / 36.9 at 2064, 53 /
+// 68 at 14336, but 96 / 74 at 16384, where the keys and lists of two blocks no
+// longer fit an SM.
 // Every write has one writer, so results are deterministic.
 //
 // What bounds it: one page over the budget, latency (12.7 us for 10 MB that could
@@ -56,7 +62,8 @@ namespace {
 constexpr int kEvictThreads = 256;
 constexpr int kEvictPerSM = 2;       // blocks an SM holds
 constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kLocalKeys = 16384;   // capacity up to which one block selects for its cluster
+constexpr int kLocalKeys = 6144;    // capacity up to which one block selects for its cluster
+constexpr int kAloneKeys = 14336;   // ... for itself where it has no peers; two blocks still fit an SM
 constexpr int kMaxKeys = 16384;     // shared selection: keys a block holds (the rest is read again)
 constexpr int kMaxTable = 2048;     // block-table entries a block holds
 constexpr int kMaxCluster = 8;
@@ -653,7 +660,7 @@ cudaError_t launch_evict(const EvictParams &p, int64_t pairs, cudaStream_t st)
 {
     static std::atomic<uint64_t> configured{0};
     auto kernel = evict_kernel<CS, LOCAL>;
-    const cudaError_t e = allow_smem(kernel, (kMaxKeys + kMaxTable) * 4 + kLocalKeys * 2, configured);
+    const cudaError_t e = allow_smem(kernel, (kMaxKeys + kMaxTable) * 4 + kAloneKeys * 2, configured);
     if (e != cudaSuccess)
         return e;
     const size_t smem = (size_t)(p.held_keys + p.held_table) * 4 + (LOCAL ? (size_t)p.capacity * 2 : 0);
@@ -778,7 +785,7 @@ int pkv_evict_tokens(float *scores, int64_t score_stride_row, int64_t score_stri
     int cluster = 1;
     while (cluster < kMaxCluster && pairs * cluster * 2 <= 148 * kEvictPerSM && capacity / (cluster * 2) >= 256)
         cluster *= 2;
-    const bool local = capacity <= kLocalKeys;
+    const bool local = capacity <= (cluster > 1 ? kLocalKeys : kAloneKeys);
     p.held_keys = (int32_t)(local ? capacity : std::min<int64_t>(ceil_div(capacity, cluster), kMaxKeys));
     p.held_keys = (p.held_keys + 3) & ~3;
     p.held_table = std::min(s.max_pages_per_seq, kMaxTable);
