@@ -460,7 +460,10 @@ PKV_API int pkv_evict_workspace_bytes(const pkv_shape *shape, size_t *bytes);
  *   scores     device float, as in pkv_paged_decode_scored
  *   positions  NULL, or device int32 laid out alike under its own strides
  *   planes     the pool's arrays (K and V of a bf16 pool; the four parts of a
- *              4-bit pool); host array of n_planes <= PKV_EVICT_MAX_PLANES
+ *              4-bit pool); host array of n_planes <= PKV_EVICT_MAX_PLANES.  No two
+ *              may share memory, which would be moved twice at once: rows of one
+ *              slot that overlap, and positions given as the scores, are refused
+ *              (PKV_ERR_INVALID)
  *   seq_lens   device int32 [B], the lengths before the call
  *   new_lens   device int32 [B], receives min(N_i, budget); not the same
  *              array as seq_lens

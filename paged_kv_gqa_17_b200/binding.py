@@ -842,7 +842,8 @@ def evict_tokens(scores: torch.Tensor, planes: Sequence[torch.Tensor], block_tab
     with their tokens; vacated slots' scores become 0.  Rows within the budget stay as they are.
 
     planes: the paged arrays to compact, [pages][H_kv][16][X] (layout "HND") or [pages][16][H_kv][X] ("NHD"), any
-    dtype, any strides with a contiguous last axis: (k_pool, v_pool), or mx4_planes(pool).  Pages that rows share
+    dtype, any strides with a contiguous last axis: (k_pool, v_pool), or mx4_planes(pool).  No two may share memory,
+    nor may scores and positions.  Pages that rows share
     must be copied first: the call moves tokens within every row's pages.  `seq_lens` is not changed."""
     L = lib()
     index = _cuda_index("scores", scores)
@@ -867,6 +868,8 @@ def evict_tokens(scores: torch.Tensor, planes: Sequence[torch.Tensor], block_tab
     if positions is not None:
         pos_st = _check_scores("positions", positions, torch.int32, B, H_kv, max_pages, index)
         pos_ptr = positions.data_ptr()
+        if pos_ptr == scores.data_ptr() and pos_ptr:
+            raise ValueError("scores and positions share memory")
     _check_tensor("block_table", block_table, torch.int32, index)
     _check_tensor("seq_lens", seq_lens, torch.int32, index)
     if out is None:
@@ -881,6 +884,7 @@ def evict_tokens(scores: torch.Tensor, planes: Sequence[torch.Tensor], block_tab
     pages = planes[0].shape[0]
     head_axis, token_axis = (1, 2) if layout == "HND" else (2, 1)
     arr = (Plane * len(planes))()
+    rows = []  # the first rows' addresses
     for i, t in enumerate(planes):
         dims, st = t.shape, t.stride()
         if t.get_device() != index:
@@ -894,9 +898,13 @@ def evict_tokens(scores: torch.Tensor, planes: Sequence[torch.Tensor], block_tab
             _check_no_overlap(f"plane {i}", dims, st)
         size = t.element_size()
         p = arr[i]
-        p.base = t.data_ptr()
+        p.base = base = t.data_ptr()
         p.stride_page, p.stride_head, p.stride_token = st[0] * size, st[head_axis] * size, st[token_axis] * size
-        p.row_bytes = dims[3] * size
+        p.row_bytes = row_bytes = dims[3] * size
+        for j, (begin, end) in enumerate(rows):
+            if begin < base + row_bytes and base < end and base:
+                raise ValueError(f"planes {j} and {i} share memory")
+        rows.append((base, base + row_bytes))
     shape = Shape.from_buffer_copy(shape)  # the plan may serve several calls at once
     shape.num_pool_pages = pages
     _launch(L.pkv_evict_tokens, "pkv_evict_tokens", index, stream, scores.data_ptr(), score_st[0], score_st[1], pos_ptr,

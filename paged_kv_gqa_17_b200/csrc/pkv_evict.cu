@@ -754,7 +754,15 @@ int pkv_evict_tokens(float *scores, int64_t score_stride_row, int64_t score_stri
             return PKV_ERR_INVALID;
         if (pl.row_bytes > PKV_EVICT_MAX_ROW_BYTES)
             return PKV_ERR_UNSUPPORTED;
+        // two planes over one array would move its rows twice at once
+        for (int j = 0; j < i; ++j) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(planes[j].base), b = reinterpret_cast<uintptr_t>(pl.base);
+            if (a < b + (uintptr_t)pl.row_bytes && b < a + (uintptr_t)planes[j].row_bytes)
+                return PKV_ERR_INVALID;
+        }
     }
+    if (positions && static_cast<const void *>(positions) == static_cast<const void *>(scores))
+        return PKV_ERR_INVALID;
     for (int wide = 1; wide >= 0; --wide) {  // planes of 16-byte units first
         for (int i = 0; i < n_planes; ++i) {
             const pkv_plane &pl = planes[i];

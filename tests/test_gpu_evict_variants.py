@@ -59,3 +59,23 @@ def test_rows_that_fill_a_variants_last_slot(n, kind):
 
 def test_rows_above_and_below_the_budget_side_by_side():
     Case([7000, 10, 6999, 500], 3, (64,), seed=2).run(501, 77)
+
+
+def test_planes_that_share_memory_are_refused():
+    c = Case([100, 40], 2, (16, 32))
+    scores, positions, planes, table, lens = c.device()
+
+    def call(p, **kw):
+        return bd.evict_tokens(scores, p, table, lens, 20, 4, **kw)
+
+    for p in ([planes[0], planes[0]], [planes[0], planes[1], planes[0].view(torch.int32)],
+              [planes[1][..., :20], planes[1][..., 19:]]):
+        with pytest.raises(ValueError):
+            call(p)
+    with pytest.raises(ValueError):
+        call(planes, positions=scores.view(torch.int32))
+    # halves of one array share none, whichever comes first
+    want = c.want(20, 4)
+    call([planes[1][..., 16:], planes[0], planes[1][..., :16]])
+    for p, w in zip(planes, want[2]):
+        assert (p.cpu().numpy() == w).all()
