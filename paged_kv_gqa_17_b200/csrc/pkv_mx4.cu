@@ -378,7 +378,11 @@ __global__ void __launch_bounds__(kTokenThreads) mx4_read_kernel(const __grid_co
 //     two on packed halves.  Halves cover 2^-24 .. 2^15, so a block's scales are
 //     taken relative to a reference exponent; pages whose scales leave the
 //     eight steps below it take the same product in bf16, whose exponents
-//     reach everywhere.
+//     reach everywhere.  Two roundings to halves: 2^-11 of a token's weight, or,
+//     for tokens that are 2^-(15 + d) or less of the heaviest (d steps up the window),
+//     2^-32 of the heaviest's weight times 6 2^(the window's top - 127).  bf16 would
+//     keep their leading bits and cost every other token three of its own; such
+//     tokens make up an output only where the heavy ones' values are next to nothing.
 // Bound by instruction issue before memory: 263 instructions and 437 cycles
 // per page and scheduler, 147 of them on the logic pipe at two cycles each (64 are
 // the conversions from e2m1, two values at a time).  One row of 32/8

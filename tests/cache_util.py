@@ -7,7 +7,9 @@ and once in the denominator, beside a few units of 2^-22 for exp2 and the divisi
 An output sum_t w v adds the rounding of the weights to the product's type and of the result to bf16, each half a
 step, finfo.eps / 2 (`p_step`: bf16, whose steps are 2^-7 of a value, 2^-8; f16, whose steps are 2^-10, 2^-11):
 (dw + p_step) sum_t w |v| + 2^-8 |out|.  The 4-bit decode multiplies in f16 while V's scales stay within eight powers
-of two, and in bf16 where they do not, blocks of zeros (scale byte 0) among them.
+of two, and in bf16 where they do not, blocks of zeros (scale byte 0) among them.  Halves below 2^-14 have fewer bits:
+that adds n 2^-32 6 2^(window's top - 127) to an output's error (test_gpu_mx4_light_tokens.py derives it), which these
+tolerances leave out: rows whose heavy tokens have ordinary values stay far below it.
 """
 import numpy as np
 import torch
