@@ -289,14 +289,15 @@ def _attend(s, k, v):
 
 def _run_evict(s):
     mx4 = s["cache"] == "mx4"
+    planes = _planes(s["pool"], s["head_dim"]) if mx4 else [s["k"], s["v"]]
     if own:
         from paged_kv_gqa_17_b200 import binding as pkv
 
-        planes = pkv.mx4_planes(s["pool"]) if mx4 else (s["k"], s["v"])
+        if mx4:
+            planes = pkv.mx4_planes(s["pool"])
         lens = pkv.evict_tokens(s["scores"], planes, s["table"], s["lens"], s["budget"], s["recent"],
                                 positions=s["positions"], plan=s["plan"])
         return lens, s["scores"], s["positions"], (s["pool"] if mx4 else (s["k"], s["v"]))
-    planes = _planes(s["pool"], s["head_dim"]) if mx4 else [s["k"], s["v"]]
     source, lens = _evicted(s["scores"], s["lens"], s["budget"], s["recent"])
     slot = torch.arange(source.shape[-1], device="cuda")
     gone = (slot >= lens[:, None, None]) & (slot < s["lens"][:, None, None])
