@@ -257,7 +257,7 @@ def _run_mx4(s):
         from paged_kv_gqa_17_b200 import binding as pkv
 
         out = pkv.mx4_decode(s["q"], s["pool"], s["table"], s["lens"], PAGE, s["scale"], plan=s["plan"],
-                             scores=s["scores"] if s["scores"] is not False else None)
+                             scores=s.get("scores"))
         return (out, s["scores"]) if s["scores"] is not False else (out,)
     kc, vc, ks, vs = (_rows(p, s["table"]) for p in _planes(s["pool"], s["head_dim"]))
     out = _attend(s, _values(_unpack(kc, False), ks.int()), _values(_unpack(vc, True), vs.int()))
