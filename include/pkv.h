@@ -465,8 +465,8 @@ PKV_API int pkv_evict_workspace_bytes(const pkv_shape *shape, size_t *bytes);
  *              slot that overlap, and positions given as the scores, are refused
  *              (PKV_ERR_INVALID)
  *   seq_lens   device int32 [B], the lengths before the call
- *   new_lens   device int32 [B], receives min(N_i, budget); not the same
- *              array as seq_lens
+ *   new_lens   device int32 [B], receives min(N_i, budget); shares no memory
+ *              with seq_lens (PKV_ERR_INVALID)
  *   shape      B, H_kv, page_size (16), max_pages_per_seq, num_pool_pages are used
  *   workspace  >= pkv_evict_workspace_bytes(), zeroed once
  * A page that two of the rows (or two places of one row) share is moved for

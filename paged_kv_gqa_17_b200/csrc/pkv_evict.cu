@@ -721,7 +721,11 @@ int pkv_evict_tokens(float *scores, int64_t score_stride_row, int64_t score_stri
     if (s.B == 0)
         return PKV_OK;
     if (!scores || !seq_lens || !new_lens || !workspace || !block_table || s.max_pages_per_seq < 1 ||
-        s.num_pool_pages < 1 || seq_lens == new_lens)
+        s.num_pool_pages < 1)
+        return PKV_ERR_INVALID;
+    // the heads of a row read its length while its first one writes the new one
+    const uintptr_t before = reinterpret_cast<uintptr_t>(seq_lens), after = reinterpret_cast<uintptr_t>(new_lens);
+    if (before < after + 4 * (uintptr_t)s.B && after < before + 4 * (uintptr_t)s.B)
         return PKV_ERR_INVALID;
     if (!aligned(scores, 4) || (positions && !aligned(positions, 4)) || !aligned(block_table, 4) ||
         !aligned(seq_lens, 4) || !aligned(new_lens, 4) || !aligned(workspace, 256))
