@@ -414,11 +414,15 @@ PKV_API int pkv_paged_decode(const void *q, const void *k_pool, const void *v_po
  * included); the workspace is sized by pkv_workspace_bytes for that plan and holds the logits
  * between the decode kernel and the weights kernel that follows it on `stream`.  A token whose
  * row attends to nothing (every logit -inf) gets no weight.  Tokens that the call did not attend
- * to keep their scores: those of a (row, KV head) one of whose work items was refused, and those
- * past the end of a plan that was made for a shorter row, which is reported as a malformed work
- * item in every mode (SPLIT_S reports it without scores too).  Nothing is added on a workspace
- * that has recorded a timeout (pkv_workspace_init clears it).  Deterministic.  Other arguments,
- * layouts, errors and return codes as pkv_paged_decode. */
+ * to keep their scores: those of a (row, KV head) one of whose work items was refused or whose
+ * items leave a gap, and those past the end of a plan that was made for a shorter row (both
+ * reported as a malformed work item; SPLIT_S reports the latter without scores too).  Nothing is
+ * added on a workspace that has recorded a timeout (pkv_workspace_init clears it).
+ * The logits take B * H_kv * max_pages_per_seq * P * G * 4 bytes of the workspace (G rounded up
+ * to a power of two, 2 at least), and the weights kernel's grid is that of the whole table, so a
+ * table far wider than its rows costs memory and empty blocks: 64 rows of 8 KV heads at G = 4
+ * under a table for 131072 tokens take 1 GB.  The same holds for pkv_mx4_decode with scores.
+ * Deterministic.  Other arguments, layouts, errors and return codes as pkv_paged_decode. */
 PKV_API int pkv_paged_decode_scored(const void *q, const void *k_pool, const void *v_pool,
                                     const int32_t *block_table, const int32_t *seq_lens,
                                     int32_t page_size, float scale, void *out, float *scores,
@@ -475,7 +479,9 @@ PKV_API int pkv_evict_workspace_bytes(const pkv_shape *shape, size_t *bytes);
  * from it leave the planes alone (scores and positions move all the same);
  * so is a length out of range, whose row is left alone
  * (new_lens gets it clamped).  One kernel, asynchronous on `stream`,
- * capturable, deterministic. */
+ * capturable, deterministic; its variant goes by max_pages_per_seq, the
+ * lengths being on the device: a table not much wider than the rows is faster.
+ * Calls that may run at the same time need workspaces of their own. */
 PKV_API int pkv_evict_tokens(float *scores, int64_t score_stride_row, int64_t score_stride_head,
                              int32_t *positions, int64_t position_stride_row,
                              int64_t position_stride_head, const pkv_plane *planes, int32_t n_planes,
@@ -485,8 +491,8 @@ PKV_API int pkv_evict_tokens(float *scores, int64_t score_stride_row, int64_t sc
 
 /* The 4-bit paged cache.  A value is an e2m1 code, (-1)^s {0, .5, 1, 1.5, 2,
  * 3, 4, 6}[low three bits], times 2^(scale - 127) with one scale byte per 32
- * dims of a token (255: NaN; 0: all the block's values are taken as 0 by the
- * decode).  A page (16 tokens) of one KV head is one record of 17 * D bytes:
+ * dims of a token (255: NaN; 0: codes of zeros, other codes under it are not
+ * of this format).  A page (16 tokens) of one KV head is one record of 17 * D bytes:
  *     K codes [16][D/2], V codes [16][D/2], K scales [16][D/32], V scales [16][D/32]
  * with dim 32 b + 8 c + j (j < 8, c < 4) of a K row in byte c D/8 + 4 b + j/2 and dim
  * 32 b + 4 r + j (j < 4, r < 8) of a V row in byte r D/16 + 2 b + j/2, in the low four bits
@@ -532,8 +538,10 @@ PKV_API int pkv_mx4_workspace_bytes(const pkv_shape *shape, const pkv_plan *plan
  * PKV_FLAG_SCORES) pkv_paged_decode_scored.  Every block derives its share of
  * the pages from the device lengths, so one plan, or one captured graph,
  * serves any lengths up to max_pages_per_seq * P.  q bf16 [B][H_q][D], out likewise; 1
- * <= G <= 16, B <= 4096, B * H_kv * max_pages_per_seq < 2^31.  Zeros for rows without tokens;
- * errors on device data as in pkv_paged_decode.  Deterministic. */
+ * <= G <= 16, B <= 4096, B * H_kv * max_pages_per_seq < 2^31.  Zeros for rows without tokens
+ * and for heads whose logits are all -inf; errors on device data as in pkv_paged_decode.
+ * Calls that may run at the same time need workspaces of their own.  Deterministic.
+ * Queries are held to multiples of 2^-38 of their head's largest element. */
 PKV_API int pkv_mx4_decode(const void *q, const void *pool, const int32_t *block_table,
                            const int32_t *seq_lens, int32_t page_size, float scale, void *out,
                            float *scores, int64_t score_stride_row, int64_t score_stride_head,

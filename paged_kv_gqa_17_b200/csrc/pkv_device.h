@@ -405,7 +405,7 @@ constexpr int kWeightTokens = 1024;
 inline int64_t weight_blocks(int64_t pairs, int64_t capacity) { return pairs * ceil_div(capacity, kWeightTokens); }
 
 // The tokens of a pair, from 0, whose logits this call's bf16 decode wrote, for the whole
-// warp: the row's, or fewer where the plan covers fewer, or -1 where some item was refused.
+// warp: the row's, fewer where the plan covers fewer, 0 where an item was refused or leaves a gap.
 __device__ __forceinline__ int attended_end(const WeightParams &p, int pair, const SlotRange &range, int lane)
 {
     bool ok = true;
@@ -424,7 +424,7 @@ __device__ __forceinline__ int attended_end(const WeightParams &p, int pair, con
              (k >= range.count || r.w == (lane == 0 ? end : above));  // the tokens follow one another without a gap
         end = __shfl_sync(0xffffffffu, te, min(31, range.count - 1 - k0));
     }
-    return __all_sync(0xffffffffu, ok) ? end : -1;
+    return __all_sync(0xffffffffu, ok) ? end : 0;
 }
 
 // One block's part of the weights kernel, after the kernel before it has
@@ -469,15 +469,19 @@ __device__ __forceinline__ void add_weights(const WeightParams &p, int pair, int
             }
         }
     }
-    if (range.first < 0 || range.count < 1 || range.first >= p.n_slots || range.slot(range.count - 1) >= p.n_slots)
-        return;  // none, or an earlier call's
+    if (range.first < 0 || range.count < 1 || range.first >= p.n_slots || range.slot(range.count - 1) >= p.n_slots) {
+        // none, or an earlier call's
+        if (RECORDS && chunk == 0 && threadIdx.x == 0)
+            atomicOr(p.ws_error, kErrItem);
+        return;
+    }
     if (error & kErrTimeout)
         return;  // some page never came: states and logits may be missing
     if (RECORDS && warp == kWeightThreads / 32 - 1) {
         const int end = attended_end(p, pair, range, lane);
         if (lane == 0) {
-            *s_end = end < 0 ? 0 : end;
-            if (chunk == 0 && end >= 0 && end < n)
+            *s_end = end;
+            if (chunk == 0 && end < n)
                 atomicOr(p.ws_error, kErrItem);  // the plan does not cover this row
         }
     }

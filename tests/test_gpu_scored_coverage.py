@@ -164,3 +164,22 @@ def test_nothing_is_added_on_a_workspace_that_timed_out_4_bits():
         else:
             assert bd.workspace_status(plan) == 1
             assert (scores.cpu().numpy() == c.before).all()
+
+
+def test_queues_with_gaps_and_missing_pairs_are_reported():
+    c = Case([100, 30], 2, 4, 64)
+    plan = bd.plan_decode(c.lens, c.shape(), "cuda", rules=rule(2, 1, 2), scores=True)
+    assert plan.indptr.tolist() == [0, 4, 8, 9, 10]
+    _, scores, _ = decode(c, plan)
+    item = plan.items[2].clone()
+    plan.items[2, 2] += 16  # its first page belongs to no item now
+    _, now, error = decode(c, plan)
+    assert error == ITEM and untouched(c, now, 0, 0)
+    for i, h in ((0, 1), (1, 0), (1, 1)):
+        assert torch.equal(now[i, h], scores[i, h])
+    # a queue that ends before the last pair, on a workspace that has seen no other
+    plan = bd.plan_decode(c.lens, c.shape(), "cuda", rules=rule(2, 1, 2), scores=True)
+    assert plan.items[2].equal(item)
+    plan.indptr[4] = 9
+    _, now, error = decode(c, plan)
+    assert error == ITEM and untouched(c, now, 1, 1) and torch.equal(now[0], scores[0])
