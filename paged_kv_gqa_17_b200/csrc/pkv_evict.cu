@@ -48,7 +48,7 @@
 // What bounds it: one page over the budget, latency (12.7 us for 10 MB that could
 // pass in 1.6 us: a dependent chain of loads of scores, three digits, lists,
 // page ids and rows); whole prompts, memory (32 rows and heads of 16384 to 32768
-// fresh tokens to 8192, with nothing in L2: 82 us, 4.2 TB/s while the rows move).
+// fresh tokens to 8192, with nothing in L2: 81 us, 4.2 TB/s while the rows move).
 #include "pkv_device.h"
 
 #include <algorithm>

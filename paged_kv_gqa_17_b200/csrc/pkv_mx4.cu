@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kTokenThreads) mx4_read_kernel(const __grid_co
 //     2^-32 of the heaviest's weight times 6 2^(the window's top - 127).  bf16 would
 //     keep their leading bits and cost every other token three of its own; such
 //     tokens make up an output only where the heavy ones' values are next to nothing.
-// Bound by instruction issue before memory: 263 instructions and 437 cycles
+// Bound by instruction issue before memory: 263 instructions and 446 cycles
 // per page and scheduler, 147 of them on the logic pipe at two cycles each (64 are
 // the conversions from e2m1, two values at a time).  One row of 32/8
 // heads, D = 128: 262144 tokens 65.4 us (4.36 TB/s of 4-bit pages, 67 % of the copy

@@ -18,8 +18,8 @@
 // so results are deterministic.
 //
 // Bound by the launch and one chain of loads (lengths and slots, then logits,
-// scores and the slots' maxima at once): 6.2 us more than the decode alone at
-// one row of 32768 tokens (28.7 against 22.5 us; 1 MB of scores and 4 MB of
+// scores and the slots' maxima at once): 6.4 us more than the decode alone at
+// one row of 32768 tokens (28.9 against 22.5 us; 1 MB of scores and 4 MB of
 // logits), 4 us of 52 us at eight rows of 533 to 16381 tokens.
 #include "pkv_device.h"
 
